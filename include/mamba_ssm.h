@@ -6,8 +6,11 @@
  *   mamba_selective_scan_fwd      the selective scan over a whole sequence
  *   mamba_selective_state_update  one token of generation (recurrent mode)
  *
- * and, next to them, the block's short causal convolution (prefill and decode
- * update) that produces the scan's input.
+ * and, next to them, the rest of a recurrent block around its projections: the
+ * short causal convolution (prefill, decode update, backward) that produces
+ * the scan's input, the gated linear recurrence (forward, backward, one token),
+ * the layer norm with the residual add (forward, backward) and the Mamba-2
+ * layer.
  *
  * Definition (per batch b, channel d, state index n, time t):
  *
@@ -40,7 +43,8 @@
  *    the dims struct is a HOST pointer.  The library keeps no per-call state
  *    and performs no device allocation.  Work is enqueued on `stream`
  *    (asynchronous); pass 0 for the legacy default stream.
- *  - All tensors are dense, row-major, contiguous, without padding.
+ *  - All tensors are dense, row-major, contiguous, without padding, except where
+ *    an entry point takes strides (gated recurrence, layer norm).
  *  - Floating-point arithmetic is fp32; the state is fp32.  u/delta/z/out
  *    (x/dt/z/out) and B/C may each be fp32 or bf16 (see mamba_dtype_t).
  *    A, D and the delta/dt bias are fp32.
@@ -486,6 +490,209 @@ MAMBA_API mamba_status_t mamba_causal_conv1d_update(void *conv_state, const void
                                                     int width, int silu, void *out,
                                                     const mamba_dims_t *dims,
                                                     cudaStream_t stream);
+
+/*
+ * Backward pass of the short causal convolution (training).
+ *
+ * Gradients of a scalar loss through mamba_causal_conv1d_fwd, given dout =
+ * dLoss/dout and optionally dfinal_conv_state = dLoss/dfinal_conv_state.  With
+ * pre_t = bias_d + sum_k weight_d,k x_{t-W+1+k} (recomputed) and dpre_t = dout_t
+ * act'(pre_t):
+ *   dx_s = sum_k weight_d,k dpre_{s+W-1-k},  plus dfinal_conv_state at the last W inputs
+ *   dweight_d,k = sum_{b,t} dpre_t x_{t-W+1+k},   dbias_d = sum_{b,t} dpre_t
+ * and dinitial_conv_state is the sum of dx at times -W .. -1.
+ *   x, dout, dx                       (batch, dim, seqlen), io_dtype; dx must not alias an input
+ *   weight, dweight                   (dim, width) fp32;  bias, dbias (dim,) fp32
+ *   initial_conv_state, dfinal_conv_state, dinitial_conv_state
+ *                                     (batch, dim, width), io_dtype
+ * bias, initial_conv_state and dfinal_conv_state may be NULL as in the forward;
+ * dbias and dinitial_conv_state may be NULL (not computed).
+ * dims->workspace: at least mamba_causal_conv1d_bwd_workspace_bytes(dims, width)
+ * bytes, 256-byte aligned, not shared by calls that overlap on the GPU.  The
+ * sums are added in a fixed order: results repeat bit for bit.
+ */
+MAMBA_API size_t mamba_causal_conv1d_bwd_workspace_bytes(const mamba_dims_t *dims, int width);
+
+MAMBA_API mamba_status_t mamba_causal_conv1d_bwd(
+    const void *x, const float *weight, const float *bias, const void *initial_conv_state,
+    int width, int silu, const void *dout, const void *dfinal_conv_state, void *dx,
+    float *dweight, float *dbias, void *dinitial_conv_state, const mamba_dims_t *dims,
+    cudaStream_t stream);
+
+/*
+ * Gated linear recurrence.
+ *
+ * "Mamba 与状态空间模型", section 由词元决定 (Theorem 1): with a one-number state
+ * the selective scan is the gate h <- (1 - g) h + g x.  Per batch row b and
+ * channel d, with f_t = gate_t + gate_bias_d:
+ *
+ *   log_decay == 0:  h_t = (1 - g_t) h_{t-1} + g_t x_t,   g_t = sigmoid(f_t)
+ *   log_decay != 0:  h_t = exp(f_t) h_{t-1} + x_t          (f_t <= 0; -infinity resets)
+ *   out_t = h_t,   h_{-1} = initial_state or 0
+ *
+ * Unlike mamba_selective_scan_fwd there are no B, C, D and Delta: the state is
+ * the output, and the decay is given per step and channel.
+ *
+ * Layouts: gate, x, out (and dout, dgate, dx) are (batch, dim, seqlen), or
+ * (batch, seqlen, dim) with MAMBA_FLAG_LAYOUT_BLD.  The last dimension is
+ * contiguous; the distances between rows are given per tensor in elements
+ * (mamba_strides_t), so that gate and x may be halves of one projection's
+ * output.  A pair of zeros stands for a packed tensor.  Distances below the
+ * row length (broadcast tensors), and outputs whose rows overlap, return
+ * MAMBA_ERR_INVALID_ARG.  States are packed fp32.
+ *
+ * Padded batches: seqlens (device, (batch,) int32, or NULL) gives each batch
+ * row's number of steps, clamped to 0 .. seqlen.  Later steps of gate, x and
+ * dout are not used, whatever they hold (NaN included); out, dgate and dx are
+ * written as 0 there; last_state is the state after the row's own last step.
+ *
+ * Arithmetic and states are fp32.  In the log-decay form a product of decays
+ * over many steps must stay finite in fp32, which f_t <= 0 guarantees.
+ */
+typedef struct {
+    int64_t batch;   /* elements between batch rows */
+    int64_t row;     /* elements between time steps (MAMBA_FLAG_LAYOUT_BLD) or channels */
+} mamba_strides_t;
+
+typedef struct {
+    int64_t batch, dim, seqlen;
+    int32_t io_dtype;          /* gate, x, out, dout, dgate, dx */
+    int32_t log_decay;
+    int32_t flags;             /* MAMBA_FLAG_LAYOUT_BLD; MAMBA_FLAG_TEST_WITHHOLD_HANDOFF (test
+                                * only: in the (batch, seqlen, dim) layout no tile hands its
+                                * state on, every wait runs out after some 0.3 s and
+                                * mamba_device_status() reports MAMBA_ERR_TIMEOUT) */
+    int32_t reserved;
+    const int32_t *seqlens;    /* device, (batch,), or NULL */
+    mamba_strides_t gate, x;
+    mamba_strides_t out;       /* out of the forward, dout of the backward */
+    mamba_strides_t dgate, dx;
+    void *workspace;           /* 256-byte aligned; not shared by calls that overlap on the GPU */
+    size_t workspace_bytes;
+} mamba_gated_dims_t;
+
+/* Steps between the states that a training forward keeps. */
+#define MAMBA_GATED_CHECKPOINT_STEPS 64
+
+/*
+ * Forward.
+ *   gate_bias        (dim,) fp32 or NULL;  initial_state (batch, dim) fp32 or NULL
+ *   last_state       (batch, dim) fp32 or NULL; may be the initial_state buffer
+ *   checkpoints      MAMBA_FLAG_LAYOUT_BLD only (NULL otherwise): NULL, or
+ *                    (batch, ceil(seqlen / 64), dim) fp32, receives the state
+ *                    entering each block of 64 steps, for the backward
+ * seqlen == 0 writes last_state only (initial_state, or zero).
+ * Asynchronous on `stream`; a bounded wait that gives up (see
+ * MAMBA_FLAG_TEST_WITHHOLD_HANDOFF) is reported by mamba_device_status().
+ */
+MAMBA_API size_t mamba_gated_scan_workspace_bytes(const mamba_gated_dims_t *dims);
+
+MAMBA_API mamba_status_t mamba_gated_scan_fwd(const void *gate, const void *x,
+                                              const float *gate_bias, const float *initial_state,
+                                              void *out, float *last_state, float *checkpoints,
+                                              const mamba_gated_dims_t *dims, cudaStream_t stream);
+
+/*
+ * Backward: gradients of a scalar loss given dout = dLoss/dout and optionally
+ * dlast_state = dLoss/dlast_state.  With l_t = dLoss/dh_t:
+ *   l_t = dout_t + a_{t+1} l_{t+1},  a_t the decay of step t
+ *   log_decay == 0:  dx_t = g_t l_t,   dgate_t = l_t (x_t - h_{t-1}) g_t (1 - g_t)
+ *   log_decay != 0:  dx_t = l_t,       dgate_t = l_t a_t h_{t-1}
+ *   dgate_bias_d = sum_{b,t} dgate_t,  dinitial_state = a_0 l_0
+ *   checkpoints      the forward's, from the same inputs; NULL: the states are
+ *                    recomputed (one more pass over gate and x)
+ *   dgate_bias (dim,), dinitial_state (batch, dim) fp32: NULL when not wanted
+ * dgate and dx must not alias inputs or each other.  Sums are added in a fixed
+ * order: results repeat bit for bit.  The workspace is smaller with the
+ * forward's checkpoints (have_checkpoints != 0 in the query).
+ */
+MAMBA_API size_t mamba_gated_scan_bwd_workspace_bytes(const mamba_gated_dims_t *dims,
+                                                      int have_checkpoints);
+
+MAMBA_API mamba_status_t mamba_gated_scan_bwd(
+    const void *gate, const void *x, const float *gate_bias, const float *initial_state,
+    const float *checkpoints, const void *dout, const float *dlast_state, void *dgate, void *dx,
+    float *dgate_bias, float *dinitial_state, const mamba_gated_dims_t *dims,
+    cudaStream_t stream);
+
+/*
+ * One token of generation: the same step on a stored state.
+ *   state            (batch, dim) fp32, updated in place
+ *   gate, x, out     (batch, dim) io_dtype; out = the new state; out may be x or gate
+ * Of dims, batch, dim, io_dtype, log_decay and the batch distances of gate, x
+ * and out are read (0: packed).
+ */
+MAMBA_API mamba_status_t mamba_gated_state_update(float *state, const void *gate, const void *x,
+                                                  const float *gate_bias, void *out,
+                                                  const mamba_gated_dims_t *dims,
+                                                  cudaStream_t stream);
+
+/*
+ * Layer norm with the residual add: the entry of the block ("超越注意力：探索
+ * Mamba与状态空间模型", section 代码实现概览: the sample block normalises its input
+ * and adds the branch back to it).  Per row of dim elements:
+ *
+ *   s = x + residual;   mean = sum(s) / dim;   var = sum((s - mean)^2) / dim
+ *   rstd = 1 / sqrt(var + eps);   out = (s - mean) rstd weight + bias
+ *
+ * rms != 0 is the root-mean-square form, mean = 0 throughout.
+ *   x, out           (rows, dim) io_dtype
+ *   residual         (rows, dim) residual_dtype or NULL (s = x)
+ *   residual_out     (rows, dim) residual_dtype or NULL: s, for the next block
+ *   weight, bias     (dim,) fp32; NULL: ones, zeros
+ *   mean, rstd       (rows,) fp32 or NULL: kept for the backward (mean is 0 with rms)
+ * The norm is taken of the fp32 sum, before s is rounded to residual_dtype.
+ * residual_dtype is io_dtype or MAMBA_F32.  Rows are contiguous, `*_stride`
+ * elements apart (0: packed; below dim: MAMBA_ERR_INVALID_ARG).  residual_out may be the residual
+ * buffer itself and out may be x, with the same stride; otherwise outputs must
+ * not alias inputs or each other.
+ */
+typedef struct {
+    int64_t rows, dim;
+    int32_t io_dtype;             /* x, out; dout, dx */
+    int32_t residual_dtype;       /* residual, residual_out; s, dresidual_out, dresidual */
+    int32_t rms;
+    float eps;                    /* forward; >= 0 */
+    int64_t x_stride;             /* forward: x;            backward: s */
+    int64_t out_stride;           /* forward: out;          backward: dout */
+    int64_t residual_stride;      /* forward: residual;     backward: dresidual */
+    int64_t residual_out_stride;  /* forward: residual_out; backward: dresidual_out */
+    int64_t dx_stride;            /* backward */
+    void *workspace;              /* backward; 256-byte aligned, not shared by overlapping calls */
+    size_t workspace_bytes;
+} mamba_norm_dims_t;
+
+MAMBA_API mamba_status_t mamba_layer_norm_fwd(const void *x, const void *residual,
+                                              const float *weight, const float *bias, void *out,
+                                              void *residual_out, float *mean, float *rstd,
+                                              const mamba_norm_dims_t *dims, cudaStream_t stream);
+
+/*
+ * Backward of the layer norm.  s is the forward's sum (its residual_out, or x
+ * when there was no residual: then residual_dtype is io_dtype), mean and rstd
+ * its statistics (mean is not read with rms).  With xh = (s - mean) rstd, q = dout weight,
+ * c1 = sum(q) / dim (0 with rms) and c2 = sum(q xh) / dim:
+ *   ds = rstd (q - c1 - xh c2) + dresidual_out
+ *   dweight = sum_rows dout xh,   dbias = sum_rows dout
+ *   dresidual_out    (rows, dim) residual_dtype or NULL: the gradient that
+ *                    reaches residual_out from later blocks
+ *   dx               (rows, dim) io_dtype: ds, the gradient of x (and of residual);
+ *                    may be dout or dresidual_out, with the same type and stride
+ *   dresidual        (rows, dim) residual_dtype or NULL: ds once more, for a
+ *                    residual of another type; may be dresidual_out, with the same stride
+ *   dweight, dbias   (dim,) fp32 or NULL (not computed)
+ * dims->workspace: at least mamba_layer_norm_bwd_workspace_bytes(dims) bytes
+ * (not needed when dweight and dbias are both NULL).  Sums are added in a fixed
+ * order: results repeat bit for bit.
+ */
+MAMBA_API size_t mamba_layer_norm_bwd_workspace_bytes(const mamba_norm_dims_t *dims);
+
+MAMBA_API mamba_status_t mamba_layer_norm_bwd(const void *s, const float *weight,
+                                              const float *mean, const float *rstd,
+                                              const void *dout, const void *dresidual_out,
+                                              void *dx, void *dresidual, float *dweight,
+                                              float *dbias, const mamba_norm_dims_t *dims,
+                                              cudaStream_t stream);
 
 /*
  * Mamba-2 layer: the selective state space with a scalar A per head

@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -20,7 +21,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIBRARY = PKG / "libmamba_ssm.so"
-SOURCES = [CSRC / "mamba_ssm.cu"]
+SOURCES = [CSRC / "mamba_ssm.cu", CSRC / "block_ops.cu"]
 DEPENDS = SOURCES + sorted(CSRC.glob("*.cuh")) + sorted(INCLUDE.glob("*.h"))
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -33,13 +34,18 @@ def nvcc_path() -> str:
     raise FileNotFoundError("nvcc not found (set NVCC or put CUDA's bin on PATH)")
 
 
-def build_command(output: Path, verbose: bool = False) -> list[str]:
-    cmd = [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared",
-           "-Xcompiler", "-fPIC,-fvisibility=hidden", "-cudart", "static",
-           f"-I{INCLUDE}", f"-I{CSRC}", *map(str, SOURCES), "-o", str(output)]
+def compile_command(source: Path, output: Path, verbose: bool = False) -> list[str]:
+    cmd = [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-c",
+           "-Xcompiler", "-fPIC,-fvisibility=hidden", f"-I{INCLUDE}", f"-I{CSRC}", str(source),
+           "-o", str(output)]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     return cmd
+
+
+def link_command(objects: list[Path], output: Path) -> list[str]:
+    return [nvcc_path(), *ARCH_FLAGS, "-shared", "-cudart", "static", *map(str, objects),
+            "-o", str(output)]
 
 
 def up_to_date() -> bool:
@@ -53,13 +59,24 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     if not force and not verbose and up_to_date():
         return LIBRARY
     tmp = LIBRARY.with_name(f".libmamba_ssm.{os.getpid()}.so")
-    cmd = build_command(tmp, verbose)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("nvcc failed building libmamba_ssm.so")
-    if verbose:
-        sys.stderr.write(res.stderr)
+    with tempfile.TemporaryDirectory() as work:
+        # the translation units compile side by side
+        jobs = []
+        for src in SOURCES:
+            obj = Path(work) / f"{src.stem}.o"
+            jobs.append((obj, subprocess.Popen(compile_command(src, obj, verbose), text=True,
+                                               stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        logs = [(job, job.communicate()[0]) for _, job in jobs]
+        failed = any(job.returncode != 0 for job, _ in logs)
+        if failed or verbose:
+            sys.stderr.write("".join(log for _, log in logs))
+        if failed:
+            raise RuntimeError("nvcc failed building libmamba_ssm.so")
+        res = subprocess.run(link_command([obj for obj, _ in jobs], tmp), capture_output=True,
+                             text=True)
+        if res.returncode != 0:
+            sys.stderr.write(res.stdout + res.stderr)
+            raise RuntimeError("nvcc failed linking libmamba_ssm.so")
     os.replace(tmp, LIBRARY)
     return LIBRARY
 

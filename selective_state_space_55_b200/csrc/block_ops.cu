@@ -1,0 +1,784 @@
+// C ABI of the operators around a recurrent block's projections: layer norm,
+// gated linear recurrence and the convolution's backward.  Argument checks,
+// planning and kernel dispatch.
+#include <algorithm>
+
+#include "mamba_ssm.h"
+#include "host_util.cuh"
+#include "layer_norm.cuh"
+#include "conv1d_backward.cuh"
+#include "gated_scan.cuh"
+
+namespace mamba {
+
+bool block_ops_take_status(int* code) { return take_device_status(code); }
+
+namespace {
+
+constexpr int64_t kLimit31 = (int64_t)1 << 31;
+
+mamba_status_t status_of(cudaError_t e) { return e == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA; }
+
+// CTAs of `kernel` that fit on an SM, cached per device by the caller's slot array.
+template <typename Kernel>
+int resident_ctas(Kernel kernel, int threads, size_t smem, int* cache, int dev) {
+    int n = (dev >= 0 && dev < kMaxDevices) ? cache[dev] : 0;
+    if (n > 0) return n;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < kMaxDevices) cache[dev] = n;
+    return n;
+}
+
+cudaError_t launch_column_sum(const float* partial, int64_t rows, int64_t cols, int64_t split,
+                              float* first, float* second, cudaStream_t stream) {
+    const unsigned grid = (unsigned)((cols + 31) / 32);
+    column_sum_kernel<<<grid, kColSumThreads, 0, stream>>>(partial, rows, cols, split, first, second);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ layer norm
+
+struct NormPlan {
+    bool wide;          // rows beyond a CTA's registers
+    int chunks;         // of 8 elements per thread (register kernels)
+    int threads;        // per row
+    int teams;          // rows side by side in a CTA
+    int64_t ctas;
+    int64_t slices;     // wide backward: row slices of the column sums
+};
+
+// Rows up to 512 elements: a warp each, 8 to a CTA, 8 or 16 elements per lane.
+// Up to 8192: a CTA of dim / 8 threads.  Beyond: 1024 threads that re-read.
+NormPlan plan_norm(int64_t rows, int64_t dim, int sms, bool backward) {
+    NormPlan n{};
+    n.teams = 1;
+    if (dim <= kNormWarpDim) {
+        n.chunks = dim <= 32 * kNormElems ? 1 : 2;
+        n.threads = 32;
+        n.teams = rows >= (int64_t)sms * kNormRowsPerCta ? kNormRowsPerCta : 1;
+    } else if (dim <= kNormCtaDim) {
+        n.chunks = 1;
+        n.threads = (int)((dim + kNormElems * 32 - 1) / (kNormElems * 32) * 32);
+    } else {
+        n.wide = true;
+        n.threads = kNormWideThreads;
+    }
+    // As many CTAs as 2048 threads per SM (the backward holds twice the registers:
+    // 1024), each walking rows with its weights in registers.
+    const int per_sm = std::max(1, (backward ? 1024 : 2048) / (n.threads * n.teams));
+    n.ctas = std::max<int64_t>(1, std::min<int64_t>((rows + n.teams - 1) / n.teams, (int64_t)sms * std::min(per_sm, 16)));
+    const int64_t col_blocks = (dim + kNormColThreads - 1) / kNormColThreads;
+    n.slices = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(rows, 1024), (int64_t)sms * 8 / col_blocks));
+    return n;
+}
+
+mamba_status_t check_norm(const mamba_norm_dims_t* d) {
+    if (d == nullptr) return MAMBA_ERR_INVALID_ARG;
+    if (d->rows < 0 || d->dim < 0 || d->rows >= ((int64_t)1 << 40)) return MAMBA_ERR_INVALID_ARG;
+    if (d->dim > ((int64_t)1 << 28)) return MAMBA_ERR_UNSUPPORTED;
+    if (!dtype_ok(d->io_dtype)) return MAMBA_ERR_UNSUPPORTED;
+    if (d->residual_dtype != d->io_dtype && d->residual_dtype != MAMBA_F32) return MAMBA_ERR_UNSUPPORTED;
+    const int64_t strides[5] = {d->x_stride, d->out_stride, d->residual_stride, d->residual_out_stride, d->dx_stride};
+    for (const int64_t s : strides)
+        if (s != 0 && (s < d->dim || s >= ((int64_t)1 << 40) || (d->rows > 0 && s > INT64_MAX / 8 / d->rows)))
+            return MAMBA_ERR_INVALID_ARG;
+    return MAMBA_OK;
+}
+
+int64_t norm_stride(int64_t s, int64_t dim) { return s != 0 ? s : dim; }
+
+// Vectors of 8 elements: pointer and stride on 16-byte boundaries.
+bool norm_vec(const void* p, int64_t stride, int es) {
+    return p == nullptr || (aligned(p, 16) && (stride * es) % 16 == 0);
+}
+
+template <typename IoT, bool kVec>
+cudaError_t launch_norm_fwd(const NormParams& prm, const NormPlan& n, cudaStream_t stream) {
+    const dim3 block(n.threads, n.teams);
+    const unsigned grid = (unsigned)n.ctas;
+    if (n.wide) layer_norm_fwd_wide_kernel<IoT, kVec><<<grid, block, 0, stream>>>(prm);
+    else if (n.chunks == 1) layer_norm_fwd_kernel<IoT, 1, kVec><<<grid, block, 0, stream>>>(prm);
+    else layer_norm_fwd_kernel<IoT, 2, kVec><<<grid, block, 0, stream>>>(prm);
+    return cudaGetLastError();
+}
+
+template <typename IoT, bool kVec>
+cudaError_t launch_norm_bwd(const NormParams& prm, const NormPlan& n, cudaStream_t stream) {
+    const dim3 block(n.threads, n.teams);
+    const unsigned grid = (unsigned)n.ctas;
+    if (n.wide) {                       // sums first: dx may replace dout
+        if (prm.partial != nullptr) {
+            const dim3 cols((unsigned)((prm.dim + kNormColThreads - 1) / kNormColThreads), (unsigned)n.slices);
+            layer_norm_bwd_cols_kernel<IoT><<<cols, kNormColThreads, 0, stream>>>(prm);
+        }
+        layer_norm_bwd_wide_kernel<IoT, kVec><<<grid, block, 0, stream>>>(prm);
+        return cudaGetLastError();
+    }
+    const size_t smem = n.teams > 1 ? (size_t)n.teams * 2 * prm.dim * sizeof(float) : 0;
+    if (n.chunks == 1) layer_norm_bwd_kernel<IoT, 1, kVec><<<grid, block, smem, stream>>>(prm);
+    else layer_norm_bwd_kernel<IoT, 2, kVec><<<grid, block, smem, stream>>>(prm);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ gated recurrence
+
+// Distances of one tensor: packed when both are 0.
+bool resolve_strides(const mamba_strides_t& s, int64_t batch, int64_t rows, int64_t inner, bool output,
+                     GatedStrides* out) {
+    out->batch = s.batch;
+    out->row = s.row;
+    if (s.batch == 0 && s.row == 0) {
+        out->batch = rows * inner;
+        out->row = inner;
+        return true;
+    }
+    const int64_t lim = (int64_t)1 << 50;
+    if (s.batch < 0 || s.row < 0 || s.batch >= lim || s.row >= lim) return false;
+    if ((rows > 1 && s.row < inner) || (batch > 1 && s.batch < inner)) return false;
+    if ((rows > 1 && s.row > lim / rows) || (batch > 1 && s.batch > lim / batch)) return false;
+    if (output && rows > 1 && batch > 1) {
+        const bool row_first = s.row <= s.batch;
+        const int64_t near = row_first ? s.row : s.batch, far = row_first ? s.batch : s.row;
+        if (far < near * ((row_first ? rows : batch) - 1) + inner) return false;
+    }
+    return true;
+}
+
+mamba_status_t check_gated(const mamba_gated_dims_t* d) {
+    if (d == nullptr) return MAMBA_ERR_INVALID_ARG;
+    if (d->batch < 0 || d->dim < 0 || d->seqlen < 0) return MAMBA_ERR_INVALID_ARG;
+    if (d->batch >= kLimit31 || d->dim >= kLimit31 || d->seqlen >= kLimit31) return MAMBA_ERR_INVALID_ARG;
+    if (!dtype_ok(d->io_dtype)) return MAMBA_ERR_UNSUPPORTED;
+    if ((d->flags & ~(MAMBA_FLAG_LAYOUT_BLD | MAMBA_FLAG_TEST_WITHHOLD_HANDOFF)) != 0) return MAMBA_ERR_UNSUPPORTED;
+    // element counts stay far inside 64 bits
+    if (d->batch > 0 && d->dim > 0 && d->seqlen > 0 &&
+        (d->batch > ((int64_t)1 << 50) / d->dim || d->batch * d->dim > ((int64_t)1 << 50) / d->seqlen))
+        return MAMBA_ERR_UNSUPPORTED;
+    return MAMBA_OK;
+}
+
+bool gated_bld(const mamba_gated_dims_t* d) { return (d->flags & MAMBA_FLAG_LAYOUT_BLD) != 0; }
+
+struct GatedLayout {           // offsets in the workspace, bytes
+    size_t tickets, flags, flags2, zeroed, maps, enter, carry, bias, states, total;
+    int64_t tiles, groups_per_row, groups, items;
+    int warps, width;          // (batch, dim, seqlen): warps per chain, lanes per chain
+};
+
+// One tile per chain needs no look-back: no tickets, flags or maps.
+mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool recompute, int phase_max,
+                            GatedLayout* w) {
+    *w = GatedLayout{};
+    const int64_t L = d->seqlen, chains = d->batch * d->dim;
+    size_t off = 0;
+    auto take = [&off](size_t bytes) { const size_t at = off; off += align256(bytes); return at; };
+    if (gated_bld(d)) {
+        w->tiles = (L + kGatedTile - 1) / kGatedTile;
+        w->groups_per_row = (d->dim + kGatedChannels - 1) / kGatedChannels;
+        w->groups = d->batch * w->groups_per_row;
+        w->items = w->groups * w->tiles;
+        if (w->items >= kLimit31 / 2) return MAMBA_ERR_UNSUPPORTED;
+        const size_t states = (size_t)d->batch * w->tiles * d->dim * sizeof(float);
+        if (w->tiles > 1) {
+            w->tickets = take(2 * sizeof(unsigned int));
+            w->flags = take((size_t)w->items * sizeof(unsigned int));
+            if (backward && recompute) w->flags2 = take((size_t)w->items * sizeof(unsigned int));
+            w->zeroed = off;
+            w->maps = take((size_t)w->items * 32 * sizeof(float4));
+        }
+        if ((!backward && w->tiles > 1) || (backward && recompute)) w->enter = take(states);
+        if (backward) {
+            w->carry = take(states);
+            w->bias = take(states);
+        }
+    } else {
+        // Lanes take 8 steps each; the row's start may lie up to phase_max steps into its tile.
+        const int64_t span = L + phase_max;
+        w->warps = 1;
+        w->width = 32;
+        if (span <= kWarpSteps) {
+            while (w->width > 1 && (w->width / 2) * (int64_t)kLaneSteps >= span) w->width /= 2;
+        } else {
+            while (w->warps < kGatedWarps && w->warps * (int64_t)kWarpSteps < span) w->warps *= 2;
+        }
+        const int64_t step = (int64_t)w->warps * w->width * kLaneSteps;
+        w->tiles = (span + step - 1) / step;
+        if (backward) {
+            w->bias = take((size_t)chains * sizeof(float));
+            if (w->tiles > 1) w->states = take((size_t)chains * w->tiles * sizeof(float));
+        }
+    }
+    w->total = off;
+    return MAMBA_OK;
+}
+
+template <typename IoT, bool kLog, bool kVec, bool kBackward>
+cudaError_t launch_gated_tiles(const GatedParams& prm, int dev, int sms, cudaStream_t stream) {
+    static int resident[kMaxDevices] = {0};
+    auto kernel = gated_scan_fwd_kernel<IoT, kLog, kVec>;
+    if constexpr (kBackward) kernel = gated_scan_bwd_kernel<IoT, kLog, kVec>;
+    const int per_sm = resident_ctas(kernel, kGatedThreads, 0, resident, dev);
+    if (per_sm <= 0) return cudaErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)std::min<int64_t>(prm.items, (int64_t)per_sm * sms);
+    kernel<<<grid, kGatedThreads, 0, stream>>>(prm);
+    return cudaGetLastError();
+}
+
+template <bool kBackward>
+cudaError_t dispatch_gated_tiles(const GatedParams& prm, bool bf16, bool log_decay, bool vec, int dev,
+                                 int sms, cudaStream_t stream) {
+    using B = __nv_bfloat16;
+    if (bf16) {
+        if (log_decay)
+            return vec ? launch_gated_tiles<B, true, true, kBackward>(prm, dev, sms, stream)
+                       : launch_gated_tiles<B, true, false, kBackward>(prm, dev, sms, stream);
+        return vec ? launch_gated_tiles<B, false, true, kBackward>(prm, dev, sms, stream)
+                   : launch_gated_tiles<B, false, false, kBackward>(prm, dev, sms, stream);
+    }
+    if (log_decay)
+        return vec ? launch_gated_tiles<float, true, true, kBackward>(prm, dev, sms, stream)
+                   : launch_gated_tiles<float, true, false, kBackward>(prm, dev, sms, stream);
+    return vec ? launch_gated_tiles<float, false, true, kBackward>(prm, dev, sms, stream)
+               : launch_gated_tiles<float, false, false, kBackward>(prm, dev, sms, stream);
+}
+
+template <typename IoT, bool kLog, bool kBackward>
+cudaError_t launch_gated_rows(const GatedParams& prm, const GatedLayout& w, cudaStream_t stream) {
+    const int64_t per_cta = w.warps > 1 ? kGatedWarps / w.warps : (int64_t)kGatedWarps * (32 / w.width);
+    const unsigned grid = (unsigned)((prm.chains + per_cta - 1) / per_cta);
+#define MAMBA_GATED_ROWS(W)                                                                          \
+    if constexpr (kBackward)                                                                         \
+        gated_scan_rows_bwd_kernel<IoT, kLog, W><<<grid, kGatedThreads, 0, stream>>>(prm, w.width); \
+    else                                                                                             \
+        gated_scan_rows_fwd_kernel<IoT, kLog, W><<<grid, kGatedThreads, 0, stream>>>(prm, w.width)
+    switch (w.warps) {
+        case 1: MAMBA_GATED_ROWS(1); break;
+        case 2: MAMBA_GATED_ROWS(2); break;
+        case 4: MAMBA_GATED_ROWS(4); break;
+        default: MAMBA_GATED_ROWS(8); break;
+    }
+#undef MAMBA_GATED_ROWS
+    return cudaGetLastError();
+}
+
+template <bool kBackward>
+cudaError_t dispatch_gated_rows(const GatedParams& prm, const GatedLayout& w, bool bf16, bool log_decay,
+                                cudaStream_t stream) {
+    using B = __nv_bfloat16;
+    if (bf16)
+        return log_decay ? launch_gated_rows<B, true, kBackward>(prm, w, stream)
+                         : launch_gated_rows<B, false, kBackward>(prm, w, stream);
+    return log_decay ? launch_gated_rows<float, true, kBackward>(prm, w, stream)
+                     : launch_gated_rows<float, false, kBackward>(prm, w, stream);
+}
+
+// Can every row of this tensor start a vector of `bytes`?
+bool rows_aligned(const void* p, const GatedStrides& s, int es, int bytes) {
+    return p == nullptr || (aligned(p, bytes) && (s.batch * es) % bytes == 0 && (s.row * es) % bytes == 0);
+}
+
+// Steps by which a row of gate may start past a 16-byte boundary, at most.
+int gated_phase_max(const void* gate, const GatedStrides& s, int es) {
+    return rows_aligned(gate, s, es, 16) ? 0 : 16 / es - 1;
+}
+
+// What both directions share: sizes, inputs, distances of gate and x.
+mamba_status_t gated_common(const void* gate, const void* x, const float* bias, const float* h0,
+                            const mamba_gated_dims_t* d, GatedParams* prm) {
+    const int64_t rows = gated_bld(d) ? d->seqlen : d->dim, inner = gated_bld(d) ? d->dim : d->seqlen;
+    const int es = dtype_bytes(d->io_dtype);
+    if (d->seqlen > 0 && (gate == nullptr || x == nullptr)) return MAMBA_ERR_INVALID_ARG;
+    if ((gate && !aligned(gate, es)) || (x && !aligned(x, es)) || (bias && !aligned(bias, 4)) ||
+        (h0 && !aligned(h0, 4)) || (d->seqlens && !aligned(d->seqlens, 4)))
+        return MAMBA_ERR_ALIGN;
+    if (!resolve_strides(d->gate, d->batch, rows, inner, false, &prm->gate_s) ||
+        !resolve_strides(d->x, d->batch, rows, inner, false, &prm->x_s))
+        return MAMBA_ERR_INVALID_ARG;
+    prm->gate = gate;
+    prm->x = x;
+    prm->bias = bias;
+    prm->h0 = h0;
+    prm->seqlens = d->seqlens;
+    prm->batch = d->batch;
+    prm->dim = d->dim;
+    prm->seqlen = d->seqlen;
+    prm->chains = d->batch * d->dim;
+    prm->withhold = (d->flags & MAMBA_FLAG_TEST_WITHHOLD_HANDOFF) != 0;
+    return MAMBA_OK;
+}
+
+void gated_apply_layout(const GatedLayout& w, uint8_t* ws, GatedParams* prm) {
+    prm->tiles = w.tiles;
+    prm->groups_per_row = w.groups_per_row;
+    prm->groups = w.groups;
+    prm->items = w.items;
+    prm->ticket = w.zeroed ? reinterpret_cast<unsigned int*>(ws + w.tickets) : nullptr;
+    prm->flags = reinterpret_cast<unsigned int*>(ws + w.flags);
+    prm->maps = reinterpret_cast<float4*>(ws + w.maps);
+}
+
+mamba_status_t check_workspace(const void* ws, size_t have, size_t need) {
+    if (need == 0) return MAMBA_OK;
+    if (ws == nullptr || have < need) return MAMBA_ERR_WORKSPACE;
+    return aligned(ws, 256) ? MAMBA_OK : MAMBA_ERR_ALIGN;
+}
+
+cudaError_t copy_or_zero(float* dst, const float* src, size_t bytes, cudaStream_t stream) {
+    if (dst == nullptr || dst == src) return cudaSuccess;
+    return src != nullptr ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, stream)
+                          : cudaMemsetAsync(dst, 0, bytes, stream);
+}
+
+// ------------------------------------------------------------------ convolution backward
+
+struct ConvBwdPlan { int64_t stretch_tiles, stretches; size_t bytes; };
+
+// A warp per row; rows are cut into stretches of whole tiles while that leaves
+// fewer than 48 warps per SM.
+mamba_status_t plan_conv_bwd(const mamba_dims_t* d, int width, int sms, ConvBwdPlan* n) {
+    const int64_t chains = d->batch * d->dim;
+    const int es = dtype_bytes(d->io_dtype);
+    const int64_t tiles = std::max<int64_t>(1, (d->seqlen + 16 / es - 1 + kWarpSteps - 1) / kWarpSteps);
+    const int64_t want = chains > 0 ? ((int64_t)sms * 48 + chains - 1) / chains : 1;
+    n->stretches = std::max<int64_t>(1, std::min<int64_t>(tiles, want));
+    n->stretch_tiles = (tiles + n->stretches - 1) / n->stretches;
+    n->stretches = (tiles + n->stretch_tiles - 1) / n->stretch_tiles;
+    if (chains * n->stretches / kConvBwdWarps >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
+    n->bytes = align256((size_t)d->batch * n->stretches * (width + 1) * d->dim * sizeof(float));
+    return MAMBA_OK;
+}
+
+mamba_status_t check_conv_bwd(const mamba_dims_t* d, int width) {
+    if (d == nullptr) return MAMBA_ERR_INVALID_ARG;
+    if (d->batch < 0 || d->dim < 0 || d->seqlen < 0) return MAMBA_ERR_INVALID_ARG;
+    if (width < 1 || width > MAMBA_MAX_CONV_WIDTH) return MAMBA_ERR_UNSUPPORTED;
+    if (!dtype_ok(d->io_dtype)) return MAMBA_ERR_UNSUPPORTED;
+    if (d->batch >= kLimit31 || d->dim >= kLimit31 || d->seqlen >= kLimit31) return MAMBA_ERR_INVALID_ARG;
+    if (d->batch * d->dim >= ((int64_t)1 << 40)) return MAMBA_ERR_UNSUPPORTED;
+    return MAMBA_OK;
+}
+
+template <typename IoT>
+cudaError_t launch_conv_bwd(const ConvBwdParams& prm, int width, cudaStream_t stream) {
+    const unsigned grid = (unsigned)((prm.chains * prm.stretches + kConvBwdWarps - 1) / kConvBwdWarps);
+    constexpr int kThreads = kConvBwdWarps * 32;
+    switch (width) {
+        case 1: causal_conv1d_bwd_kernel<IoT, 1><<<grid, kThreads, 0, stream>>>(prm); break;
+        case 2: causal_conv1d_bwd_kernel<IoT, 2><<<grid, kThreads, 0, stream>>>(prm); break;
+        case 3: causal_conv1d_bwd_kernel<IoT, 3><<<grid, kThreads, 0, stream>>>(prm); break;
+        default: causal_conv1d_bwd_kernel<IoT, 4><<<grid, kThreads, 0, stream>>>(prm); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace mamba
+
+using namespace mamba;
+
+extern "C" {
+
+MAMBA_API mamba_status_t mamba_layer_norm_fwd(const void* x, const void* residual, const float* weight,
+                                              const float* bias, void* out, void* residual_out,
+                                              float* mean, float* rstd, const mamba_norm_dims_t* dims,
+                                              cudaStream_t stream) {
+    const mamba_status_t st = check_norm(dims);
+    if (st != MAMBA_OK) return st;
+    if (!(dims->eps >= 0.0f)) return MAMBA_ERR_INVALID_ARG;
+    if (dims->rows == 0 || dims->dim == 0) return MAMBA_OK;
+    if (x == nullptr || out == nullptr) return MAMBA_ERR_INVALID_ARG;
+    const int es = dtype_bytes(dims->io_dtype), rs = dtype_bytes(dims->residual_dtype);
+    if (!aligned(x, es) || !aligned(out, es) || (residual && !aligned(residual, rs)) ||
+        (residual_out && !aligned(residual_out, rs)) || (weight && !aligned(weight, 4)) ||
+        (bias && !aligned(bias, 4)) || (mean && !aligned(mean, 4)) || (rstd && !aligned(rstd, 4)))
+        return MAMBA_ERR_ALIGN;
+    NormParams prm{};
+    prm.x = x;
+    prm.residual = residual;
+    prm.weight = weight;
+    prm.bias = bias;
+    prm.out = out;
+    prm.residual_out = residual_out;
+    prm.mean = mean;
+    prm.rstd = rstd;
+    prm.rows = dims->rows;
+    prm.dim = (int)dims->dim;
+    prm.x_stride = norm_stride(dims->x_stride, dims->dim);
+    prm.out_stride = norm_stride(dims->out_stride, dims->dim);
+    prm.residual_stride = norm_stride(dims->residual_stride, dims->dim);
+    prm.residual_out_stride = norm_stride(dims->residual_out_stride, dims->dim);
+    prm.eps = dims->eps;
+    prm.rms = dims->rms != 0;
+    prm.res_f32 = dims->residual_dtype == MAMBA_F32;
+    // buffers may coincide only element for element
+    if ((out == x && prm.out_stride != prm.x_stride) || (residual != nullptr && residual == out) ||
+        (residual_out != nullptr &&
+         (residual_out == x || residual_out == out ||
+          (residual_out == residual && prm.residual_out_stride != prm.residual_stride))))
+        return MAMBA_ERR_INVALID_ARG;
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return MAMBA_ERR_CUDA;
+    const NormPlan n = plan_norm(dims->rows, dims->dim, sms, false);
+    const bool vec = dims->dim % kNormElems == 0 && norm_vec(x, prm.x_stride, es) &&
+                     norm_vec(out, prm.out_stride, es) && norm_vec(residual, prm.residual_stride, rs) &&
+                     norm_vec(residual_out, prm.residual_out_stride, rs) && norm_vec(weight, 0, 4) &&
+                     norm_vec(bias, 0, 4);
+    if (dims->io_dtype == MAMBA_BF16)
+        return status_of(vec ? launch_norm_fwd<__nv_bfloat16, true>(prm, n, stream)
+                             : launch_norm_fwd<__nv_bfloat16, false>(prm, n, stream));
+    return status_of(vec ? launch_norm_fwd<float, true>(prm, n, stream)
+                         : launch_norm_fwd<float, false>(prm, n, stream));
+}
+
+MAMBA_API size_t mamba_layer_norm_bwd_workspace_bytes(const mamba_norm_dims_t* dims) {
+    if (check_norm(dims) != MAMBA_OK) return static_cast<size_t>(-1);
+    if (dims->rows == 0 || dims->dim == 0) return 0;
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return static_cast<size_t>(-1);
+    const NormPlan n = plan_norm(dims->rows, dims->dim, sms, true);
+    return align256((size_t)(n.wide ? n.slices : n.ctas) * 2 * dims->dim * sizeof(float));
+}
+
+MAMBA_API mamba_status_t mamba_layer_norm_bwd(const void* s, const float* weight, const float* mean,
+                                              const float* rstd, const void* dout,
+                                              const void* dresidual_out, void* dx, void* dresidual,
+                                              float* dweight, float* dbias,
+                                              const mamba_norm_dims_t* dims, cudaStream_t stream) {
+    mamba_status_t st = check_norm(dims);
+    if (st != MAMBA_OK) return st;
+    if (dims->dim == 0) return MAMBA_OK;
+    if ((dweight && !aligned(dweight, 4)) || (dbias && !aligned(dbias, 4))) return MAMBA_ERR_ALIGN;
+    if (dims->rows == 0) {              // sums over no rows
+        cudaError_t e = copy_or_zero(dweight, nullptr, (size_t)dims->dim * sizeof(float), stream);
+        if (e == cudaSuccess) e = copy_or_zero(dbias, nullptr, (size_t)dims->dim * sizeof(float), stream);
+        return status_of(e);
+    }
+    if (s == nullptr || dout == nullptr || dx == nullptr || rstd == nullptr ||
+        (!dims->rms && mean == nullptr))
+        return MAMBA_ERR_INVALID_ARG;
+    const int es = dtype_bytes(dims->io_dtype), rs = dtype_bytes(dims->residual_dtype);
+    if (!aligned(s, rs) || !aligned(dout, es) || !aligned(dx, es) ||
+        (dresidual_out && !aligned(dresidual_out, rs)) || (dresidual && !aligned(dresidual, rs)) ||
+        (weight && !aligned(weight, 4)) || (mean && !aligned(mean, 4)) || !aligned(rstd, 4))
+        return MAMBA_ERR_ALIGN;
+    NormParams prm{};
+    prm.x = s;
+    prm.weight = weight;
+    prm.mean_in = mean;
+    prm.rstd_in = rstd;
+    prm.dout = dout;
+    prm.dresidual_out = dresidual_out;
+    prm.dx = dx;
+    prm.dresidual = dresidual;
+    prm.rows = dims->rows;
+    prm.dim = (int)dims->dim;
+    prm.x_stride = norm_stride(dims->x_stride, dims->dim);
+    prm.out_stride = norm_stride(dims->out_stride, dims->dim);
+    prm.residual_out_stride = norm_stride(dims->residual_out_stride, dims->dim);
+    prm.dx_stride = norm_stride(dims->dx_stride, dims->dim);
+    prm.dresidual_stride = norm_stride(dims->residual_stride, dims->dim);
+    prm.rms = dims->rms != 0;
+    prm.res_f32 = dims->residual_dtype == MAMBA_F32;
+    prm.has_dw = dweight != nullptr;
+    prm.has_db = dbias != nullptr;
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return MAMBA_ERR_CUDA;
+    const NormPlan n = plan_norm(dims->rows, dims->dim, sms, true);
+    // buffers may coincide only element for element
+    if (dx == s || (dresidual != nullptr && (dresidual == s || dresidual == dx || dresidual == dout)) ||
+        (dx == dout && prm.dx_stride != prm.out_stride) ||
+        (dx == dresidual_out && (prm.dx_stride != prm.residual_out_stride || es != rs)) ||
+        (dresidual != nullptr && dresidual == dresidual_out && prm.dresidual_stride != prm.residual_out_stride))
+        return MAMBA_ERR_INVALID_ARG;
+    const int sums = prm.has_dw + prm.has_db;
+    if (sums > 0) {
+        const size_t need = align256((size_t)(n.wide ? n.slices : n.ctas) * 2 * dims->dim * sizeof(float));
+        st = check_workspace(dims->workspace, dims->workspace_bytes, need);
+        if (st != MAMBA_OK) return st;
+        prm.partial = static_cast<float*>(dims->workspace);
+    }
+    const bool vec = dims->dim % kNormElems == 0 && norm_vec(s, prm.x_stride, rs) &&
+                     norm_vec(dout, prm.out_stride, es) && norm_vec(dresidual_out, prm.residual_out_stride, rs) &&
+                     norm_vec(dx, prm.dx_stride, es) && norm_vec(dresidual, prm.dresidual_stride, rs) &&
+                     norm_vec(weight, 0, 4);
+    cudaError_t e;
+    if (dims->io_dtype == MAMBA_BF16)
+        e = vec ? launch_norm_bwd<__nv_bfloat16, true>(prm, n, stream)
+                : launch_norm_bwd<__nv_bfloat16, false>(prm, n, stream);
+    else
+        e = vec ? launch_norm_bwd<float, true>(prm, n, stream) : launch_norm_bwd<float, false>(prm, n, stream);
+    if (e == cudaSuccess && sums > 0)
+        e = launch_column_sum(prm.partial, n.wide ? n.slices : n.ctas, (int64_t)sums * dims->dim,
+                              prm.has_dw ? dims->dim : 0, dweight, dbias, stream);
+    return status_of(e);
+}
+
+MAMBA_API size_t mamba_causal_conv1d_bwd_workspace_bytes(const mamba_dims_t* dims, int width) {
+    if (check_conv_bwd(dims, width) != MAMBA_OK) return static_cast<size_t>(-1);
+    if (dims->batch * dims->dim == 0) return 0;
+    const int sms = current_sm_count(nullptr);
+    ConvBwdPlan n;
+    if (sms <= 0 || plan_conv_bwd(dims, width, sms, &n) != MAMBA_OK) return static_cast<size_t>(-1);
+    return n.bytes;
+}
+
+MAMBA_API mamba_status_t mamba_causal_conv1d_bwd(
+    const void* x, const float* weight, const float* bias, const void* initial_conv_state, int width,
+    int silu, const void* dout, const void* dfinal_conv_state, void* dx, float* dweight, float* dbias,
+    void* dinitial_conv_state, const mamba_dims_t* dims, cudaStream_t stream) {
+    mamba_status_t st = check_conv_bwd(dims, width);
+    if (st != MAMBA_OK) return st;
+    if (dims->dim == 0) return MAMBA_OK;
+    if (weight == nullptr || dweight == nullptr) return MAMBA_ERR_INVALID_ARG;
+    if (!aligned(weight, 4) || !aligned(dweight, 4) || (bias && !aligned(bias, 4)) || (dbias && !aligned(dbias, 4)))
+        return MAMBA_ERR_ALIGN;
+    const int64_t chains = dims->batch * dims->dim;
+    if (chains == 0) {                  // sums over no rows
+        cudaError_t e = copy_or_zero(dweight, nullptr, (size_t)dims->dim * width * sizeof(float), stream);
+        if (e == cudaSuccess) e = copy_or_zero(dbias, nullptr, (size_t)dims->dim * sizeof(float), stream);
+        return status_of(e);
+    }
+    if (dims->seqlen > 0 && (x == nullptr || dout == nullptr || dx == nullptr)) return MAMBA_ERR_INVALID_ARG;
+    const int es = dtype_bytes(dims->io_dtype);
+    const void* io_ptrs[6] = {x, dout, dx, initial_conv_state, dfinal_conv_state, dinitial_conv_state};
+    for (const void* q : io_ptrs)
+        if (q && !aligned(q, es)) return MAMBA_ERR_ALIGN;
+    if ((dx != nullptr && (dx == x || dx == dout)) ||
+        (dinitial_conv_state != nullptr &&
+         (dinitial_conv_state == initial_conv_state || dinitial_conv_state == dfinal_conv_state)))
+        return MAMBA_ERR_INVALID_ARG;
+    const int sms = current_sm_count(nullptr);
+    if (sms <= 0) return MAMBA_ERR_CUDA;
+    ConvBwdPlan n;
+    st = plan_conv_bwd(dims, width, sms, &n);
+    if (st != MAMBA_OK) return st;
+    st = check_workspace(dims->workspace, dims->workspace_bytes, n.bytes);
+    if (st != MAMBA_OK) return st;
+    ConvBwdParams prm{};
+    prm.x = x;
+    prm.dout = dout;
+    prm.weight = weight;
+    prm.bias = bias;
+    prm.init = initial_conv_state;
+    prm.dfinal = dfinal_conv_state;
+    prm.dx = dx;
+    prm.dinit = dinitial_conv_state;
+    prm.partial = static_cast<float*>(dims->workspace);
+    prm.dim = dims->dim;
+    prm.seqlen = dims->seqlen;
+    prm.chains = chains;
+    prm.stretch_tiles = n.stretch_tiles;
+    prm.stretches = n.stretches;
+    prm.silu = silu != 0;
+    cudaError_t e = dims->io_dtype == MAMBA_BF16 ? launch_conv_bwd<__nv_bfloat16>(prm, width, stream)
+                                                 : launch_conv_bwd<float>(prm, width, stream);
+    if (e == cudaSuccess)
+        e = launch_column_sum(prm.partial, dims->batch * n.stretches, (int64_t)(width + 1) * dims->dim,
+                              (int64_t)width * dims->dim, dweight, dbias, stream);
+    return status_of(e);
+}
+
+MAMBA_API size_t mamba_gated_scan_workspace_bytes(const mamba_gated_dims_t* dims) {
+    GatedLayout w;
+    if (check_gated(dims) != MAMBA_OK) return static_cast<size_t>(-1);
+    if (dims->batch * dims->dim == 0 || dims->seqlen == 0) return 0;
+    return gated_layout(dims, false, false, 0, &w) == MAMBA_OK ? w.total : static_cast<size_t>(-1);
+}
+
+MAMBA_API mamba_status_t mamba_gated_scan_fwd(const void* gate, const void* x, const float* gate_bias,
+                                              const float* initial_state, void* out, float* last_state,
+                                              float* checkpoints, const mamba_gated_dims_t* dims,
+                                              cudaStream_t stream) {
+    mamba_status_t st = check_gated(dims);
+    if (st != MAMBA_OK) return st;
+    if (dims->batch * dims->dim == 0) return MAMBA_OK;
+    const bool bld = gated_bld(dims);
+    const int64_t rows = bld ? dims->seqlen : dims->dim, inner = bld ? dims->dim : dims->seqlen;
+    const int es = dtype_bytes(dims->io_dtype);
+    GatedParams prm{};
+    st = gated_common(gate, x, gate_bias, initial_state, dims, &prm);
+    if (st != MAMBA_OK) return st;
+    if (dims->seqlen > 0 && out == nullptr) return MAMBA_ERR_INVALID_ARG;
+    if (checkpoints != nullptr && !bld) return MAMBA_ERR_UNSUPPORTED;
+    if ((out && !aligned(out, es)) || (last_state && !aligned(last_state, 4)) || (checkpoints && !aligned(checkpoints, 4)))
+        return MAMBA_ERR_ALIGN;
+    if (!resolve_strides(dims->out, dims->batch, rows, inner, true, &prm.out_s)) return MAMBA_ERR_INVALID_ARG;
+    if (out != nullptr && (out == gate || out == x)) return MAMBA_ERR_INVALID_ARG;
+    if (dims->seqlen == 0)
+        return status_of(copy_or_zero(last_state, initial_state, (size_t)prm.chains * sizeof(float), stream));
+    GatedLayout w;
+    st = gated_layout(dims, false, false, bld ? 0 : gated_phase_max(gate, prm.gate_s, es), &w);
+    if (st != MAMBA_OK) return st;
+    st = check_workspace(dims->workspace, dims->workspace_bytes, w.total);
+    if (st != MAMBA_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(dims->workspace);
+    gated_apply_layout(w, ws, &prm);
+    prm.out = out;
+    prm.last = last_state;
+    const bool bf16 = dims->io_dtype == MAMBA_BF16, log_decay = dims->log_decay != 0;
+    if (!bld) {
+        const int64_t per_cta = w.warps > 1 ? kGatedWarps / w.warps : kGatedWarps;
+        if (prm.chains / per_cta >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
+        return status_of(dispatch_gated_rows<false>(prm, w, bf16, log_decay, stream));
+    }
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
+    if (sms <= 0) return MAMBA_ERR_CUDA;
+    if (w.zeroed && cudaMemsetAsync(ws, 0, w.zeroed, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
+    prm.enter = checkpoints != nullptr ? checkpoints : (w.tiles > 1 ? reinterpret_cast<float*>(ws + w.enter) : nullptr);
+    const bool vec = dims->dim % 2 == 0 && rows_aligned(gate, prm.gate_s, es, 2 * es) &&
+                     rows_aligned(x, prm.x_s, es, 2 * es) && rows_aligned(out, prm.out_s, es, 2 * es) &&
+                     (!gate_bias || aligned(gate_bias, 8)) && (!initial_state || aligned(initial_state, 8)) &&
+                     (!last_state || aligned(last_state, 8)) && (!checkpoints || aligned(checkpoints, 8));
+    return status_of(dispatch_gated_tiles<false>(prm, bf16, log_decay, vec, dev, sms, stream));
+}
+
+MAMBA_API size_t mamba_gated_scan_bwd_workspace_bytes(const mamba_gated_dims_t* dims, int have_checkpoints) {
+    GatedLayout w;
+    if (check_gated(dims) != MAMBA_OK) return static_cast<size_t>(-1);
+    if (dims->batch * dims->dim == 0 || dims->seqlen == 0) return 0;
+    // the largest phase: alignment is only known at the call
+    return gated_layout(dims, true, have_checkpoints == 0, 16 / dtype_bytes(dims->io_dtype) - 1, &w) == MAMBA_OK
+               ? w.total : static_cast<size_t>(-1);
+}
+
+MAMBA_API mamba_status_t mamba_gated_scan_bwd(
+    const void* gate, const void* x, const float* gate_bias, const float* initial_state,
+    const float* checkpoints, const void* dout, const float* dlast_state, void* dgate, void* dx,
+    float* dgate_bias, float* dinitial_state, const mamba_gated_dims_t* dims, cudaStream_t stream) {
+    mamba_status_t st = check_gated(dims);
+    if (st != MAMBA_OK) return st;
+    if (dims->dim == 0) return MAMBA_OK;
+    if (dgate_bias && !aligned(dgate_bias, 4)) return MAMBA_ERR_ALIGN;
+    const size_t bias_bytes = (size_t)dims->dim * sizeof(float);
+    if (dims->batch == 0) return status_of(copy_or_zero(dgate_bias, nullptr, bias_bytes, stream));
+    const bool bld = gated_bld(dims);
+    const int64_t rows = bld ? dims->seqlen : dims->dim, inner = bld ? dims->dim : dims->seqlen;
+    const int es = dtype_bytes(dims->io_dtype);
+    GatedParams prm{};
+    st = gated_common(gate, x, gate_bias, initial_state, dims, &prm);
+    if (st != MAMBA_OK) return st;
+    if (dims->seqlen > 0 && (dout == nullptr || dgate == nullptr || dx == nullptr)) return MAMBA_ERR_INVALID_ARG;
+    if (checkpoints != nullptr && !bld) return MAMBA_ERR_UNSUPPORTED;
+    if ((dout && !aligned(dout, es)) || (dgate && !aligned(dgate, es)) || (dx && !aligned(dx, es)) ||
+        (dlast_state && !aligned(dlast_state, 4)) || (dinitial_state && !aligned(dinitial_state, 4)) ||
+        (checkpoints && !aligned(checkpoints, 4)))
+        return MAMBA_ERR_ALIGN;
+    if (!resolve_strides(dims->out, dims->batch, rows, inner, false, &prm.out_s) ||
+        !resolve_strides(dims->dgate, dims->batch, rows, inner, true, &prm.dgate_s) ||
+        !resolve_strides(dims->dx, dims->batch, rows, inner, true, &prm.dx_s))
+        return MAMBA_ERR_INVALID_ARG;
+    if (dims->seqlen > 0 && (dgate == dx || dgate == gate || dgate == x || dgate == dout || dx == gate || dx == x || dx == dout))
+        return MAMBA_ERR_INVALID_ARG;
+    if (dims->seqlen == 0) {
+        cudaError_t e = copy_or_zero(dgate_bias, nullptr, bias_bytes, stream);
+        if (e == cudaSuccess) e = copy_or_zero(dinitial_state, dlast_state, (size_t)prm.chains * sizeof(float), stream);
+        return status_of(e);
+    }
+    const bool recompute = checkpoints == nullptr;
+    GatedLayout w;
+    st = gated_layout(dims, true, recompute, bld ? 0 : gated_phase_max(gate, prm.gate_s, es), &w);
+    if (st != MAMBA_OK) return st;
+    st = check_workspace(dims->workspace, dims->workspace_bytes, w.total);
+    if (st != MAMBA_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(dims->workspace);
+    gated_apply_layout(w, ws, &prm);
+    prm.dout = dout;
+    prm.dlast = dlast_state;
+    prm.dgate = dgate;
+    prm.dx = dx;
+    prm.dh0 = dinitial_state;
+    prm.bias_partial = dgate_bias != nullptr ? reinterpret_cast<float*>(ws + w.bias) : nullptr;
+    const bool bf16 = dims->io_dtype == MAMBA_BF16, log_decay = dims->log_decay != 0;
+    cudaError_t e;
+    if (!bld) {
+        const int64_t per_cta = w.warps > 1 ? kGatedWarps / w.warps : kGatedWarps;
+        if (prm.chains / per_cta >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
+        prm.chain_states = w.tiles > 1 ? reinterpret_cast<float*>(ws + w.states) : nullptr;
+        e = dispatch_gated_rows<true>(prm, w, bf16, log_decay, stream);
+        if (e == cudaSuccess && dgate_bias != nullptr)
+            e = launch_column_sum(prm.bias_partial, dims->batch, dims->dim, dims->dim, dgate_bias, nullptr, stream);
+        return status_of(e);
+    }
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
+    if (sms <= 0) return MAMBA_ERR_CUDA;
+    if (w.zeroed && cudaMemsetAsync(ws, 0, w.zeroed, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
+    const bool vec_in = dims->dim % 2 == 0 && rows_aligned(gate, prm.gate_s, es, 2 * es) &&
+                        rows_aligned(x, prm.x_s, es, 2 * es) && (!gate_bias || aligned(gate_bias, 8)) &&
+                        (!initial_state || aligned(initial_state, 8));
+    if (recompute) {                    // the forward's states, no outputs
+        GatedParams fwd = prm;
+        fwd.out = nullptr;
+        fwd.last = nullptr;
+        fwd.enter = reinterpret_cast<float*>(ws + w.enter);
+        if (w.zeroed) {
+            fwd.ticket = prm.ticket + 1;
+            fwd.flags = reinterpret_cast<unsigned int*>(ws + w.flags2);
+        }
+        e = dispatch_gated_tiles<false>(fwd, bf16, log_decay, vec_in, dev, sms, stream);
+        if (e != cudaSuccess) return MAMBA_ERR_CUDA;
+        prm.enter = fwd.enter;
+    } else {
+        prm.enter = const_cast<float*>(checkpoints);
+    }
+    prm.carry = reinterpret_cast<float*>(ws + w.carry);
+    const bool vec = vec_in && rows_aligned(dout, prm.out_s, es, 2 * es) &&
+                     rows_aligned(dgate, prm.dgate_s, es, 2 * es) && rows_aligned(dx, prm.dx_s, es, 2 * es) &&
+                     (!dlast_state || aligned(dlast_state, 8)) && (!dinitial_state || aligned(dinitial_state, 8)) &&
+                     (!checkpoints || aligned(checkpoints, 8));
+    e = dispatch_gated_tiles<true>(prm, bf16, log_decay, vec, dev, sms, stream);
+    if (e == cudaSuccess && dgate_bias != nullptr)
+        e = launch_column_sum(prm.bias_partial, dims->batch * w.tiles, dims->dim, dims->dim, dgate_bias, nullptr, stream);
+    return status_of(e);
+}
+
+MAMBA_API mamba_status_t mamba_gated_state_update(float* state, const void* gate, const void* x,
+                                                  const float* gate_bias, void* out,
+                                                  const mamba_gated_dims_t* dims, cudaStream_t stream) {
+    if (dims == nullptr || dims->batch < 0 || dims->dim < 0 || dims->batch >= kLimit31 || dims->dim >= kLimit31)
+        return MAMBA_ERR_INVALID_ARG;
+    if (!dtype_ok(dims->io_dtype)) return MAMBA_ERR_UNSUPPORTED;
+    if (dims->batch * dims->dim == 0) return MAMBA_OK;
+    if (state == nullptr || gate == nullptr || x == nullptr || out == nullptr) return MAMBA_ERR_INVALID_ARG;
+    const int es = dtype_bytes(dims->io_dtype);
+    if (!aligned(state, 4) || !aligned(gate, es) || !aligned(x, es) || !aligned(out, es) || (gate_bias && !aligned(gate_bias, 4)))
+        return MAMBA_ERR_ALIGN;
+    GatedUpdateParams prm{};
+    const int64_t strides[3] = {dims->gate.batch, dims->x.batch, dims->out.batch};
+    for (const int64_t s : strides)
+        if (s < 0 || (s != 0 && (s < dims->dim || s > ((int64_t)1 << 50) / dims->batch))) return MAMBA_ERR_INVALID_ARG;
+    prm.gate_stride = strides[0] ? strides[0] : dims->dim;
+    prm.x_stride = strides[1] ? strides[1] : dims->dim;
+    prm.out_stride = strides[2] ? strides[2] : dims->dim;
+    if ((out == x && prm.out_stride != prm.x_stride) || (out == gate && prm.out_stride != prm.gate_stride) || out == state)
+        return MAMBA_ERR_INVALID_ARG;
+    prm.state = state;
+    prm.gate = gate;
+    prm.x = x;
+    prm.bias = gate_bias;
+    prm.out = out;
+    prm.batch = dims->batch;
+    prm.dim = dims->dim;
+    auto on16 = [es](const void* p, int64_t stride) { return aligned(p, 16) && (stride * es) % 16 == 0; };
+    const bool vec = dims->dim % 8 == 0 && aligned(state, 16) && on16(gate, prm.gate_stride) &&
+                     on16(x, prm.x_stride) && on16(out, prm.out_stride) && (!gate_bias || aligned(gate_bias, 16));
+    prm.per_row = vec ? dims->dim / 8 : dims->dim;
+    const int64_t ctas = (prm.per_row * dims->batch + kGatedUpdateThreads - 1) / kGatedUpdateThreads;
+    if (ctas >= kLimit31) return MAMBA_ERR_UNSUPPORTED;
+    const unsigned grid = (unsigned)ctas;
+#define MAMBA_GATED_UPDATE(T, LOG)                                                                   \
+    if (vec) gated_update_kernel<T, LOG, 8><<<grid, kGatedUpdateThreads, 0, stream>>>(prm);          \
+    else gated_update_kernel<T, LOG, 1><<<grid, kGatedUpdateThreads, 0, stream>>>(prm)
+    if (dims->io_dtype == MAMBA_BF16) {
+        if (dims->log_decay) { MAMBA_GATED_UPDATE(__nv_bfloat16, true); }
+        else { MAMBA_GATED_UPDATE(__nv_bfloat16, false); }
+    } else {
+        if (dims->log_decay) { MAMBA_GATED_UPDATE(float, true); }
+        else { MAMBA_GATED_UPDATE(float, false); }
+    }
+#undef MAMBA_GATED_UPDATE
+    return status_of(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -1,0 +1,46 @@
+// Host-side helpers shared by the library's translation units.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "mamba_ssm.h"
+#include "ssm_device.cuh"
+
+namespace mamba {
+
+// Read and clear the device status word of block_ops.cu (device synchronised).
+bool block_ops_take_status(int* code);
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+inline int dtype_bytes(int32_t dt) { return dt == MAMBA_BF16 ? 2 : 4; }
+inline bool dtype_ok(int32_t dt) { return dt == MAMBA_F32 || dt == MAMBA_BF16; }
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// SM count of the current device, cached per device.
+inline int current_sm_count(int* device_out) {
+    static int cached[kMaxDevices] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    if (device_out) *device_out = dev;
+    if (dev >= 0 && dev < kMaxDevices && cached[dev] > 0) return cached[dev];
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+    if (dev >= 0 && dev < kMaxDevices) cached[dev] = sms;
+    return sms;
+}
+
+// Read and clear this translation unit's device status word.
+inline bool take_device_status(int* code) {
+    const int zero = 0;
+    return cudaMemcpyFromSymbol(code, g_device_status, sizeof(int)) == cudaSuccess &&
+           cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) == cudaSuccess;
+}
+
+}  // namespace
+}  // namespace mamba

@@ -1,6 +1,7 @@
 // C ABI of the selective-SSM library: argument validation, planning, TMA
-// descriptor set-up and kernel dispatch.  One translation unit holds every
-// kernel so that device globals need no separate device link.
+// descriptor set-up and kernel dispatch of the scans, the state update, the
+// convolution and the Mamba-2 layer.  block_ops.cu holds the layer norm, the
+// gated recurrence and the convolution's backward.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -8,6 +9,7 @@
 #include <mutex>
 
 #include "mamba_ssm.h"
+#include "host_util.cuh"
 #include "selective_scan.cuh"
 #include "state_update.cuh"
 #include "conv1d.cuh"
@@ -19,13 +21,6 @@
 namespace mamba {
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-
-int dtype_bytes(int32_t dt) { return dt == MAMBA_BF16 ? 2 : 4; }
-bool dtype_ok(int32_t dt) { return dt == MAMBA_F32 || dt == MAMBA_BF16; }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 mamba_status_t check_dims(const mamba_dims_t* dims, bool scan) {
     if (dims == nullptr) return MAMBA_ERR_INVALID_ARG;
@@ -40,19 +35,6 @@ mamba_status_t check_dims(const mamba_dims_t* dims, bool scan) {
     if (dims->batch >= lim || dims->dim >= lim || (scan && dims->seqlen >= lim))
         return MAMBA_ERR_INVALID_ARG;
     return MAMBA_OK;
-}
-
-// SM count of the current device, cached per device.
-int current_sm_count(int* device_out) {
-    static int cached[kMaxDevices] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-    if (device_out) *device_out = dev;
-    if (dev >= 0 && dev < kMaxDevices && cached[dev] > 0) return cached[dev];
-    int sms = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-    if (dev >= 0 && dev < kMaxDevices) cached[dev] = sms;
-    return sms;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -1575,13 +1557,9 @@ MAMBA_API mamba_status_t mamba_selective_scan_bwd(
 
 MAMBA_API mamba_status_t mamba_device_status(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return MAMBA_ERR_CUDA;
-    int code = 0;
-    if (cudaMemcpyFromSymbol(&code, g_device_status, sizeof(int)) != cudaSuccess)
-        return MAMBA_ERR_CUDA;
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) != cudaSuccess)
-        return MAMBA_ERR_CUDA;
-    return static_cast<mamba_status_t>(code);
+    int here = 0, block = 0;
+    if (!take_device_status(&here) || !block_ops_take_status(&block)) return MAMBA_ERR_CUDA;
+    return static_cast<mamba_status_t>(here != 0 ? here : block);
 }
 
 MAMBA_API const char* mamba_status_string(mamba_status_t status) {

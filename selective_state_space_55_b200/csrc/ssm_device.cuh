@@ -19,9 +19,9 @@ constexpr float kLog2e = 1.4426950408889634f;   // log2(e)
 constexpr float kLn2 = 0.6931471805599453f;     // ln(2)
 constexpr int kNPad = 16;                        // compiled state size (smaller N is zero-padded)
 
-// First device-side error since the host last read it (0 = none).  The
-// library is compiled as one translation unit, which owns this definition.
-__device__ int g_device_status = 0;
+// First device-side error since the host last read it (0 = none).  Each
+// translation unit has its own word; mamba_device_status reads them all.
+static __device__ int g_device_status = 0;
 
 __device__ __forceinline__ void record_device_error(int code) {
     atomicCAS(&g_device_status, 0, code);

@@ -32,6 +32,7 @@ MAMBA_FLAG_PDL = 0x10
 MAMBA_FLAG_LAYOUT_BLD = 0x20
 MAMBA_FLAG_ONE_LANE_PER_CHANNEL = 0x40
 MAMBA_FLAG_PARALLEL_ONE_LAUNCH = 0x80
+MAMBA_GATED_CHECKPOINT_STEPS = 64
 
 _DTYPE_CODE = {torch.float32: MAMBA_F32, torch.bfloat16: MAMBA_BF16}
 
@@ -51,6 +52,31 @@ class SsdDims(ctypes.Structure):
         ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
         ("headdim", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("dstate", ctypes.c_int64),
         ("io_dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32),
+    ]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("row", ctypes.c_int64)]
+
+
+class GatedDims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("dim", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+        ("io_dtype", ctypes.c_int32), ("log_decay", ctypes.c_int32), ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("seqlens", ctypes.c_void_p),
+        ("gate", Strides), ("x", Strides), ("out", Strides), ("dgate", Strides), ("dx", Strides),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32), ("rms", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64), ("residual_out_stride", ctypes.c_int64),
+        ("dx_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -117,6 +143,27 @@ def library(path: Path | str | None = None) -> ctypes.CDLL:
     lib.mamba_selective_state_update.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, dims_p, vp]
     lib.mamba_ssd_chunk_scan_fwd.restype = i32
     lib.mamba_ssd_chunk_scan_fwd.argtypes = [vp] * 11 + [ctypes.POINTER(SsdDims), vp]
+    gated_p, norm_p = ctypes.POINTER(GatedDims), ctypes.POINTER(NormDims)
+    lib.mamba_causal_conv1d_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.mamba_causal_conv1d_bwd_workspace_bytes.argtypes = [dims_p, i32]
+    lib.mamba_causal_conv1d_bwd.restype = i32
+    lib.mamba_causal_conv1d_bwd.argtypes = [vp] * 4 + [i32, i32] + [vp] * 6 + [dims_p, vp]
+    lib.mamba_gated_scan_workspace_bytes.restype = ctypes.c_size_t
+    lib.mamba_gated_scan_workspace_bytes.argtypes = [gated_p]
+    lib.mamba_gated_scan_fwd.restype = i32
+    lib.mamba_gated_scan_fwd.argtypes = [vp] * 7 + [gated_p, vp]
+    lib.mamba_gated_scan_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.mamba_gated_scan_bwd_workspace_bytes.argtypes = [gated_p, i32]
+    lib.mamba_gated_scan_bwd.restype = i32
+    lib.mamba_gated_scan_bwd.argtypes = [vp] * 11 + [gated_p, vp]
+    lib.mamba_gated_state_update.restype = i32
+    lib.mamba_gated_state_update.argtypes = [vp] * 5 + [gated_p, vp]
+    lib.mamba_layer_norm_fwd.restype = i32
+    lib.mamba_layer_norm_fwd.argtypes = [vp] * 8 + [norm_p, vp]
+    lib.mamba_layer_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.mamba_layer_norm_bwd_workspace_bytes.argtypes = [norm_p]
+    lib.mamba_layer_norm_bwd.restype = i32
+    lib.mamba_layer_norm_bwd.argtypes = [vp] * 10 + [norm_p, vp]
     lib.mamba_device_status.restype = i32
     lib.mamba_device_status.argtypes = []
     lib.mamba_status_string.restype = ctypes.c_char_p
@@ -551,6 +598,429 @@ def ssd_chunk_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     if return_final_state or final_state is not None:
         return out, final_state
     return out
+
+
+# ---------------------------------------------------------------------------
+# Operators around a recurrent block's projections.  These run on the device of
+# their first tensor, whichever device is current, and every other tensor has
+# to be there too.  Outputs and workspaces are allocated on the stream that the
+# kernels run on.
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_F32 = (torch.float32,)
+
+
+def _on(device, stream, call):
+    """``call(stream handle)`` with ``device`` and ``stream`` (default: the
+    device's current stream) current."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream().cuda_stream)
+    if stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _check(name, t, dtypes, shape, device):
+    """Packed tensor of the given dtype and shape on ``device`` (None passes)."""
+    if t is None:
+        return
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_rows(name, t, dtypes, shape, device):
+    """A (rows, dim) view whose rows are contiguous; returns the distance of rows."""
+    if t is None:
+        return 0
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.is_contiguous():
+        return 0
+    dim = shape[-1]
+    if dim > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # leading dimensions of size 1 say nothing; the others have to form one run of rows
+    dims = [(n, st) for n, st in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    if t.numel() == 0 or not dims:
+        return 0
+    for (_, outer), (n, inner) in zip(dims, dims[1:]):
+        if outer != n * inner:
+            raise ValueError(f"{name}: rows are not evenly spaced (strides {t.stride()})")
+    if dims[-1][1] < dim:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return dims[-1][1]
+
+
+def _check_strided(name, t, dtypes, shape, device):
+    """A 3-dimensional tensor with a contiguous last dimension; returns its Strides."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.is_contiguous():
+        return Strides(0, 0)
+    n = shape[-1]
+    sb, sr, si = t.stride()
+    if n > 1 and si != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if (shape[0] > 1 and sb < n) or (shape[1] > 1 and sr < n):
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    # distances along dimensions of size 1 are arbitrary: give them a harmless value
+    return Strides(sb if shape[0] > 1 else max(n, 1), sr if shape[1] > 1 else max(n, 1))
+
+
+def _raise_on(name, rc):
+    if rc != MAMBA_OK:
+        raise MambaError(name, rc)
+
+
+def _workspace(workspace, need, device, name):
+    """The caller's workspace, or a new one of ``need`` bytes; None when nothing is needed."""
+    if need == ctypes.c_size_t(-1).value:
+        raise MambaError(name, -1)
+    if workspace is not None:
+        _check("workspace", workspace, (torch.uint8,), workspace.shape, device)
+        return workspace
+    return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+
+
+def _set_workspace(dims, ws):
+    if ws is not None:
+        dims.workspace = ws.data_ptr()
+        dims.workspace_bytes = ws.numel()
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False, out=None,
+                   residual_out=None, return_stats=False, stream=None):
+    """Layer norm with the residual add through ``mamba_layer_norm_fwd``.
+
+    s = x + residual; out = (s - mean) / sqrt(var + eps) * weight + bias over the
+    last dimension (``rms``: mean = 0, the root-mean-square form).  x: (..., dim)
+    fp32 or bf16, rows contiguous and evenly spaced; weight, bias: (dim,) fp32 or
+    None; residual: x's shape, in x's dtype or fp32.  ``residual_out`` receives s
+    (default: a new tensor when ``residual`` is given; it may be ``residual``
+    itself, and ``out`` may be x).  Returns ``out``; with a residual or a
+    residual_out, (out, residual_out); with ``return_stats``, mean (None for
+    ``rms``) and rstd, fp32 in x's leading shape, are appended.
+    """
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    device, io, shape = x.device, x.dtype, x.shape
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dim = shape[-1]
+    rdt = (residual if residual is not None else residual_out if residual_out is not None else x).dtype
+    dims = NormDims(dim=dim, rms=int(bool(rms)), eps=eps)
+    dims.x_stride = _check_rows("x", x, _FLOATS, shape, device)
+    dims.residual_stride = _check_rows("residual", residual, (io, torch.float32), shape, device)
+    _check("weight", weight, _F32, (dim,), device)
+    _check("bias", bias, _F32, (dim,), device)
+    dims.rows = x.numel() // dim if dim else 0
+    dims.io_dtype, dims.residual_dtype = _DTYPE_CODE[io], _DTYPE_CODE[rdt]
+
+    def call(handle):
+        y = torch.empty(shape, dtype=io, device=device) if out is None else out
+        s = residual_out
+        if s is None and residual is not None:
+            s = torch.empty(shape, dtype=rdt, device=device)
+        dims.out_stride = _check_rows("out", y, (io,), shape, device)
+        dims.residual_out_stride = _check_rows("residual_out", s, (rdt,), shape, device)
+        mean = rstd = None
+        if return_stats:
+            rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+            mean = None if rms else torch.empty(shape[:-1], dtype=torch.float32, device=device)
+        rc = library().mamba_layer_norm_fwd(
+            x.data_ptr(), _address(residual), _address(weight), _address(bias), y.data_ptr(),
+            _address(s), _address(mean), _address(rstd), ctypes.byref(dims), handle)
+        _raise_on("mamba_layer_norm_fwd", rc)
+        r = (y,) if s is None else (y, s)
+        if return_stats:
+            r += (mean, rstd)
+        return r if len(r) > 1 else y
+
+    return _on(device, stream, call)
+
+
+def layer_norm_bwd(dout, s, rstd, mean=None, weight=None, bias=None, dresidual_out=None, rms=False,
+                   dx=None, dresidual=None, workspace=None, stream=None):
+    """Gradients of the layer norm through ``mamba_layer_norm_bwd``.
+
+    s: the forward's sum (its residual_out, or x without a residual), dout: the
+    gradient of its out, x's dtype; s, dresidual_out (the gradient that reaches
+    residual_out from later blocks, or None): dout's shape, in dout's dtype or
+    fp32 (both the same).  mean, rstd: the forward's statistics (``rms``: mean is
+    not read).  Returns a dict: dx (dout's dtype; the gradient of x and of a
+    residual of the same dtype), dresidual (s's dtype) when that differs or a
+    buffer is given, dweight and dbias (fp32) for the weight and bias given.
+    """
+    device, io, shape = dout.device, dout.dtype, dout.shape
+    if not dout.is_cuda:
+        raise ValueError("dout must be a CUDA tensor")
+    if dout.dim() < 1:
+        raise ValueError("dout must have at least one dimension")
+    dim = shape[-1]
+    rdt = s.dtype
+    dims = NormDims(dim=dim, rms=int(bool(rms)))
+    dims.out_stride = _check_rows("dout", dout, _FLOATS, shape, device)
+    dims.x_stride = _check_rows("s", s, (io, torch.float32), shape, device)
+    dims.residual_out_stride = _check_rows("dresidual_out", dresidual_out, (rdt,), shape, device)
+    lead = shape[:-1]
+    _check("rstd", rstd, _F32, lead, device)
+    if not rms:
+        if mean is None:
+            raise ValueError("mean is needed (unless rms)")
+        _check("mean", mean, _F32, lead, device)
+    _check("weight", weight, _F32, (dim,), device)
+    _check("bias", bias, _F32, (dim,), device)
+    dims.rows = dout.numel() // dim if dim else 0
+    dims.io_dtype, dims.residual_dtype = _DTYPE_CODE[io], _DTYPE_CODE[rdt]
+
+    def call(handle):
+        g = {"dx": torch.empty(shape, dtype=io, device=device) if dx is None else dx}
+        if dresidual is not None:
+            g["dresidual"] = dresidual
+        elif rdt != io:
+            g["dresidual"] = torch.empty(shape, dtype=rdt, device=device)
+        dims.dx_stride = _check_rows("dx", g["dx"], (io,), shape, device)
+        dims.residual_stride = _check_rows("dresidual", g.get("dresidual"), (rdt,), shape, device)
+        if weight is not None:
+            g["dweight"] = torch.empty((dim,), dtype=torch.float32, device=device)
+        if bias is not None:
+            g["dbias"] = torch.empty((dim,), dtype=torch.float32, device=device)
+        ws = None
+        if weight is not None or bias is not None:
+            need = library().mamba_layer_norm_bwd_workspace_bytes(ctypes.byref(dims))
+            ws = _workspace(workspace, need, device, "mamba_layer_norm_bwd_workspace_bytes")
+            _set_workspace(dims, ws)
+        rc = library().mamba_layer_norm_bwd(
+            s.data_ptr(), _address(weight), None if rms else mean.data_ptr(), rstd.data_ptr(),
+            dout.data_ptr(), _address(dresidual_out), g["dx"].data_ptr(),
+            _address(g.get("dresidual")), _address(g.get("dweight")), _address(g.get("dbias")),
+            ctypes.byref(dims), handle)
+        _raise_on("mamba_layer_norm_bwd", rc)
+        return g
+
+    return _on(device, stream, call)
+
+
+def _gated_sizes(gate, layout):
+    if layout not in ("bdl", "bld"):
+        raise ValueError(f"layout must be 'bdl' or 'bld', not {layout!r}")
+    if gate.dim() != 3:
+        raise ValueError(f"gate must have 3 dimensions, got shape {tuple(gate.shape)}")
+    if not gate.is_cuda:
+        raise ValueError("gate must be a CUDA tensor")
+    if layout == "bld":
+        batch, L, dim = gate.shape
+        return batch, dim, L, MAMBA_FLAG_LAYOUT_BLD
+    batch, dim, L = gate.shape
+    return batch, dim, L, 0
+
+
+def _checkpoint_shape(batch, dim, L):
+    return (batch, -(-L // MAMBA_GATED_CHECKPOINT_STEPS), dim)
+
+
+def gated_scan_fwd(gate, x, gate_bias=None, initial_state=None, seqlens=None, log_decay=False,
+                   out=None, last_state=None, return_last_state=False, checkpoints=None,
+                   return_checkpoints=False, workspace=None, stream=None, layout="bdl", flags=0):
+    """Gated linear recurrence through ``mamba_gated_scan_fwd``.
+
+    With f = gate + gate_bias: h_t = (1 - g_t) h_{t-1} + g_t x_t, g = sigmoid(f), or,
+    with ``log_decay``, h_t = exp(f_t) h_{t-1} + x_t.  gate, x: (batch, dim, L) fp32
+    or bf16 (one dtype), or (batch, L, dim) with ``layout="bld"``; the last dimension
+    contiguous, rows at any distance.  gate_bias: (dim,) fp32; initial_state:
+    (batch, dim) fp32; seqlens: (batch,) int32 lengths of a padded batch (outputs
+    beyond them are 0).  Returns out (gate's shape and dtype), followed by the last
+    state (batch, dim) fp32 and, layout "bld" only, the states entering each block
+    of 64 steps, (batch, ceil(L / 64), dim) fp32, when asked for or given.
+    """
+    batch, dim, L, lay = _gated_sizes(gate, layout)
+    device, io, shape = gate.device, gate.dtype, gate.shape
+    dims = GatedDims(batch=batch, dim=dim, seqlen=L, log_decay=int(bool(log_decay)), flags=flags | lay)
+    dims.gate = _check_strided("gate", gate, _FLOATS, shape, device)
+    dims.x = _check_strided("x", x, (io,), shape, device)
+    dims.io_dtype = _DTYPE_CODE[io]
+    _check("gate_bias", gate_bias, _F32, (dim,), device)
+    _check("initial_state", initial_state, _F32, (batch, dim), device)
+    _check("seqlens", seqlens, (torch.int32,), (batch,), device)
+    dims.seqlens = _address(seqlens)
+    want_ck = return_checkpoints or checkpoints is not None
+    if want_ck and layout != "bld":
+        raise ValueError("checkpoints are for layout 'bld'")
+
+    def call(handle):
+        y = torch.empty(shape, dtype=io, device=device) if out is None else out
+        dims.out = _check_strided("out", y, (io,), shape, device)
+        last, ck = last_state, checkpoints
+        if last is None and return_last_state:
+            last = torch.empty((batch, dim), dtype=torch.float32, device=device)
+        _check("last_state", last, _F32, (batch, dim), device)
+        if want_ck:
+            cs = _checkpoint_shape(batch, dim, L)
+            if ck is None:
+                ck = torch.empty(cs, dtype=torch.float32, device=device)
+            _check("checkpoints", ck, _F32, cs, device)
+        need = library().mamba_gated_scan_workspace_bytes(ctypes.byref(dims))
+        ws = _workspace(workspace, need, device, "mamba_gated_scan_workspace_bytes")
+        _set_workspace(dims, ws)
+        rc = library().mamba_gated_scan_fwd(
+            gate.data_ptr(), x.data_ptr(), _address(gate_bias), _address(initial_state),
+            y.data_ptr(), _address(last), _address(ck), ctypes.byref(dims), handle)
+        _raise_on("mamba_gated_scan_fwd", rc)
+        r = (y,)
+        if last is not None:
+            r += (last,)
+        if want_ck:
+            r += (ck,)
+        return r if len(r) > 1 else y
+
+    return _on(device, stream, call)
+
+
+def gated_scan_bwd(gate, x, dout, gate_bias=None, initial_state=None, seqlens=None,
+                   dlast_state=None, checkpoints=None, log_decay=False, dgate=None, dx=None,
+                   workspace=None, stream=None, layout="bdl", flags=0):
+    """Gradients of the gated recurrence through ``mamba_gated_scan_bwd``.
+
+    The forward's inputs, dout (gate's shape and dtype), dlast_state (batch, dim)
+    fp32 or None, and, layout "bld" only, the forward's ``checkpoints`` (without
+    them the states are recomputed).  Returns a dict: dgate, dx (buffers may be
+    passed, for instance halves of one tensor), dgate_bias and dinitial_state
+    (fp32) for the optional inputs given.
+    """
+    batch, dim, L, lay = _gated_sizes(gate, layout)
+    device, io, shape = gate.device, gate.dtype, gate.shape
+    dims = GatedDims(batch=batch, dim=dim, seqlen=L, log_decay=int(bool(log_decay)), flags=flags | lay)
+    dims.gate = _check_strided("gate", gate, _FLOATS, shape, device)
+    dims.x = _check_strided("x", x, (io,), shape, device)
+    dims.out = _check_strided("dout", dout, (io,), shape, device)
+    dims.io_dtype = _DTYPE_CODE[io]
+    _check("gate_bias", gate_bias, _F32, (dim,), device)
+    _check("initial_state", initial_state, _F32, (batch, dim), device)
+    _check("dlast_state", dlast_state, _F32, (batch, dim), device)
+    _check("seqlens", seqlens, (torch.int32,), (batch,), device)
+    dims.seqlens = _address(seqlens)
+    if checkpoints is not None:
+        if layout != "bld":
+            raise ValueError("checkpoints are for layout 'bld'")
+        _check("checkpoints", checkpoints, _F32, _checkpoint_shape(batch, dim, L), device)
+
+    def call(handle):
+        g = {"dgate": torch.empty(shape, dtype=io, device=device) if dgate is None else dgate,
+             "dx": torch.empty(shape, dtype=io, device=device) if dx is None else dx}
+        dims.dgate = _check_strided("dgate", g["dgate"], (io,), shape, device)
+        dims.dx = _check_strided("dx", g["dx"], (io,), shape, device)
+        if gate_bias is not None:
+            g["dgate_bias"] = torch.empty((dim,), dtype=torch.float32, device=device)
+        if initial_state is not None:
+            g["dinitial_state"] = torch.empty((batch, dim), dtype=torch.float32, device=device)
+        need = library().mamba_gated_scan_bwd_workspace_bytes(ctypes.byref(dims),
+                                                              int(checkpoints is not None))
+        ws = _workspace(workspace, need, device, "mamba_gated_scan_bwd_workspace_bytes")
+        _set_workspace(dims, ws)
+        rc = library().mamba_gated_scan_bwd(
+            gate.data_ptr(), x.data_ptr(), _address(gate_bias), _address(initial_state),
+            _address(checkpoints), dout.data_ptr(), _address(dlast_state), g["dgate"].data_ptr(),
+            g["dx"].data_ptr(), _address(g.get("dgate_bias")), _address(g.get("dinitial_state")),
+            ctypes.byref(dims), handle)
+        _raise_on("mamba_gated_scan_bwd", rc)
+        return g
+
+    return _on(device, stream, call)
+
+
+def gated_state_update(state, gate, x, gate_bias=None, log_decay=False, out=None, stream=None):
+    """One token of the gated recurrence through ``mamba_gated_state_update``;
+    ``state`` (batch, dim) fp32 is updated in place.  gate, x: (batch, dim) fp32 or
+    bf16, rows contiguous.  Returns ``out``, the new state in x's dtype."""
+    if state.dim() != 2:
+        raise ValueError(f"state must have 2 dimensions, got shape {tuple(state.shape)}")
+    if not state.is_cuda:
+        raise ValueError("state must be a CUDA tensor")
+    device, io, shape = state.device, x.dtype, state.shape
+    dims = GatedDims(batch=shape[0], dim=shape[1], log_decay=int(bool(log_decay)))
+    _check("state", state, _F32, shape, device)
+    dims.x.batch = _check_rows("x", x, _FLOATS, shape, device)
+    dims.gate.batch = _check_rows("gate", gate, (io,), shape, device)
+    _check("gate_bias", gate_bias, _F32, (shape[1],), device)
+    dims.io_dtype = _DTYPE_CODE[io]
+
+    def call(handle):
+        y = torch.empty(shape, dtype=io, device=device) if out is None else out
+        dims.out.batch = _check_rows("out", y, (io,), shape, device)
+        rc = library().mamba_gated_state_update(
+            state.data_ptr(), gate.data_ptr(), x.data_ptr(), _address(gate_bias), y.data_ptr(),
+            ctypes.byref(dims), handle)
+        _raise_on("mamba_gated_state_update", rc)
+        return y
+
+    return _on(device, stream, call)
+
+
+def causal_conv1d_bwd(x, weight, dout, bias=None, initial_conv_state=None, dfinal_conv_state=None,
+                      silu=True, workspace=None, stream=None):
+    """Gradients of the short causal convolution through ``mamba_causal_conv1d_bwd``.
+
+    The inputs of ``causal_conv1d_fwd``, dout (x's shape and dtype) and
+    dfinal_conv_state (batch, dim, W) in x's dtype or None.  Returns a dict: dx
+    (x's dtype), dweight (fp32), and dbias (fp32) and dinitial_conv_state (x's
+    dtype) for the optional inputs given.
+    """
+    if x.dim() != 3 or weight.dim() != 2:
+        raise ValueError("x must be (batch, dim, L) and weight (dim, W)")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    batch, dim, L = x.shape
+    W = weight.shape[1]
+    device, io, shape = x.device, x.dtype, x.shape
+    _check("x", x, _FLOATS, shape, device)
+    _check("dout", dout, (io,), shape, device)
+    _check("weight", weight, _F32, (dim, W), device)
+    _check("bias", bias, _F32, (dim,), device)
+    _check("initial_conv_state", initial_conv_state, (io,), (batch, dim, W), device)
+    _check("dfinal_conv_state", dfinal_conv_state, (io,), (batch, dim, W), device)
+    dims = _conv_dims(batch, dim, L, io)
+
+    def call(handle):
+        g = {"dx": torch.empty(shape, dtype=io, device=device),
+             "dweight": torch.empty((dim, W), dtype=torch.float32, device=device)}
+        if bias is not None:
+            g["dbias"] = torch.empty((dim,), dtype=torch.float32, device=device)
+        if initial_conv_state is not None:
+            g["dinitial_conv_state"] = torch.empty((batch, dim, W), dtype=io, device=device)
+        need = library().mamba_causal_conv1d_bwd_workspace_bytes(ctypes.byref(dims), W)
+        ws = _workspace(workspace, need, device, "mamba_causal_conv1d_bwd_workspace_bytes")
+        _set_workspace(dims, ws)
+        rc = library().mamba_causal_conv1d_bwd(
+            x.data_ptr(), weight.data_ptr(), _address(bias), _address(initial_conv_state), W,
+            int(bool(silu)), dout.data_ptr(), _address(dfinal_conv_state), g["dx"].data_ptr(),
+            g["dweight"].data_ptr(), _address(g.get("dbias")),
+            _address(g.get("dinitial_conv_state")), ctypes.byref(dims), handle)
+        _raise_on("mamba_causal_conv1d_bwd", rc)
+        return g
+
+    return _on(device, stream, call)
 
 
 def device_status() -> int:

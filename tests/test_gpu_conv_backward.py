@@ -1,0 +1,125 @@
+"""Backward of the short causal convolution against its 64-bit form."""
+import pytest
+import torch
+
+import block_reference as ref
+from block_reference import assert_close
+from selective_state_space_55_b200 import ops
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def make(batch, dim, L, W, dtype, seed, bias=True, state=True):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    randn = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    return dict(x=randn(batch, dim, L).to(dtype), weight=randn(dim, W), dout=randn(batch, dim, L).to(dtype),
+                bias=randn(dim) if bias else None,
+                initial_conv_state=randn(batch, dim, W).to(dtype) if state else None,
+                dfinal_conv_state=randn(batch, dim, W).to(dtype) if state else None)
+
+
+def check(v, silu=True):
+    want = ref.conv_bwd(**v, silu=silu)
+    g = ops.causal_conv1d_bwd(**v, silu=silu)
+    assert ("dbias" in g) == (v["bias"] is not None)
+    assert ("dinitial_conv_state" in g) == (v["initial_conv_state"] is not None)
+    for k in g:
+        assert_close(k, g[k], *want[k])
+    return g
+
+
+@pytest.mark.parametrize("L", [1, 2, 3, 4, 7, 8, 9, 255, 256, 257, 333, 1001])
+@pytest.mark.parametrize("W", [1, 2, 3, 4])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_lengths_and_widths(dtype, W, L):
+    check(make(3, 37, L, W, dtype, seed=10 * L + W))
+
+
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("state", [True, False])
+@pytest.mark.parametrize("silu", [True, False])
+def test_options(silu, state, bias):
+    check(make(2, 50, 300, 4, BF, seed=1, bias=bias, state=state), silu=silu)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("L", [40000, 39999])
+def test_long_rows_are_cut_into_stretches(L, dtype):
+    """Few chains: stretches of a row meet at tile borders, aligned or shifted."""
+    check(make(2, 3, L, 4, dtype, seed=2))
+
+
+def test_many_chains():
+    check(make(4, 3000, 96, 4, BF, seed=3))
+
+
+def test_empty_sequence():
+    v = make(2, 6, 0, 4, F32, seed=4)
+    g = check(v)
+    assert torch.equal(g["dinitial_conv_state"], v["dfinal_conv_state"])
+    assert (g["dweight"] == 0).all()
+
+
+def test_empty_batch():
+    v = make(0, 6, 9, 4, F32, seed=5)
+    g = ops.causal_conv1d_bwd(**v)
+    assert (g["dweight"] == 0).all() and (g["dbias"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_shifted_buffers(dtype):
+    """Each tensor starts at its own element offset."""
+    v = make(2, 9, 530, 4, dtype, seed=6)
+    for i, k in enumerate(("x", "dout", "initial_conv_state", "dfinal_conv_state", "weight", "bias")):
+        buf = torch.empty(v[k].numel() + i + 1, dtype=v[k].dtype, device=DEV)
+        w = buf[i + 1:].view(v[k].shape)
+        w.copy_(v[k])
+        v[k] = w
+    check(v)
+
+
+def test_forward_then_backward():
+    """The gradient of the forward kernel's own result, by 64-bit differences of its formula."""
+    v = make(1, 2, 6, 3, F32, seed=7)
+    want = ref.conv_bwd(**v)
+    x, w, b = (v[k].double().cpu() for k in ("x", "weight", "bias"))
+    init, dy, df = (v[k].double().cpu() for k in ("initial_conv_state", "dout", "dfinal_conv_state"))
+
+    def loss(x, w, b, init):
+        seq = torch.cat([init, x], 2)
+        pre = b[:, None] + sum(w[:, k, None] * seq[:, :, 1 + k:7 + k] for k in range(3))
+        return (pre * torch.sigmoid(pre) * dy).sum() + (seq[:, :, 6:] * df).sum()
+
+    for k, name in enumerate(("dx", "dweight", "dbias", "dinitial_conv_state")):
+        args = [x, w, b, init]
+        for i in range(args[k].numel()):
+            e = torch.zeros(args[k].numel(), dtype=torch.float64)
+            e[i] = 1e-6
+            hi, lo = list(args), list(args)
+            hi[k] = args[k] + e.view(args[k].shape)
+            lo[k] = args[k] - e.view(args[k].shape)
+            d = (loss(*hi) - loss(*lo)) / 2e-6
+            assert abs(d - want[name][0].flatten()[i]) <= 1e-7 * (1 + abs(d))
+    check(v)
+
+
+def test_repeats_bit_for_bit():
+    v = make(3, 200, 2000, 4, BF, seed=8)
+    runs = [ops.causal_conv1d_bwd(**v) for _ in range(3)]
+    for g in runs[1:]:
+        for k in g:
+            assert torch.equal(g[k], runs[0][k])
+
+
+def test_saturated_activation():
+    """pre of +-300: silu' is 1 or 0, never NaN."""
+    v = make(1, 8, 64, 1, F32, seed=9, state=False)
+    v["x"] = v["x"].sign() * 100.0
+    v["weight"].fill_(3.0)
+    v["bias"].zero_()
+    g = check(v)
+    assert torch.isfinite(g["dx"]).all()

@@ -1,0 +1,194 @@
+"""Layer norm with the residual add, forward and backward, against its 64-bit form."""
+import pytest
+import torch
+
+import block_reference as ref
+from block_reference import assert_close
+from selective_state_space_55_b200 import ops
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def make(rows, dim, dtype, res, seed, offset=0.5):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    randn = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    rdt = {"none": None, "same": dtype, "fp32": F32}[res]
+    x = (randn(rows, dim) + offset).to(dtype)
+    return dict(x=x, residual=None if rdt is None else randn(rows, dim).to(rdt),
+                weight=1.0 + 0.2 * randn(dim), bias=0.3 * randn(dim), dout=randn(rows, dim).to(dtype),
+                ds=None if rdt is None else randn(rows, dim).to(rdt))
+
+
+def check(v, rms=False, eps=1e-5, weight=True, bias=True, fwd_kw=None, bwd_kw=None):
+    w, b = v["weight"] if weight else None, v["bias"] if bias else None
+    want = ref.norm_fwd(v["x"], w, b, v["residual"], eps, rms)
+    r = ops.layer_norm_fwd(v["x"], weight=w, bias=b, residual=v["residual"], eps=eps, rms=rms,
+                           return_stats=True, **(fwd_kw or {}))
+    out, mean, rstd = r[0], r[-2], r[-1]
+    s = v["x"] if v["residual"] is None else r[1]
+    assert_close("out", out, *want["out"])
+    assert_close("rstd", rstd, *want["rstd"])
+    if rms:
+        assert mean is None
+    else:
+        assert_close("mean", mean, *want["mean"])
+    if v["residual"] is not None:
+        assert_close("residual_out", s, *want["residual_out"])
+    gw = ref.norm_bwd(v["dout"], s, rstd, mean, w, v["ds"], rms)
+    g = ops.layer_norm_bwd(v["dout"], s, rstd, mean=mean, weight=w, bias=b, dresidual_out=v["ds"],
+                           rms=rms, **(bwd_kw or {}))
+    assert ("dweight" in g) == weight and ("dbias" in g) == bias
+    for k in g:
+        assert_close(k, g[k], *gw[k])
+    return r, g
+
+
+@pytest.mark.parametrize("dim", [1, 7, 8, 31, 64, 100, 255, 256, 257, 500, 512, 513, 520, 768, 1001,
+                                 2560, 4096, 5000, 8192])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rms", [False, True])
+def test_widths(rms, dtype, dim):
+    check(make(5, dim, dtype, "same", seed=dim), rms=rms)
+
+
+@pytest.mark.parametrize("dim", [8193, 8200, 16384, 20001])
+@pytest.mark.parametrize("dtype,res", [(BF, "none"), (BF, "fp32"), (F32, "same")])
+def test_wide_rows(dtype, res, dim):
+    check(make(7, dim, dtype, res, seed=dim))
+
+
+@pytest.mark.parametrize("rows", [1, 2, 9, 147, 1185, 5000])
+@pytest.mark.parametrize("dim", [96, 392, 1024])
+@pytest.mark.parametrize("res", ["none", "same", "fp32"])
+def test_row_counts(res, dim, rows):
+    check(make(rows, dim, BF, res, seed=rows))
+
+
+@pytest.mark.parametrize("weight,bias", [(True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("dim", [130, 640, 9000])
+def test_without_weight_or_bias(dim, weight, bias):
+    check(make(300, dim, BF, "same", seed=1), weight=weight, bias=bias)
+
+
+def test_offset_far_above_the_spread():
+    """Mean 1000, spread 1: the variance keeps its digits (two reductions, not E[s^2] - mean^2)."""
+    check(make(33, 1024, F32, "none", seed=2, offset=1000.0))
+    check(make(33, 384, F32, "none", seed=2, offset=1000.0))
+
+
+@pytest.mark.parametrize("dim", [64, 1024, 8448])
+def test_constant_rows(dim):
+    v = make(4, dim, BF, "none", seed=3)
+    v["x"].fill_(2.0)
+    r, g = check(v)
+    assert torch.equal(r[0].float(), v["bias"].to(BF).float().expand(4, -1))
+
+
+def test_a_nan_row_stays_in_its_row():
+    v = make(20, 512, BF, "none", seed=4)
+    v["x"][7, 3] = float("nan")
+    out = ops.layer_norm_fwd(v["x"], v["weight"], v["bias"])
+    assert out[7].isnan().all() and not out[:7].isnan().any() and not out[8:].isnan().any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [128, 131, 1000, 9001])
+def test_strided_rows_and_shapes(dtype, dim):
+    """Rows as a slice of wider ones, at odd offsets, (batch, L, dim) in front."""
+    v = make(24, dim, dtype, "same", seed=dim)
+    wide = torch.full((24, 2 * dim + 3), 9.0, dtype=dtype, device=DEV)
+    x = wide[:, 1:dim + 1]
+    x.copy_(v["x"])
+    out = torch.full((24, dim + 5), 4.0, dtype=dtype, device=DEV)
+    v["x"] = x
+    check(v, fwd_kw=dict(out=out[:, 2:dim + 2]))
+    assert (out[:, :2] == 4.0).all() and (out[:, dim + 2:] == 4.0).all()
+    y = ops.layer_norm_fwd(x.view(2, 3, 4, dim) if x.is_contiguous() else x.unflatten(0, (2, 3, 4)),
+                           v["weight"], v["bias"], return_stats=True)
+    assert y[0].shape == (2, 3, 4, dim) and y[1].shape == (2, 3, 4)
+    assert_close("out", y[0].view(24, dim), *ref.norm_fwd(x, v["weight"], v["bias"])["out"])
+
+
+@pytest.mark.parametrize("dim", [256, 2560, 9216])
+def test_in_place(dim):
+    v = make(40, dim, BF, "same", seed=5)
+    want = ref.norm_fwd(v["x"], v["weight"], v["bias"], v["residual"])
+    x, res = v["x"].clone(), v["residual"].clone()
+    out, s, mean, rstd = ops.layer_norm_fwd(x, v["weight"], v["bias"], residual=res, out=x,
+                                            residual_out=res, return_stats=True)
+    assert out is x and s is res
+    assert_close("out", x, *want["out"])
+    assert_close("residual_out", res, *want["residual_out"])
+    gw = ref.norm_bwd(v["dout"], s, rstd, mean, v["weight"], v["ds"])
+    dout = v["dout"].clone()
+    g = ops.layer_norm_bwd(dout, s, rstd, mean=mean, weight=v["weight"], bias=v["bias"],
+                           dresidual_out=v["ds"], dx=dout)
+    for k in g:
+        assert_close(k, g[k], *gw[k])
+    ds = v["ds"].clone()
+    g = ops.layer_norm_bwd(v["dout"], s, rstd, mean=mean, weight=v["weight"], bias=v["bias"],
+                           dresidual_out=ds, dx=ds)
+    for k in g:
+        assert_close(k, g[k], *gw[k])
+
+
+def test_first_block_keeps_the_stream_in_fp32():
+    """No residual yet, residual_out in fp32: s = x."""
+    v = make(10, 320, BF, "none", seed=6)
+    s = torch.empty(10, 320, device=DEV)
+    out, s2 = ops.layer_norm_fwd(v["x"], v["weight"], residual_out=s)
+    assert s2 is s and torch.equal(s, v["x"].float())
+
+
+def test_no_rows():
+    e = torch.empty(0, 64, device=DEV)
+    st = torch.empty(0, device=DEV)
+    w = torch.ones(64, device=DEV)
+    assert ops.layer_norm_fwd(e, w).shape == (0, 64)
+    g = ops.layer_norm_bwd(e, e, st, mean=st, weight=w, bias=w)
+    assert (g["dweight"] == 0).all() and (g["dbias"] == 0).all()
+
+
+def test_repeats_bit_for_bit():
+    v = make(3000, 768, BF, "same", seed=7)
+    _, s, mean, rstd = ops.layer_norm_fwd(v["x"], v["weight"], v["bias"], residual=v["residual"], return_stats=True)
+    runs = [ops.layer_norm_bwd(v["dout"], s, rstd, mean=mean, weight=v["weight"], bias=v["bias"]) for _ in range(3)]
+    for g in runs[1:]:
+        for k in g:
+            assert torch.equal(g[k], runs[0][k])
+
+
+def test_gradients_match_differences():
+    v = make(2, 5, F32, "none", seed=8)
+    x, w, b = (v[k].double().cpu() for k in ("x", "weight", "bias"))
+    dy = v["dout"].double().cpu()
+
+    def loss(x, w, b):
+        return (ref.norm_fwd(x, w, b)["out"][0] * dy).sum()
+
+    o = ref.norm_fwd(x, w, b)
+    g = ref.norm_bwd(dy, x, o["rstd"][0], o["mean"][0], w)
+    for k, name in enumerate(("dx", "dweight", "dbias")):
+        args = [x, w, b]
+        for i in range(args[k].numel()):
+            e = torch.zeros(args[k].numel(), dtype=torch.float64)
+            e[i] = 1e-6
+            hi, lo = list(args), list(args)
+            hi[k] = args[k] + e.view(args[k].shape)
+            lo[k] = args[k] - e.view(args[k].shape)
+            d = (loss(*hi) - loss(*lo)) / 2e-6
+            assert abs(d - g[name][0].flatten()[i]) <= 1e-7 * (1 + abs(d))
+    check(v)
+
+
+def test_stream_of_its_own():
+    v = make(64, 512, BF, "same", seed=9)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out, s = ops.layer_norm_fwd(v["x"], v["weight"], v["bias"], residual=v["residual"], stream=st)
+    st.synchronize()
+    assert_close("out", out, *ref.norm_fwd(v["x"], v["weight"], v["bias"], v["residual"])["out"])
