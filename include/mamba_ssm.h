@@ -559,7 +559,7 @@ typedef struct {
     int32_t io_dtype;          /* gate, x, out, dout, dgate, dx */
     int32_t log_decay;
     int32_t flags;             /* MAMBA_FLAG_LAYOUT_BLD; MAMBA_FLAG_TEST_WITHHOLD_HANDOFF (test
-                                * only: in the (batch, seqlen, dim) layout no tile hands its
+                                * only: in the (batch, seqlen, dim) layout no segment hands its
                                 * state on, every wait runs out after some 0.3 s and
                                 * mamba_device_status() reports MAMBA_ERR_TIMEOUT) */
     int32_t reserved;

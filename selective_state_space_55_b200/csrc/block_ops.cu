@@ -160,12 +160,13 @@ mamba_status_t check_gated(const mamba_gated_dims_t* d) {
 bool gated_bld(const mamba_gated_dims_t* d) { return (d->flags & MAMBA_FLAG_LAYOUT_BLD) != 0; }
 
 struct GatedLayout {           // offsets in the workspace, bytes
-    size_t tickets, flags, flags2, zeroed, maps, enter, carry, bias, states, total;
-    int64_t tiles, groups_per_row, groups, items;
-    int warps, width;          // (batch, dim, seqlen): warps per chain, lanes per chain
+    size_t tickets, flags, flags2, zeroed, maps, joins, enter, bias, states, total;
+    int64_t blocks, segments, groups_per_row, groups, items;
+    int64_t tiles;
+    int warps, width;          // (batch, seqlen, dim): blocks per segment; else warps and lanes per chain
 };
 
-// One tile per chain needs no look-back: no tickets, flags or maps.
+// One segment per chain needs no look-back: no tickets, flags or maps.
 mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool recompute, int phase_max,
                             GatedLayout* w) {
     *w = GatedLayout{};
@@ -173,24 +174,23 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
     size_t off = 0;
     auto take = [&off](size_t bytes) { const size_t at = off; off += align256(bytes); return at; };
     if (gated_bld(d)) {
-        w->tiles = (L + kGatedTile - 1) / kGatedTile;
+        w->blocks = (L + kGatedBlock - 1) / kGatedBlock;
+        w->warps = (int)std::min<int64_t>(kGatedWarps, w->blocks);
+        w->segments = (w->blocks + w->warps - 1) / w->warps;
         w->groups_per_row = (d->dim + kGatedChannels - 1) / kGatedChannels;
         w->groups = d->batch * w->groups_per_row;
-        w->items = w->groups * w->tiles;
+        w->items = w->groups * w->segments;
         if (w->items >= kLimit31 / 2) return MAMBA_ERR_UNSUPPORTED;
-        const size_t states = (size_t)d->batch * w->tiles * d->dim * sizeof(float);
-        if (w->tiles > 1) {
+        if (w->segments > 1) {
             w->tickets = take(2 * sizeof(unsigned int));
             w->flags = take((size_t)w->items * sizeof(unsigned int));
             if (backward && recompute) w->flags2 = take((size_t)w->items * sizeof(unsigned int));
             w->zeroed = off;
             w->maps = take((size_t)w->items * 32 * sizeof(float4));
+            w->joins = take((size_t)w->groups * ((w->segments + kGatedJoin - 1) / kGatedJoin) * 32 * sizeof(float2));
         }
-        if ((!backward && w->tiles > 1) || (backward && recompute)) w->enter = take(states);
-        if (backward) {
-            w->carry = take(states);
-            w->bias = take(states);
-        }
+        if (backward && recompute) w->enter = take((size_t)d->batch * w->blocks * d->dim * sizeof(float));
+        if (backward) w->bias = take((size_t)d->batch * w->segments * d->dim * sizeof(float));
     } else {
         // Lanes take 8 steps each; the row's start may lie up to phase_max steps into its tile.
         const int64_t span = L + phase_max;
@@ -213,33 +213,36 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
 }
 
 template <typename IoT, bool kLog, bool kVec, bool kBackward>
-cudaError_t launch_gated_tiles(const GatedParams& prm, int dev, int sms, cudaStream_t stream) {
+cudaError_t launch_gated_tiles(const GatedParams& prm, int warps, int dev, int sms, cudaStream_t stream) {
     static int resident[kMaxDevices] = {0};
     auto kernel = gated_scan_fwd_kernel<IoT, kLog, kVec>;
     if constexpr (kBackward) kernel = gated_scan_bwd_kernel<IoT, kLog, kVec>;
-    const int per_sm = resident_ctas(kernel, kGatedThreads, 0, resident, dev);
-    if (per_sm <= 0) return cudaErrorInvalidConfiguration;
-    const unsigned grid = (unsigned)std::min<int64_t>(prm.items, (int64_t)per_sm * sms);
-    kernel<<<grid, kGatedThreads, 0, stream>>>(prm);
+    int64_t grid = prm.items;
+    if (prm.ticket != nullptr) {        // several segments: CTAs that stay and take one after another
+        const int per_sm = resident_ctas(kernel, kGatedThreads, 0, resident, dev);
+        if (per_sm <= 0) return cudaErrorInvalidConfiguration;
+        grid = std::min<int64_t>(grid, (int64_t)per_sm * sms);
+    }
+    kernel<<<(unsigned)grid, warps * 32, 0, stream>>>(prm);
     return cudaGetLastError();
 }
 
 template <bool kBackward>
-cudaError_t dispatch_gated_tiles(const GatedParams& prm, bool bf16, bool log_decay, bool vec, int dev,
-                                 int sms, cudaStream_t stream) {
+cudaError_t dispatch_gated_tiles(const GatedParams& prm, int warps, bool bf16, bool log_decay, bool vec,
+                                 int dev, int sms, cudaStream_t stream) {
     using B = __nv_bfloat16;
     if (bf16) {
         if (log_decay)
-            return vec ? launch_gated_tiles<B, true, true, kBackward>(prm, dev, sms, stream)
-                       : launch_gated_tiles<B, true, false, kBackward>(prm, dev, sms, stream);
-        return vec ? launch_gated_tiles<B, false, true, kBackward>(prm, dev, sms, stream)
-                   : launch_gated_tiles<B, false, false, kBackward>(prm, dev, sms, stream);
+            return vec ? launch_gated_tiles<B, true, true, kBackward>(prm, warps, dev, sms, stream)
+                       : launch_gated_tiles<B, true, false, kBackward>(prm, warps, dev, sms, stream);
+        return vec ? launch_gated_tiles<B, false, true, kBackward>(prm, warps, dev, sms, stream)
+                   : launch_gated_tiles<B, false, false, kBackward>(prm, warps, dev, sms, stream);
     }
     if (log_decay)
-        return vec ? launch_gated_tiles<float, true, true, kBackward>(prm, dev, sms, stream)
-                   : launch_gated_tiles<float, true, false, kBackward>(prm, dev, sms, stream);
-    return vec ? launch_gated_tiles<float, false, true, kBackward>(prm, dev, sms, stream)
-               : launch_gated_tiles<float, false, false, kBackward>(prm, dev, sms, stream);
+        return vec ? launch_gated_tiles<float, true, true, kBackward>(prm, warps, dev, sms, stream)
+                   : launch_gated_tiles<float, true, false, kBackward>(prm, warps, dev, sms, stream);
+    return vec ? launch_gated_tiles<float, false, true, kBackward>(prm, warps, dev, sms, stream)
+               : launch_gated_tiles<float, false, false, kBackward>(prm, warps, dev, sms, stream);
 }
 
 template <typename IoT, bool kLog, bool kBackward>
@@ -309,12 +312,15 @@ mamba_status_t gated_common(const void* gate, const void* x, const float* bias, 
 
 void gated_apply_layout(const GatedLayout& w, uint8_t* ws, GatedParams* prm) {
     prm->tiles = w.tiles;
+    prm->blocks = w.blocks;
+    prm->segments = w.segments;
     prm->groups_per_row = w.groups_per_row;
     prm->groups = w.groups;
     prm->items = w.items;
     prm->ticket = w.zeroed ? reinterpret_cast<unsigned int*>(ws + w.tickets) : nullptr;
     prm->flags = reinterpret_cast<unsigned int*>(ws + w.flags);
     prm->maps = reinterpret_cast<float4*>(ws + w.maps);
+    prm->states = reinterpret_cast<float2*>(ws + w.joins);
 }
 
 mamba_status_t check_workspace(const void* ws, size_t have, size_t need) {
@@ -625,12 +631,12 @@ MAMBA_API mamba_status_t mamba_gated_scan_fwd(const void* gate, const void* x, c
     const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
     if (w.zeroed && cudaMemsetAsync(ws, 0, w.zeroed, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
-    prm.enter = checkpoints != nullptr ? checkpoints : (w.tiles > 1 ? reinterpret_cast<float*>(ws + w.enter) : nullptr);
+    prm.enter = checkpoints;
     const bool vec = dims->dim % 2 == 0 && rows_aligned(gate, prm.gate_s, es, 2 * es) &&
                      rows_aligned(x, prm.x_s, es, 2 * es) && rows_aligned(out, prm.out_s, es, 2 * es) &&
                      (!gate_bias || aligned(gate_bias, 8)) && (!initial_state || aligned(initial_state, 8)) &&
                      (!last_state || aligned(last_state, 8)) && (!checkpoints || aligned(checkpoints, 8));
-    return status_of(dispatch_gated_tiles<false>(prm, bf16, log_decay, vec, dev, sms, stream));
+    return status_of(dispatch_gated_tiles<false>(prm, w.warps, bf16, log_decay, vec, dev, sms, stream));
 }
 
 MAMBA_API size_t mamba_gated_scan_bwd_workspace_bytes(const mamba_gated_dims_t* dims, int have_checkpoints) {
@@ -716,20 +722,19 @@ MAMBA_API mamba_status_t mamba_gated_scan_bwd(
             fwd.ticket = prm.ticket + 1;
             fwd.flags = reinterpret_cast<unsigned int*>(ws + w.flags2);
         }
-        e = dispatch_gated_tiles<false>(fwd, bf16, log_decay, vec_in, dev, sms, stream);
+        e = dispatch_gated_tiles<false>(fwd, w.warps, bf16, log_decay, vec_in, dev, sms, stream);
         if (e != cudaSuccess) return MAMBA_ERR_CUDA;
         prm.enter = fwd.enter;
     } else {
         prm.enter = const_cast<float*>(checkpoints);
     }
-    prm.carry = reinterpret_cast<float*>(ws + w.carry);
     const bool vec = vec_in && rows_aligned(dout, prm.out_s, es, 2 * es) &&
                      rows_aligned(dgate, prm.dgate_s, es, 2 * es) && rows_aligned(dx, prm.dx_s, es, 2 * es) &&
                      (!dlast_state || aligned(dlast_state, 8)) && (!dinitial_state || aligned(dinitial_state, 8)) &&
                      (!checkpoints || aligned(checkpoints, 8));
-    e = dispatch_gated_tiles<true>(prm, bf16, log_decay, vec, dev, sms, stream);
+    e = dispatch_gated_tiles<true>(prm, w.warps, bf16, log_decay, vec, dev, sms, stream);
     if (e == cudaSuccess && dgate_bias != nullptr)
-        e = launch_column_sum(prm.bias_partial, dims->batch * w.tiles, dims->dim, dims->dim, dgate_bias, nullptr, stream);
+        e = launch_column_sum(prm.bias_partial, dims->batch * w.segments, dims->dim, dims->dim, dgate_bias, nullptr, stream);
     return status_of(e);
 }
 

@@ -22,16 +22,18 @@
 // long as the step's arithmetic (two special-function operations for the
 // sigmoid, one for the log decay) and the joins stay below the issue rate.
 //
-// Layout (batch, seqlen, dim): a tile is 64 steps x 64 channels; each of 8
-// warps takes 8 steps, a lane two neighbouring channels (128- or 256-byte rows
-// per warp access).  A warp folds its steps into one map, the CTA composes the
-// maps through shared memory, and the tiles of a chain are joined by a
-// look-back: a tile publishes its map, then takes the state entering it from
-// the nearest earlier tile that knows its own (folding the published maps in
-// between), publishes the state that leaves it, and replays its steps from
-// registers.  Each input is read once.  Tiles are handed out by a counter, the
-// earliest steps of all chains first, so that every tile's predecessors belong
-// to CTAs that are running or done; the wait is bounded all the same.
+// Layout (batch, seqlen, dim): a warp takes a block of 64 steps of 64 channels
+// (a lane two neighbours: rows of 128 or 256 bytes per access), up to 8 warps
+// side by side in time make a segment of 512 steps.  Phase one walks the block
+// and keeps only its map; the segment's maps are composed through shared
+// memory; segments of a chain are joined by a look-back in fixed groups of 8,
+// so that every state is composed in the same order whatever the timing.  Phase
+// two walks the block again from its true start: its inputs come from L1 and
+// L2 (a segment is 128 KB in bf16, some 70 MB over all resident CTAs), so HBM
+// sees each input once.  The steps' arithmetic is done twice in exchange, in
+// packed fp32x2.  Segments are handed out by a counter, the earliest steps of
+// all chains first, so that every segment's predecessors belong to CTAs that
+// are running or done; the wait is bounded all the same.
 //
 // Layout (batch, dim, seqlen): a lane takes 8 consecutive steps of one chain,
 // the warp composes its lanes' maps by shuffles, and 1 to 8 warps per chain
@@ -44,12 +46,12 @@
 
 namespace mamba {
 
-constexpr int kGatedSteps = 8;                              // steps per thread
-constexpr int kGatedWarps = 8;
-constexpr int kGatedTile = kGatedSteps * kGatedWarps;       // 64 steps
-constexpr int kGatedChannels = 64;                          // per tile, two per lane
+constexpr int kGatedBlock = 64;                             // steps per warp
+constexpr int kGatedWarps = 8;                              // blocks per segment, at most
+constexpr int kGatedChannels = 64;                          // per CTA, two per lane
 constexpr int kGatedThreads = kGatedWarps * 32;
-static_assert(kGatedTile == MAMBA_GATED_CHECKPOINT_STEPS, "checkpoints are the states entering tiles");
+constexpr int kGatedJoin = 8;                               // segments folded from one known state
+static_assert(kGatedBlock == MAMBA_GATED_CHECKPOINT_STEPS, "checkpoints are the states entering blocks");
 
 struct GatedStrides { int64_t batch, row; };
 
@@ -66,48 +68,82 @@ struct GatedParams {
     void* dgate;                  // bwd
     void* dx;                     // bwd
     float* dh0;                   // bwd, (batch, dim) or null
-    float* bias_partial;          // bwd: [batch * tiles][dim] (seqlen fastest: [batch][dim]) or null
-    // (batch, seqlen, dim): states entering tiles, [batch][tiles][dim]
-    float* enter;                 // fwd: written; bwd: read
-    float* carry;                 // bwd: r entering tiles from the right, [batch][tiles][dim]
-    float4* maps;                 // [groups][tiles][32]: a lane's two (A, H) pairs
-    unsigned int* flags;          // [groups][tiles]: 0, 1 = map published, 2 = state published
-    unsigned int* ticket;
+    float* bias_partial;          // bwd: [batch * segments][dim] (seqlen fastest: [batch][dim]) or null
+    // (batch, seqlen, dim)
+    float* enter;                 // [batch][blocks][dim], states entering blocks; fwd: written or null
+    float4* maps;                 // [groups][segments][32]: a lane's two (A, H) pairs
+    float2* states;               // [groups][segments / kGatedJoin][32]: states entering a join group
+    unsigned int* flags;          // [groups][segments]: 0, 1 = map published, 2 = state published
+    unsigned int* ticket;         // null: one segment per chain, one CTA per segment
     // (batch, dim, seqlen), bwd: states entering tiles, [chains][tiles]
     float* chain_states;
     GatedStrides gate_s, x_s, out_s, dgate_s, dx_s;          // out_s: out, or dout
     int64_t batch, dim, seqlen, chains;
-    int64_t tiles;                // per chain
+    int64_t blocks;               // of 64 steps, per chain
+    int64_t segments;             // per chain
     int64_t groups_per_row;       // 64-channel groups per batch row
     int64_t groups;
-    int64_t items;                // groups * tiles
+    int64_t items;                // groups * segments
+    int64_t tiles;                // (batch, dim, seqlen): per chain
     int withhold;                 // test only: publish nothing
 };
 
 constexpr unsigned int kGatedPollLimit = 1u << 19;
 
-// g and a of the sigmoid gate; a = 1 - g to fp32 on both sides.  With
-// e = exp(-|f|), small = e / (1 + e) is the smaller of the two and the other is
-// 1 - small, rounded to nearest: a decay close to 1 is applied over about 1 / g
-// steps, and a biased rounding would grow with that memory.
-__device__ __forceinline__ void sigmoid_gate(float f, float& g, float& a) {
-    const float e = ex2_approx(-fabsf(f) * kLog2e);
-    const float small = __fdividef(e, 1.0f + e);
-    const float big = 1.0f - small;
-    g = f < 0.0f ? small : big;
-    a = f < 0.0f ? big : small;
+// g and a of the sigmoid gate from f log2(e); a = 1 - g to fp32 on both sides.
+// With e = exp(-|f|), small = e / (1 + e) is the smaller of the two and the
+// other is 1 - small, rounded to nearest: a decay close to 1 is applied over
+// about 1 / g steps, and a biased rounding would grow with that memory.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void sigmoid_gate2(float2 f2, float2& g, float2& a) {
+    const float2 one = make_float2(1.0f, 1.0f);
+    const float2 e = make_float2(ex2_approx(-fabsf(f2.x)), ex2_approx(-fabsf(f2.y)));
+    const float2 d = __fadd2_rn(e, one);
+    const float2 small = __fmul2_rn(e, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+    const float2 big = __ffma2_rn(small, make_float2(-1.0f, -1.0f), one);
+    g = make_float2(f2.x < 0.0f ? small.x : big.x, f2.y < 0.0f ? small.y : big.y);
+    a = make_float2(f2.x < 0.0f ? big.x : small.x, f2.y < 0.0f ? big.y : small.y);
+}
+
+// Decay a and input gain g of two gates (gate values f, bias times log2(e)).
+template <bool kLog>
+__device__ __forceinline__ void gated_gains2(float2 f, float2 bias2, float2& g, float2& a) {
+    const float2 f2 = __ffma2_rn(f, make_float2(kLog2e, kLog2e), bias2);
+    if constexpr (kLog) {
+        a = exp2_near_one_exact2(f2);
+        g = make_float2(1.0f, 1.0f);
+    } else {
+        sigmoid_gate2(f2, g, a);
+    }
+}
+
+// One gate.
+template <bool kLog>
+__device__ __forceinline__ void gated_gains(float f, float bias, float& g, float& a) {
+    float2 g2, a2;
+    gated_gains2<kLog>(make_float2(f, f), make_float2(bias * kLog2e, bias * kLog2e), g2, a2);
+    g = g2.x;
+    a = a2.x;
 }
 
 template <bool kLog>
-__device__ __forceinline__ void gated_terms(float f, float x, float& a, float& u) {
-    if constexpr (kLog) {
-        a = exp2_near_one_exact(f * kLog2e);
-        u = x;
-    } else {
-        float g;
-        sigmoid_gate(f, g, a);
-        u = g * x;
-    }
+__device__ __forceinline__ void gated_terms(float f, float bias, float x, float& a, float& u) {
+    float g;
+    gated_gains<kLog>(f, bias, g, a);
+    u = kLog ? x : g * x;
+}
+
+// Decay and input term.
+template <bool kLog>
+__device__ __forceinline__ void gated_terms2(float2 f, float2 bias2, float2 x, float2& a, float2& u) {
+    float2 g;
+    gated_gains2<kLog>(f, bias2, g, a);
+    u = kLog ? x : __fmul2_rn(g, x);
 }
 
 __device__ __forceinline__ int64_t gated_length(const GatedParams& p, int64_t b) {
@@ -181,64 +217,40 @@ __device__ __forceinline__ void store_f2(float* p, bool c0, bool c1, float2 v) {
     store_pair<float, kVec>(p, c0, c1, v);
 }
 
-// Where a tile lies: item = position * groups + group, positions in the order
-// of the scan (kReverse: the last tile of a chain first).
-struct GatedTileAt {
-    int64_t b, group, tile, t0, d;      // d: this lane's first channel
-    int64_t n;                          // the row's length
+// Where a warp's block lies: item = position * groups + group, positions in the
+// order of the scan (kReverse: the last segment of a chain first).
+struct GatedBlockAt {
+    int64_t b, group, pos, segment, block, t, d;    // t: first step; d: this lane's first channel
+    int left, rows;                                 // steps inside the sequence, inside the tensor
 };
 
 template <bool kReverse>
-__device__ __forceinline__ GatedTileAt gated_tile(const GatedParams& p, int64_t item, int lane) {
-    GatedTileAt at;
-    const int64_t pos = item / p.groups;
-    at.group = item - pos * p.groups;
-    at.tile = kReverse ? p.tiles - 1 - pos : pos;
+__device__ __forceinline__ GatedBlockAt gated_block(const GatedParams& p, int64_t item, int warp, int lane) {
+    GatedBlockAt at;
+    at.pos = item / p.groups;
+    at.group = item - at.pos * p.groups;
+    at.segment = kReverse ? p.segments - 1 - at.pos : at.pos;
     at.b = at.group / p.groups_per_row;
     at.d = (at.group - at.b * p.groups_per_row) * kGatedChannels + 2 * lane;
-    at.t0 = at.tile * kGatedTile;
-    at.n = gated_length(p, at.b);
+    at.block = at.segment * (blockDim.x >> 5) + warp;
+    at.t = at.block * kGatedBlock;
+    const int64_t n = gated_length(p, at.b) - at.t, rows = p.seqlen - at.t;
+    at.left = (int)(n < 0 ? 0 : (n > kGatedBlock ? kGatedBlock : n));
+    at.rows = (int)(rows < 0 ? 0 : (rows > kGatedBlock ? kGatedBlock : rows));
     return at;
 }
 
-// The state (or r) entering tile `at` of a chain that is scanned from `pos` 0
-// on, for this lane's two channels: `own` is what chain position 0 starts from.
-// Called by one warp.  Walks back from the tile before: published maps are
-// folded until a tile with a published state is met.  state_row(k) is where
-// the state that LEAVES position k is kept.
-template <bool kVec, typename StateAt>
-__device__ __forceinline__ float2 gated_look_back(const GatedParams& p, int64_t group, int64_t pos,
-                                                  int lane, bool c0, bool c1, StateAt state_at) {
-    const unsigned int* flags = p.flags + group * p.tiles;
-    const float4* maps = p.maps + (group * p.tiles) * 32 + lane;
-    float2 A = make_float2(1.0f, 1.0f), H = make_float2(0.0f, 0.0f);
-    int64_t next = pos - 1;               // nearest position not folded yet
-    for (unsigned int poll = 0; poll < kGatedPollLimit; ++poll) {
-        const int64_t k = next - lane;
-        const unsigned int f = k >= 0 ? load_acquire(flags + k) : 2u;
-        const unsigned int known = __ballot_sync(0xffffffffu, f == 2u);
-        const unsigned int missing = __ballot_sync(0xffffffffu, f == 0u);
-        // fold the run of published maps before the first known state or gap
-        const int stop = known ? __ffs(known) - 1 : 32;
-        const int gap = missing ? __ffs(missing) - 1 : 32;
-        const int run = stop < gap ? stop : gap;
-        if (run > 0 && (stop < gap || run >= 8)) {
-            for (int j = 0; j < run; ++j) {
-                const float4 m = __ldcg(maps + (next - j) * 32);
-                H.x = fmaf(A.x, m.y, H.x);
-                H.y = fmaf(A.y, m.w, H.y);
-                A.x *= m.x;
-                A.y *= m.z;
-            }
-            next -= run;
-        }
-        if (stop < gap) {                 // position `next` has published its state
-            const float2 h = load_f2<kVec>(state_at(next), c0, c1);
-            return make_float2(fmaf(A.x, h.x, H.x), fmaf(A.y, h.y, H.y));
-        }
+// kN steps of two channels; steps from `left` on are not read and give 0.
+template <typename IoT, bool kVec, int kN>
+__device__ __forceinline__ void load_pairs(Pair<IoT> (&r)[kN], const IoT* p, int64_t stride, int left,
+                                           bool c0, bool c1) {
+    if (left >= kN) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) r[i] = load_pair<IoT, kVec>(p + i * stride, c0, c1);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) r[i] = load_pair<IoT, kVec>(p + i * stride, i < left && c0, i < left && c1);
     }
-    if (lane == 0) record_device_error(MAMBA_ERR_TIMEOUT);
-    return make_float2(0.0f, 0.0f);
 }
 
 // Publishing: every lane has written its part; lane 0 raises the flag.
@@ -251,295 +263,288 @@ __device__ __forceinline__ void gated_publish(const GatedParams& p, unsigned int
     }
 }
 
-// Forward.  Shared memory holds the warps' maps and the entering state.
+// The state entering segment `pos` of a chain (positions in scan order) for
+// this lane's two channels; called by one warp with the segment's own map.
+// Positions form groups of kGatedJoin.  The last of a group publishes the state
+// that leaves it, the others their maps; a segment waits for the state entering
+// its group and the maps of the group's earlier segments, and folds them in
+// order.  `start` is the state entering position 0.
+__device__ __forceinline__ float2 gated_join(const GatedParams& p, int64_t group, int64_t pos, int lane,
+                                             float4 map, float2 start) {
+    const int64_t join = pos / kGatedJoin, first = join * kGatedJoin;
+    const int before = (int)(pos - first);
+    unsigned int* flags = p.flags + group * p.segments;
+    float4* maps = p.maps + (group * p.segments) * 32 + lane;
+    const int64_t joins = (p.segments + kGatedJoin - 1) / kGatedJoin;
+    float2* states = p.states + (group * joins) * 32 + lane;
+    const bool closes = before == kGatedJoin - 1;
+    if (!closes && pos + 1 < p.segments) {
+        __stcg(maps + pos * 32, map);
+        gated_publish(p, flags + pos, lane, 1u);
+    }
+    // lane l < before waits for the map of segment first + l, lane kGatedJoin for the state
+    const bool wait_map = lane < before, wait_state = lane == kGatedJoin && join > 0;
+    const unsigned int* mine = flags + (wait_map ? first + lane : first - 1);
+    bool ready = !(wait_map || wait_state);
+    unsigned int poll = 0;
+    for (; poll < kGatedPollLimit; ++poll) {
+        if (!ready) ready = load_acquire(mine) >= (wait_state ? 2u : 1u);
+        if (__all_sync(0xffffffffu, ready)) break;
+    }
+    float2 h = start;
+    if (poll == kGatedPollLimit) {
+        if (lane == 0) record_device_error(MAMBA_ERR_TIMEOUT);
+    } else {
+        float4 m[kGatedJoin - 1];
+#pragma unroll
+        for (int i = 0; i < kGatedJoin - 1; ++i)
+            m[i] = i < before ? __ldcg(maps + (first + i) * 32) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+        if (join > 0) h = __ldcg(states + join * 32);
+#pragma unroll
+        for (int i = 0; i < kGatedJoin - 1; ++i)
+            if (i < before) {
+                h.x = fmaf(m[i].x, h.x, m[i].y);
+                h.y = fmaf(m[i].z, h.y, m[i].w);
+            }
+    }
+    if (closes && pos + 1 < p.segments) {
+        __stcg(states + (join + 1) * 32, make_float2(fmaf(map.x, h.x, map.y), fmaf(map.z, h.y, map.w)));
+        gated_publish(p, flags + pos, lane, 2u);
+    }
+    return h;
+}
+
+// The next item of a CTA.  `slot` is written before a barrier and read after it.
+__device__ __forceinline__ int64_t gated_first_item(const GatedParams& p, int64_t* slot) {
+    if (p.ticket == nullptr) return blockIdx.x;
+    if (threadIdx.x == 0) *slot = atomicAdd(p.ticket, 1u);
+    __syncthreads();
+    return *slot;
+}
+
+constexpr int kGatedSub = 8;                 // steps requested at a time
+
 template <typename IoT, bool kLog, bool kVec>
-__global__ void __launch_bounds__(kGatedThreads, 2)
+__global__ void __launch_bounds__(kGatedThreads)
     gated_scan_fwd_kernel(const __grid_constant__ GatedParams p) {
     __shared__ float4 maps[kGatedWarps][32];
     __shared__ float2 entering[32];
-    __shared__ int64_t first_item, next_item;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool dynamic = p.ticket != nullptr;
-    if (threadIdx.x == 0) first_item = dynamic ? (int64_t)atomicAdd(p.ticket, 1u) : (int64_t)blockIdx.x;
-    __syncthreads();
-    int64_t item = first_item;
-    Pair<IoT> rf[kGatedSteps], rx[kGatedSteps];
-
-    auto request = [&](int64_t it) {
-        const GatedTileAt at = gated_tile<false>(p, it, lane);
-        const bool c0 = at.d < p.dim, c1 = at.d + 1 < p.dim;
-        const int64_t t = at.t0 + warp * kGatedSteps;
-        const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + t * p.gate_s.row + at.d;
-        const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + t * p.x_s.row + at.d;
-#pragma unroll
-        for (int i = 0; i < kGatedSteps; ++i) {
-            const bool in = t + i < at.n;
-            rf[i] = load_pair<IoT, kVec>(gate + i * p.gate_s.row, in && c0, in && c1);
-            rx[i] = load_pair<IoT, kVec>(x + i * p.x_s.row, in && c0, in && c1);
-        }
-    };
-    if (item < p.items) request(item);
-
+    __shared__ int64_t first_slot, next_slot;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const float2 zero = make_float2(0.0f, 0.0f), one = make_float2(1.0f, 1.0f);
+    int64_t item = gated_first_item(p, &first_slot);
     while (item < p.items) {
-        const GatedTileAt at = gated_tile<false>(p, item, lane);
+        const GatedBlockAt at = gated_block<false>(p, item, warp, lane);
         const bool c0 = at.d < p.dim, c1 = at.d + 1 < p.dim;
-        const int64_t t = at.t0 + warp * kGatedSteps;
-        const float2 bias = p.bias != nullptr ? load_f2<kVec>(p.bias + at.d, c0, c1) : make_float2(0.0f, 0.0f);
-        float2 a[kGatedSteps], u[kGatedSteps];
-        float2 A = make_float2(1.0f, 1.0f), H = make_float2(0.0f, 0.0f);
+        float2 bias2 = p.bias != nullptr ? load_f2<kVec>(p.bias + at.d, c0, c1) : zero;
+        bias2 = __fmul2_rn(bias2, make_float2(kLog2e, kLog2e));
+        const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + at.t * p.gate_s.row + at.d;
+        const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.t * p.x_s.row + at.d;
+        float2 h = p.h0 != nullptr ? load_f2<kVec>(p.h0 + at.b * p.dim + at.d, c0, c1) : zero;
+        int64_t following = p.items;
+        if (p.blocks > 1) {
+            if (threadIdx.x == 0 && p.ticket != nullptr) next_slot = atomicAdd(p.ticket, 1u);
+            float2 A = one, H = zero;
+            for (int s = 0; s < at.left; s += kGatedSub) {
+                Pair<IoT> rf[kGatedSub], rx[kGatedSub];
+                load_pairs<IoT, kVec>(rf, gate + s * p.gate_s.row, p.gate_s.row, at.left - s, c0, c1);
+                load_pairs<IoT, kVec>(rx, x + s * p.x_s.row, p.x_s.row, at.left - s, c0, c1);
+                float2 a[kGatedSub], u[kGatedSub];
 #pragma unroll
-        for (int i = 0; i < kGatedSteps; ++i) {
-            const float2 f = rf[i].get(), x = rx[i].get();
-            gated_terms<kLog>(f.x + bias.x, x.x, a[i].x, u[i].x);
-            gated_terms<kLog>(f.y + bias.y, x.y, a[i].y, u[i].y);
-            if (t + i >= at.n) {
-                a[i] = make_float2(1.0f, 1.0f);
-                u[i] = make_float2(0.0f, 0.0f);
+                for (int i = 0; i < kGatedSub; ++i)
+                    gated_terms2<kLog>(rf[i].get(), bias2, rx[i].get(), a[i], u[i]);
+                if (at.left - s < kGatedSub)
+#pragma unroll
+                    for (int i = 0; i < kGatedSub; ++i)
+                        if (s + i >= at.left) a[i] = one;       // u is 0: x was not read
+#pragma unroll
+                for (int i = 0; i < kGatedSub; ++i) {
+                    H = __ffma2_rn(a[i], H, u[i]);
+                    A = __fmul2_rn(A, a[i]);
+                }
             }
-            H.x = fmaf(a[i].x, H.x, u[i].x);
-            H.y = fmaf(a[i].y, H.y, u[i].y);
-            A.x *= a[i].x;
-            A.y *= a[i].y;
-        }
-        maps[warp][lane] = make_float4(A.x, H.x, A.y, H.y);
-        if (threadIdx.x == 0)
-            next_item = dynamic ? (int64_t)atomicAdd(p.ticket, 1u) : item + gridDim.x;
-        __syncthreads();
-        const int64_t following = next_item;
-        if (following < p.items) request(following);
-
-        // the map of the warps before this one (warp 0: of the whole tile)
-        float2 Ap = make_float2(1.0f, 1.0f), Hp = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int v = 0; v < kGatedWarps; ++v)
-            if (v < warp || warp == 0) {
+            maps[warp][lane] = make_float4(A.x, H.x, A.y, H.y);
+            __syncthreads();
+            if (p.ticket != nullptr) {
+                following = next_slot;
+                if (warp == 0) {
+                    float2 At = one, Ht = zero;
+                    for (int v = 0; v < warps; ++v) {
+                        const float4 m = maps[v][lane];
+                        Ht = __ffma2_rn(make_float2(m.x, m.z), Ht, make_float2(m.y, m.w));
+                        At = __fmul2_rn(At, make_float2(m.x, m.z));
+                    }
+                    entering[lane] = gated_join(p, at.group, at.pos, lane, make_float4(At.x, Ht.x, At.y, Ht.y), h);
+                }
+            }
+            float2 Ap = one, Hp = zero;
+            for (int v = 0; v < warp; ++v) {
                 const float4 m = maps[v][lane];
-                Hp.x = fmaf(m.x, Hp.x, m.y);
-                Hp.y = fmaf(m.z, Hp.y, m.w);
-                Ap.x *= m.x;
-                Ap.y *= m.z;
+                Hp = __ffma2_rn(make_float2(m.x, m.z), Hp, make_float2(m.y, m.w));
+                Ap = __fmul2_rn(Ap, make_float2(m.x, m.z));
             }
-        float* enter = p.enter != nullptr ? p.enter + (at.b * p.tiles + at.tile) * p.dim + at.d : nullptr;
-        if (warp == 0) {
-            float2 h;
-            unsigned int* flag = p.flags + at.group * p.tiles + at.tile;
-            if (at.tile == 0) {
-                h = p.h0 != nullptr ? load_f2<kVec>(p.h0 + at.b * p.dim + at.d, c0, c1) : make_float2(0.0f, 0.0f);
-                if (enter != nullptr) store_f2<kVec>(enter, c0, c1, h);
-            } else {
-                __stcg(p.maps + (at.group * p.tiles + at.tile) * 32 + lane,
-                       make_float4(Ap.x, Hp.x, Ap.y, Hp.y));
-                gated_publish(p, flag, lane, 1u);
-                // the state leaving tile k is the one entering tile k + 1
-                const float* base = p.enter + (at.b * p.tiles + 1) * p.dim + at.d;
-                const int64_t dim = p.dim;
-                h = gated_look_back<kVec>(p, at.group, at.tile, lane, c0, c1,
-                                          [base, dim](int64_t k) { return base + k * dim; });
+            if (p.ticket != nullptr) {
+                __syncthreads();
+                h = entering[lane];
             }
-            const float2 leave = make_float2(fmaf(Ap.x, h.x, Hp.x), fmaf(Ap.y, h.y, Hp.y));
-            if (at.tile + 1 < p.tiles) {
-                store_f2<kVec>(enter + p.dim, c0, c1, leave);
-                gated_publish(p, flag, lane, 2u);
-            } else if (p.last != nullptr) {
-                store_f2<kVec>(p.last + at.b * p.dim + at.d, c0, c1, leave);
-            }
-            entering[lane] = h;
-            Ap = make_float2(1.0f, 1.0f);
-            Hp = make_float2(0.0f, 0.0f);
+            h = __ffma2_rn(Ap, h, Hp);
         }
-        __syncthreads();
-        const float2 h_in = entering[lane];
+        if (at.rows > 0 && p.enter != nullptr)
+            store_f2<kVec>(p.enter + (at.b * p.blocks + at.block) * p.dim + at.d, c0, c1, h);
         if (p.out != nullptr) {
-            float2 h = make_float2(fmaf(Ap.x, h_in.x, Hp.x), fmaf(Ap.y, h_in.y, Hp.y));
-            IoT* out = static_cast<IoT*>(p.out) + at.b * p.out_s.batch + t * p.out_s.row + at.d;
+            IoT* out = static_cast<IoT*>(p.out) + at.b * p.out_s.batch + at.t * p.out_s.row + at.d;
+            int s = 0;
+            for (; s < at.left; s += kGatedSub) {
+                Pair<IoT> rf[kGatedSub], rx[kGatedSub];
+                load_pairs<IoT, kVec>(rf, gate + s * p.gate_s.row, p.gate_s.row, at.left - s, c0, c1);
+                load_pairs<IoT, kVec>(rx, x + s * p.x_s.row, p.x_s.row, at.left - s, c0, c1);
+                float2 a[kGatedSub], u[kGatedSub];
 #pragma unroll
-            for (int i = 0; i < kGatedSteps; ++i) {
-                h.x = fmaf(a[i].x, h.x, u[i].x);
-                h.y = fmaf(a[i].y, h.y, u[i].y);
-                if (t + i < p.seqlen)
-                    store_pair<IoT, kVec>(out + i * p.out_s.row, c0, c1,
-                                          t + i < at.n ? h : make_float2(0.0f, 0.0f));
+                for (int i = 0; i < kGatedSub; ++i)
+                    gated_terms2<kLog>(rf[i].get(), bias2, rx[i].get(), a[i], u[i]);
+                IoT* o = out + s * p.out_s.row;
+                if (at.left - s >= kGatedSub) {
+#pragma unroll
+                    for (int i = 0; i < kGatedSub; ++i) {
+                        h = __ffma2_rn(a[i], h, u[i]);
+                        store_pair<IoT, kVec>(o + i * p.out_s.row, c0, c1, h);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kGatedSub; ++i) {
+                        const bool in = s + i < at.left;
+                        if (in) h = __ffma2_rn(a[i], h, u[i]);
+                        if (s + i < at.rows) store_pair<IoT, kVec>(o + i * p.out_s.row, c0, c1, in ? h : zero);
+                    }
+                }
             }
+            for (; s < at.rows; ++s) store_pair<IoT, kVec>(out + s * p.out_s.row, c0, c1, zero);
+            if (p.last != nullptr && at.block == p.blocks - 1)
+                store_f2<kVec>(p.last + at.b * p.dim + at.d, c0, c1, h);
         }
         item = following;
     }
 }
 
-// Backward.  r runs from the last tile to the first; the states of a tile are
-// replayed from the state entering it.
+// Backward.  Phase one walks a block forward from its checkpoint, keeps the
+// state every kGatedBack steps in shared memory and accumulates the block's map
+// of r, R = sum_t (prod_{s <= t} a_s) dout_t; phase two walks it backward.
+constexpr int kGatedBack = 4;
+
 template <typename IoT, bool kLog, bool kVec>
 __global__ void __launch_bounds__(kGatedThreads, 2)
     gated_scan_bwd_kernel(const __grid_constant__ GatedParams p) {
-    __shared__ float4 maps[kGatedWarps][32];            // (A, H) of the warps' steps
-    __shared__ float2 rights[kGatedWarps][32];          // R: r leaving a warp's steps when 0 enters
+    __shared__ float4 maps[kGatedWarps][32];
     __shared__ float2 entering[32];
     __shared__ float2 bias_sums[kGatedWarps][32];
-    __shared__ int64_t first_item, next_item;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool dynamic = p.ticket != nullptr;
-    if (threadIdx.x == 0) first_item = dynamic ? (int64_t)atomicAdd(p.ticket, 1u) : (int64_t)blockIdx.x;
-    __syncthreads();
-    int64_t item = first_item;
-    Pair<IoT> rf[kGatedSteps], rx[kGatedSteps], rd[kGatedSteps];
-    float2 enter = make_float2(0.0f, 0.0f);
-
-    auto request = [&](int64_t it) {
-        const GatedTileAt at = gated_tile<true>(p, it, lane);
-        const bool c0 = at.d < p.dim, c1 = at.d + 1 < p.dim;
-        const int64_t t = at.t0 + warp * kGatedSteps;
-        const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + t * p.gate_s.row + at.d;
-        const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + t * p.x_s.row + at.d;
-        const IoT* dout = static_cast<const IoT*>(p.dout) + at.b * p.out_s.batch + t * p.out_s.row + at.d;
-#pragma unroll
-        for (int i = 0; i < kGatedSteps; ++i) {
-            const bool in = t + i < at.n;
-            rf[i] = load_pair<IoT, kVec>(gate + i * p.gate_s.row, in && c0, in && c1);
-            rx[i] = load_pair<IoT, kVec>(x + i * p.x_s.row, in && c0, in && c1);
-            rd[i] = load_pair<IoT, kVec>(dout + i * p.out_s.row, in && c0, in && c1);
-        }
-        enter = load_f2<kVec>(p.enter + (at.b * p.tiles + at.tile) * p.dim + at.d, c0, c1);
-    };
-    if (item < p.items) request(item);
-
+    __shared__ float2 kept[kGatedWarps][kGatedBlock / kGatedBack][32];
+    __shared__ int64_t first_slot, next_slot;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const float2 zero = make_float2(0.0f, 0.0f), one = make_float2(1.0f, 1.0f);
+    int64_t item = gated_first_item(p, &first_slot);
     while (item < p.items) {
-        const GatedTileAt at = gated_tile<true>(p, item, lane);
+        const GatedBlockAt at = gated_block<true>(p, item, warp, lane);
         const bool c0 = at.d < p.dim, c1 = at.d + 1 < p.dim;
-        const int64_t t = at.t0 + warp * kGatedSteps;
-        const float2 bias = p.bias != nullptr ? load_f2<kVec>(p.bias + at.d, c0, c1) : make_float2(0.0f, 0.0f);
-        float2 a[kGatedSteps], g[kGatedSteps], x[kGatedSteps], dd[kGatedSteps];
-        float2 A = make_float2(1.0f, 1.0f), H = make_float2(0.0f, 0.0f);
+        float2 bias2 = p.bias != nullptr ? load_f2<kVec>(p.bias + at.d, c0, c1) : zero;
+        bias2 = __fmul2_rn(bias2, make_float2(kLog2e, kLog2e));
+        const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + at.t * p.gate_s.row + at.d;
+        const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.t * p.x_s.row + at.d;
+        const IoT* dout = static_cast<const IoT*>(p.dout) + at.b * p.out_s.batch + at.t * p.out_s.row + at.d;
+        int64_t following = p.items;
+        if (threadIdx.x == 0 && p.ticket != nullptr) next_slot = atomicAdd(p.ticket, 1u);
+        float2 h = at.rows > 0 ? load_f2<kVec>(p.enter + (at.b * p.blocks + at.block) * p.dim + at.d, c0, c1) : zero;
+        float2 P = one, R = zero;
+        for (int s = 0; s < at.left; s += kGatedSub) {
+            Pair<IoT> rf[kGatedSub], rx[kGatedSub], rd[kGatedSub];
+            load_pairs<IoT, kVec>(rf, gate + s * p.gate_s.row, p.gate_s.row, at.left - s, c0, c1);
+            load_pairs<IoT, kVec>(rx, x + s * p.x_s.row, p.x_s.row, at.left - s, c0, c1);
+            load_pairs<IoT, kVec>(rd, dout + s * p.out_s.row, p.out_s.row, at.left - s, c0, c1);
 #pragma unroll
-        for (int i = 0; i < kGatedSteps; ++i) {
-            const float2 f = rf[i].get();
-            x[i] = rx[i].get();
-            dd[i] = rd[i].get();
-            if constexpr (kLog) {
-                a[i].x = exp2_near_one_exact((f.x + bias.x) * kLog2e);
-                a[i].y = exp2_near_one_exact((f.y + bias.y) * kLog2e);
-                g[i] = make_float2(1.0f, 1.0f);
-            } else {
-                sigmoid_gate(f.x + bias.x, g[i].x, a[i].x);
-                sigmoid_gate(f.y + bias.y, g[i].y, a[i].y);
+            for (int i = 0; i < kGatedSub; ++i) {
+                if (i % kGatedBack == 0) kept[warp][(s + i) / kGatedBack][lane] = h;
+                float2 a, u;
+                gated_terms2<kLog>(rf[i].get(), bias2, rx[i].get(), a, u);
+                if (s + i >= at.left) a = one;
+                h = __ffma2_rn(a, h, u);
+                P = __fmul2_rn(P, a);
+                R = __ffma2_rn(P, rd[i].get(), R);
             }
-            if (t + i >= at.n) {          // outside: x and dout were not read and are 0
-                a[i] = make_float2(1.0f, 1.0f);
-                g[i] = make_float2(0.0f, 0.0f);
-            }
-            H.x = fmaf(a[i].x, H.x, g[i].x * x[i].x);
-            H.y = fmaf(a[i].y, H.y, g[i].y * x[i].y);
-            A.x *= a[i].x;
-            A.y *= a[i].y;
         }
-        float2 R = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int i = kGatedSteps - 1; i >= 0; --i) {
-            R.x = a[i].x * (dd[i].x + R.x);
-            R.y = a[i].y * (dd[i].y + R.y);
-        }
-        maps[warp][lane] = make_float4(A.x, H.x, A.y, H.y);
-        rights[warp][lane] = R;
-        if (threadIdx.x == 0)
-            next_item = dynamic ? (int64_t)atomicAdd(p.ticket, 1u) : item + gridDim.x;
+        maps[warp][lane] = make_float4(P.x, R.x, P.y, R.y);
         __syncthreads();
-        const int64_t following = next_item;
-        // states: from the tile's entry through the warps before this one
-        float2 h = enter;
-#pragma unroll
-        for (int v = 0; v < kGatedWarps - 1; ++v)
-            if (v < warp) {
-                const float4 m = maps[v][lane];
-                h.x = fmaf(m.x, h.x, m.y);
-                h.y = fmaf(m.z, h.y, m.w);
-            }
-        // r: the map of the warps after this one (last warp: of the whole tile)
-        constexpr int kLast = kGatedWarps - 1;
-        float2 Ap = make_float2(1.0f, 1.0f), Rp = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int v = kLast; v >= 0; --v)
-            if (v > warp || warp == kLast) {
-                const float4 m = maps[v][lane];
-                const float2 r = rights[v][lane];
-                Rp.x = fmaf(m.x, Rp.x, r.x);
-                Rp.y = fmaf(m.z, Rp.y, r.y);
-                Ap.x *= m.x;
-                Ap.y *= m.z;
-            }
-        if (following < p.items) request(following);
-        if (warp == kLast) {
-            float2 r;
-            const int64_t pos = p.tiles - 1 - at.tile;
-            unsigned int* flag = p.flags + at.group * p.tiles + pos;
-            float* carry = p.carry + (at.b * p.tiles + at.tile) * p.dim + at.d;   // r leaving this tile
-            if (pos == 0) {
-                r = p.dlast != nullptr ? load_f2<kVec>(p.dlast + at.b * p.dim + at.d, c0, c1)
-                                       : make_float2(0.0f, 0.0f);
-            } else {
-                __stcg(p.maps + (at.group * p.tiles + pos) * 32 + lane,
-                       make_float4(Ap.x, Rp.x, Ap.y, Rp.y));
-                gated_publish(p, flag, lane, 1u);
-                const float* base = p.carry + (at.b * p.tiles + p.tiles - 1) * p.dim + at.d;
-                const int64_t dim = p.dim;
-                r = gated_look_back<kVec>(p, at.group, pos, lane, c0, c1,
-                                          [base, dim](int64_t k) { return base - k * dim; });
-            }
-            const float2 leave = make_float2(fmaf(Ap.x, r.x, Rp.x), fmaf(Ap.y, r.y, Rp.y));
-            if (at.tile > 0) {
-                store_f2<kVec>(carry, c0, c1, leave);
-                gated_publish(p, flag, lane, 2u);
-            } else if (p.dh0 != nullptr) {
-                store_f2<kVec>(p.dh0 + at.b * p.dim + at.d, c0, c1, leave);
-            }
-            entering[lane] = r;
-            Ap = make_float2(1.0f, 1.0f);
-            Rp = make_float2(0.0f, 0.0f);
-        }
-        // replay the states while the last warp looks back
-        float2 before[kGatedSteps];
-#pragma unroll
-        for (int i = 0; i < kGatedSteps; ++i) {
-            before[i] = h;
-            h.x = fmaf(a[i].x, h.x, g[i].x * x[i].x);
-            h.y = fmaf(a[i].y, h.y, g[i].y * x[i].y);
-        }
-        __syncthreads();
-        const float2 r_in = entering[lane];
-        float2 r = make_float2(fmaf(Ap.x, r_in.x, Rp.x), fmaf(Ap.y, r_in.y, Rp.y));
-        float2 db = make_float2(0.0f, 0.0f);
-        IoT* dgate = static_cast<IoT*>(p.dgate) + at.b * p.dgate_s.batch + t * p.dgate_s.row + at.d;
-        IoT* dx = static_cast<IoT*>(p.dx) + at.b * p.dx_s.batch + t * p.dx_s.row + at.d;
-#pragma unroll
-        for (int i = kGatedSteps - 1; i >= 0; --i) {
-            const float2 l = make_float2(dd[i].x + r.x, dd[i].y + r.y);
-            r.x = a[i].x * l.x;
-            r.y = a[i].y * l.y;
-            float2 df, dv;
-            if constexpr (kLog) {
-                df = make_float2(r.x * before[i].x, r.y * before[i].y);
-                dv = l;
-            } else {
-                dv = make_float2(g[i].x * l.x, g[i].y * l.y);
-                df.x = g[i].x * r.x * (x[i].x - before[i].x);
-                df.y = g[i].y * r.y * (x[i].y - before[i].y);
-            }
-            if (t + i >= at.n) df = dv = make_float2(0.0f, 0.0f);
-            db.x += df.x;
-            db.y += df.y;
-            if (t + i < p.seqlen) {
-                store_pair<IoT, kVec>(dgate + i * p.dgate_s.row, c0, c1, df);
-                store_pair<IoT, kVec>(dx + i * p.dx_s.row, c0, c1, dv);
+        float2 r = p.dlast != nullptr ? load_f2<kVec>(p.dlast + at.b * p.dim + at.d, c0, c1) : zero;
+        if (p.ticket != nullptr) {
+            following = next_slot;
+            if (warp == 0) {
+                float2 At = one, Rt = zero;
+                for (int v = warps - 1; v >= 0; --v) {
+                    const float4 m = maps[v][lane];
+                    Rt = __ffma2_rn(make_float2(m.x, m.z), Rt, make_float2(m.y, m.w));
+                    At = __fmul2_rn(At, make_float2(m.x, m.z));
+                }
+                entering[lane] = gated_join(p, at.group, at.pos, lane, make_float4(At.x, Rt.x, At.y, Rt.y), r);
             }
         }
+        float2 Ap = one, Rp = zero;
+        for (int v = warps - 1; v > warp; --v) {
+            const float4 m = maps[v][lane];
+            Rp = __ffma2_rn(make_float2(m.x, m.z), Rp, make_float2(m.y, m.w));
+            Ap = __fmul2_rn(Ap, make_float2(m.x, m.z));
+        }
+        if (p.ticket != nullptr) {
+            __syncthreads();
+            r = entering[lane];
+        }
+        r = __ffma2_rn(Ap, r, Rp);
+
+        float2 db = zero;
+        IoT* dgate = static_cast<IoT*>(p.dgate) + at.b * p.dgate_s.batch + at.t * p.dgate_s.row + at.d;
+        IoT* dx = static_cast<IoT*>(p.dx) + at.b * p.dx_s.batch + at.t * p.dx_s.row + at.d;
+        for (int s = at.left; s < at.rows; ++s) {
+            store_pair<IoT, kVec>(dgate + s * p.dgate_s.row, c0, c1, zero);
+            store_pair<IoT, kVec>(dx + s * p.dx_s.row, c0, c1, zero);
+        }
+        for (int s = (at.left - 1) & ~(kGatedBack - 1); s >= 0; s -= kGatedBack) {
+            const int left = at.left - s;
+            Pair<IoT> rf[kGatedBack], rx[kGatedBack], rd[kGatedBack];
+            load_pairs<IoT, kVec>(rf, gate + s * p.gate_s.row, p.gate_s.row, left, c0, c1);
+            load_pairs<IoT, kVec>(rx, x + s * p.x_s.row, p.x_s.row, left, c0, c1);
+            load_pairs<IoT, kVec>(rd, dout + s * p.out_s.row, p.out_s.row, left, c0, c1);
+            float2 a[kGatedBack], g[kGatedBack], before[kGatedBack];
+            h = kept[warp][s / kGatedBack][lane];
+#pragma unroll
+            for (int i = 0; i < kGatedBack; ++i) {
+                gated_gains2<kLog>(rf[i].get(), bias2, g[i], a[i]);
+                before[i] = h;
+                h = __ffma2_rn(a[i], h, kLog ? rx[i].get() : __fmul2_rn(g[i], rx[i].get()));
+            }
+#pragma unroll
+            for (int i = kGatedBack - 1; i >= 0; --i)
+                if (i < left) {
+                    const float2 l = __fadd2_rn(rd[i].get(), r);
+                    r = __fmul2_rn(a[i], l);
+                    float2 df, dv;
+                    if constexpr (kLog) {
+                        dv = l;
+                        df = __fmul2_rn(r, before[i]);
+                    } else {
+                        const float2 diff = __ffma2_rn(before[i], make_float2(-1.0f, -1.0f), rx[i].get());
+                        dv = __fmul2_rn(g[i], l);
+                        df = __fmul2_rn(__fmul2_rn(g[i], r), diff);
+                    }
+                    db = __fadd2_rn(db, df);
+                    store_pair<IoT, kVec>(dgate + (s + i) * p.dgate_s.row, c0, c1, df);
+                    store_pair<IoT, kVec>(dx + (s + i) * p.dx_s.row, c0, c1, dv);
+                }
+        }
+        if (p.dh0 != nullptr && at.block == 0) store_f2<kVec>(p.dh0 + at.b * p.dim + at.d, c0, c1, r);
         if (p.bias_partial != nullptr) {
             bias_sums[warp][lane] = db;
             __syncthreads();
             if (warp == 0) {
-                float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int v = 0; v < kGatedWarps; ++v) {
-                    sum.x += bias_sums[v][lane].x;
-                    sum.y += bias_sums[v][lane].y;
-                }
-                store_f2<kVec>(p.bias_partial + (at.b * p.tiles + at.tile) * p.dim + at.d, c0, c1, sum);
+                float2 sum = zero;
+                for (int v = 0; v < warps; ++v) sum = __fadd2_rn(sum, bias_sums[v][lane]);
+                store_f2<kVec>(p.bias_partial + (at.b * p.segments + at.segment) * p.dim + at.d, c0, c1, sum);
             }
         }
         item = following;
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__(kGatedThreads)
         float A = 1.0f, H = 0.0f, At, Ht;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            gated_terms<kLog>(a[i] + bias, x8[i], a[i], u[i]);
+            gated_terms<kLog>(a[i], bias, x8[i], a[i], u[i]);
             if (t0 + i < 0 || t0 + i >= at.n) {
                 a[i] = 1.0f;
                 u[i] = 0.0f;
@@ -694,7 +699,7 @@ __global__ void __launch_bounds__(kGatedThreads)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float a, u;
-            gated_terms<kLog>(f[i] + bias, x8[i], a, u);
+            gated_terms<kLog>(f[i], bias, x8[i], a, u);
             if (t0 + i < 0 || t0 + i >= at.n) {
                 a = 1.0f;
                 u = 0.0f;
@@ -721,12 +726,7 @@ __global__ void __launch_bounds__(kGatedThreads)
         float A = 1.0f, H = 0.0f, At, Ht;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if constexpr (kLog) {
-                a[i] = exp2_near_one_exact((a[i] + bias) * kLog2e);
-                g[i] = 1.0f;
-            } else {
-                sigmoid_gate(a[i] + bias, g[i], a[i]);
-            }
+            gated_gains<kLog>(a[i], bias, g[i], a[i]);
             if (t0 + i < 0 || t0 + i >= at.n) {
                 a[i] = 1.0f;
                 g[i] = 0.0f;
@@ -820,14 +820,14 @@ __global__ void __launch_bounds__(kGatedUpdateThreads)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             float a, u;
-            gated_terms<kLog>(f[k] + bias[k], v[k], a, u);
+            gated_terms<kLog>(f[k], bias[k], v[k], a, u);
             h[k] = fmaf(a, h[k], u);
         }
         store_steps(state, 0, 0, 8, h);
         store_steps(out, 0, 0, 8, h);
     } else {
         float a, u;
-        gated_terms<kLog>(DType<IoT>::load(gate) + (p.bias != nullptr ? p.bias[d] : 0.0f),
+        gated_terms<kLog>(DType<IoT>::load(gate), p.bias != nullptr ? p.bias[d] : 0.0f,
                           DType<IoT>::load(x), a, u);
         const float h = fmaf(a, *state, u);
         *state = h;

@@ -20,7 +20,7 @@ def lib():
 
 
 def gated_dims(**kw):
-    d = ops.GatedDims(batch=2, dim=64, seqlen=128, io_dtype=ops.MAMBA_BF16, flags=BLD)
+    d = ops.GatedDims(batch=2, dim=64, seqlen=1024, io_dtype=ops.MAMBA_BF16, flags=BLD)
     for k, v in kw.items():
         setattr(d, k, v)
     return d
@@ -84,9 +84,9 @@ def test_gated_empty_problems_need_nothing(lib):
 def test_gated_workspace_sizes(lib):
     size = lambda **kw: lib.mamba_gated_scan_workspace_bytes(ctypes.byref(gated_dims(**kw)))  # noqa: E731
     bwd = lambda have, **kw: lib.mamba_gated_scan_bwd_workspace_bytes(ctypes.byref(gated_dims(**kw)), have)  # noqa: E731
-    assert size(seqlen=64) == 0                    # one tile per chain: nothing to hand on
+    assert size(seqlen=512) == 0                   # one segment per chain: nothing to hand on
     assert size(flags=0, seqlen=100000) == 0       # a chain stays with its warps
-    assert size(seqlen=65) > 0
+    assert size(seqlen=513) > 0
     assert bwd(0) > bwd(1) > 0
     none = ctypes.c_size_t(-1).value
     assert size(batch=-1) == none and bwd(0, io_dtype=9) == none
