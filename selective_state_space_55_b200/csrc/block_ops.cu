@@ -8,6 +8,7 @@
 #include "layer_norm.cuh"
 #include "conv1d_backward.cuh"
 #include "gated_scan.cuh"
+#include "gated_chain.cuh"
 
 namespace mamba {
 
@@ -164,7 +165,19 @@ struct GatedLayout {           // offsets in the workspace, bytes
     int64_t blocks, segments, groups_per_row, groups, items;
     int64_t tiles;
     int warps, width;          // (batch, seqlen, dim): blocks per segment; else warps and lanes per chain
+    // chained stretches
+    size_t chain_zeroed, chain_zeroed_bytes, chain_handoff, chain_bias;
+    int64_t chain_groups, chain_stretches, chain_stretch_tiles;
 };
+
+#ifndef CHAINMIN
+#define CHAINMIN 128
+#endif
+#ifndef CHAINK
+#define CHAINK 4
+#endif
+constexpr int64_t kChainMinGroups = CHAINMIN;
+constexpr int64_t kChainResident = 2 * 148;      // CTAs that a B200 holds
 
 // One segment per chain needs no look-back: no tickets, flags or maps.
 mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool recompute, int phase_max,
@@ -186,11 +199,26 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
             w->flags = take((size_t)w->items * sizeof(unsigned int));
             if (backward && recompute) w->flags2 = take((size_t)w->items * sizeof(unsigned int));
             w->zeroed = off;
-            w->maps = take((size_t)w->items * 32 * sizeof(float4));
-            w->joins = take((size_t)w->groups * ((w->segments + kGatedJoin - 1) / kGatedJoin) * 32 * sizeof(float2));
+            w->maps = take((size_t)w->items * 64 * sizeof(float4));
+            w->joins = take((size_t)w->groups * ((w->segments + kGatedJoin - 1) / kGatedJoin) * 32 * sizeof(float4));
         }
         if (backward && recompute) w->enter = take((size_t)d->batch * w->blocks * d->dim * sizeof(float));
         if (backward) w->bias = take((size_t)d->batch * w->segments * d->dim * sizeof(float));
+        // Chained stretches: some CHAINK items per resident CTA, 8 tiles or more each.
+        w->chain_groups = d->batch * ((d->dim + kChainChannels - 1) / kChainChannels);
+        const int64_t want = (CHAINK * kChainResident + w->chain_groups - 1) / w->chain_groups;
+        w->chain_stretches = std::max<int64_t>(1, std::min<int64_t>(want, w->blocks / 8));
+        w->chain_stretch_tiles = (w->blocks + w->chain_stretches - 1) / w->chain_stretches;
+        w->chain_stretches = (w->blocks + w->chain_stretch_tiles - 1) / w->chain_stretch_tiles;
+        const size_t items = (size_t)w->chain_groups * w->chain_stretches;
+        if (w->chain_groups >= kChainMinGroups && items < (size_t)kLimit31 / 2) {
+            if (w->chain_stretches > 1) {
+                w->chain_zeroed = take(256 + items * sizeof(unsigned int));
+                w->chain_zeroed_bytes = 256 + items * sizeof(unsigned int);
+                w->chain_handoff = take(items * kChainChannels * sizeof(float));
+            }
+            if (backward) w->chain_bias = take((size_t)d->batch * w->chain_stretches * d->dim * sizeof(float));
+        }
     } else {
         // Lanes take 8 steps each; the row's start may lie up to phase_max steps into its tile.
         const int64_t span = L + phase_max;
@@ -216,14 +244,21 @@ template <typename IoT, bool kLog, bool kVec, bool kBackward>
 cudaError_t launch_gated_tiles(const GatedParams& prm, int warps, int dev, int sms, cudaStream_t stream) {
     static int resident[kMaxDevices] = {0};
     auto kernel = gated_scan_fwd_kernel<IoT, kLog, kVec>;
-    if constexpr (kBackward) kernel = gated_scan_bwd_kernel<IoT, kLog, kVec>;
+    size_t smem = 0;
+    if constexpr (kBackward) {
+        static bool attr_done[kMaxDevices] = {false};
+        kernel = gated_scan_bwd_kernel<IoT, kLog, kVec>;
+        const cudaError_t e = ensure_smem_attr(kernel, kGatedBwdSmem, attr_done, dev);
+        if (e != cudaSuccess) return e;
+        smem = (size_t)kGatedBwdSmem / kGatedWarps * warps;
+    }
     int64_t grid = prm.items;
     if (prm.ticket != nullptr) {        // several segments: CTAs that stay and take one after another
-        const int per_sm = resident_ctas(kernel, kGatedThreads, 0, resident, dev);
+        const int per_sm = resident_ctas(kernel, kGatedThreads, smem, resident, dev);
         if (per_sm <= 0) return cudaErrorInvalidConfiguration;
         grid = std::min<int64_t>(grid, (int64_t)per_sm * sms);
     }
-    kernel<<<(unsigned)grid, warps * 32, 0, stream>>>(prm);
+    kernel<<<(unsigned)grid, warps * 32, smem, stream>>>(prm);
     return cudaGetLastError();
 }
 
@@ -243,6 +278,105 @@ cudaError_t dispatch_gated_tiles(const GatedParams& prm, int warps, bool bf16, b
                    : launch_gated_tiles<float, true, false, kBackward>(prm, warps, dev, sms, stream);
     return vec ? launch_gated_tiles<float, false, true, kBackward>(prm, warps, dev, sms, stream)
                : launch_gated_tiles<float, false, false, kBackward>(prm, warps, dev, sms, stream);
+}
+
+// Can TMA move boxes of this tensor?  16-byte base and distances.
+bool chain_tensor_ok(const void* p, const GatedStrides& s, int es, int64_t batch) {
+    return aligned(p, 16) && (s.row * es) % 16 == 0 && s.row * es < ((int64_t)1 << 40) &&
+           (batch == 1 || ((s.batch * es) % 16 == 0 && s.batch * es < ((int64_t)1 << 40)));
+}
+
+bool encode_chain_map(CUtensorMap* map, const void* base, const GatedStrides& s, const mamba_gated_dims_t* d,
+                      int es, uint32_t steps) {
+    auto encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d->dim, (cuuint64_t)d->seqlen, (cuuint64_t)d->batch};
+    const cuuint64_t row = (cuuint64_t)s.row * es;
+    const cuuint64_t strides[2] = {row, d->batch > 1 ? (cuuint64_t)s.batch * es : row};
+    const cuuint32_t box[3] = {(cuuint32_t)kChainChannels, steps, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The states entering tiles, (batch, tiles, dim) fp32, one tile's 64 channels per box.
+bool encode_chain_states(CUtensorMap* map, const float* base, int64_t dim, int64_t tiles, int64_t batch) {
+    auto encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)tiles, (cuuint64_t)batch};
+    const cuuint64_t strides[2] = {(cuuint64_t)dim * 4, (cuuint64_t)(dim * tiles) * 4};
+    const cuuint32_t box[3] = {(cuuint32_t)kChainChannels, 1, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename IoT, bool kLog, bool kBackward>
+cudaError_t launch_gated_chain(const ChainParams& prm, int dev, int sms, cudaStream_t stream) {
+    static int resident[kMaxDevices] = {0};
+    static bool attr_done[kMaxDevices] = {false};
+    auto kernel = gated_chain_fwd_kernel<IoT, kLog>;
+    if constexpr (kBackward) kernel = gated_chain_bwd_kernel<IoT, kLog>;
+    constexpr int smem = (int)sizeof(ChainShared<IoT, kBackward>);
+    const cudaError_t e = ensure_smem_attr(kernel, smem, attr_done, dev);
+    if (e != cudaSuccess) return e;
+    int64_t grid = prm.items;
+    if (prm.ticket != nullptr) {
+        const int per_sm = resident_ctas(kernel, kChainThreads, smem, resident, dev);
+        if (per_sm <= 0) return cudaErrorInvalidConfiguration;
+        grid = std::min<int64_t>(grid, (int64_t)per_sm * sms);
+    }
+    kernel<<<(unsigned)grid, kChainThreads, smem, stream>>>(prm);
+    return cudaGetLastError();
+}
+
+// The chained kernels: what the tile kernels' parameters say, with TMA maps.
+template <bool kBackward>
+mamba_status_t run_gated_chain(const GatedParams& g, const GatedLayout& w, const mamba_gated_dims_t* d, uint8_t* ws,
+                               int dev, int sms, cudaStream_t stream) {
+    const int es = dtype_bytes(d->io_dtype);
+    ChainParams prm{};
+    bool ok = encode_chain_map(&prm.gate, g.gate, g.gate_s, d, es, kChainTile) &&
+              encode_chain_map(&prm.x, g.x, g.x_s, d, es, kChainTile);
+    if (kBackward)
+        ok = ok && encode_chain_map(&prm.dout, g.dout, g.out_s, d, es, kChainTile) &&
+             encode_chain_map(&prm.out0, g.dgate, g.dgate_s, d, es, kChainSteps) &&
+             encode_chain_map(&prm.out1, g.dx, g.dx_s, d, es, kChainSteps) &&
+             encode_chain_states(&prm.states, g.enter, d->dim, w.blocks, d->batch);
+    else
+        ok = ok && encode_chain_map(&prm.out0, g.out, g.out_s, d, es, kChainSteps);
+    if (!ok) return MAMBA_ERR_CUDA;
+    prm.bias = g.bias;
+    prm.h0 = g.h0;
+    prm.dlast = g.dlast;
+    prm.seqlens = g.seqlens;
+    prm.last = kBackward ? g.dh0 : g.last;
+    prm.enter = g.enter;
+    prm.bias_partial = kBackward && g.bias_partial != nullptr ? reinterpret_cast<float*>(ws + w.chain_bias) : nullptr;
+    prm.dim = d->dim;
+    prm.seqlen = d->seqlen;
+    prm.tiles = w.blocks;
+    prm.groups_per_row = (d->dim + kChainChannels - 1) / kChainChannels;
+    prm.groups = w.chain_groups;
+    prm.stretch_tiles = w.chain_stretch_tiles;
+    prm.stretches = w.chain_stretches;
+    prm.items = prm.groups * prm.stretches;
+    prm.withhold = g.withhold;
+    if (prm.stretches > 1) {
+        prm.ticket = reinterpret_cast<unsigned int*>(ws + w.chain_zeroed);
+        prm.flags = reinterpret_cast<unsigned int*>(ws + w.chain_zeroed + 256);
+        prm.handoff = reinterpret_cast<float*>(ws + w.chain_handoff);
+        if (cudaMemsetAsync(ws + w.chain_zeroed, 0, w.chain_zeroed_bytes, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
+    }
+    const bool log_decay = d->log_decay != 0;
+    if (d->io_dtype == MAMBA_BF16)
+        return status_of(log_decay ? launch_gated_chain<__nv_bfloat16, true, kBackward>(prm, dev, sms, stream)
+                                   : launch_gated_chain<__nv_bfloat16, false, kBackward>(prm, dev, sms, stream));
+    return status_of(log_decay ? launch_gated_chain<float, true, kBackward>(prm, dev, sms, stream)
+                               : launch_gated_chain<float, false, kBackward>(prm, dev, sms, stream));
 }
 
 template <typename IoT, bool kLog, bool kBackward>
@@ -320,7 +454,7 @@ void gated_apply_layout(const GatedLayout& w, uint8_t* ws, GatedParams* prm) {
     prm->ticket = w.zeroed ? reinterpret_cast<unsigned int*>(ws + w.tickets) : nullptr;
     prm->flags = reinterpret_cast<unsigned int*>(ws + w.flags);
     prm->maps = reinterpret_cast<float4*>(ws + w.maps);
-    prm->states = reinterpret_cast<float2*>(ws + w.joins);
+    prm->states = reinterpret_cast<float4*>(ws + w.joins);
 }
 
 mamba_status_t check_workspace(const void* ws, size_t have, size_t need) {
@@ -630,12 +764,15 @@ MAMBA_API mamba_status_t mamba_gated_scan_fwd(const void* gate, const void* x, c
     int dev = 0;
     const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
-    if (w.zeroed && cudaMemsetAsync(ws, 0, w.zeroed, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
     prm.enter = checkpoints;
-    const bool vec = dims->dim % 2 == 0 && rows_aligned(gate, prm.gate_s, es, 2 * es) &&
-                     rows_aligned(x, prm.x_s, es, 2 * es) && rows_aligned(out, prm.out_s, es, 2 * es) &&
-                     (!gate_bias || aligned(gate_bias, 8)) && (!initial_state || aligned(initial_state, 8)) &&
-                     (!last_state || aligned(last_state, 8)) && (!checkpoints || aligned(checkpoints, 8));
+    if (w.chain_groups >= kChainMinGroups && chain_tensor_ok(gate, prm.gate_s, es, dims->batch) &&
+        chain_tensor_ok(x, prm.x_s, es, dims->batch) && chain_tensor_ok(out, prm.out_s, es, dims->batch))
+        return run_gated_chain<false>(prm, w, dims, ws, dev, sms, stream);
+    if (w.zeroed && cudaMemsetAsync(ws, 0, w.zeroed, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
+    const bool vec = dims->dim % 4 == 0 && rows_aligned(gate, prm.gate_s, es, 4 * es) &&
+                     rows_aligned(x, prm.x_s, es, 4 * es) && rows_aligned(out, prm.out_s, es, 4 * es) &&
+                     (!gate_bias || aligned(gate_bias, 16)) && (!initial_state || aligned(initial_state, 16)) &&
+                     (!last_state || aligned(last_state, 16)) && (!checkpoints || aligned(checkpoints, 16));
     return status_of(dispatch_gated_tiles<false>(prm, w.warps, bf16, log_decay, vec, dev, sms, stream));
 }
 
@@ -710,9 +847,9 @@ MAMBA_API mamba_status_t mamba_gated_scan_bwd(
     const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
     if (w.zeroed && cudaMemsetAsync(ws, 0, w.zeroed, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
-    const bool vec_in = dims->dim % 2 == 0 && rows_aligned(gate, prm.gate_s, es, 2 * es) &&
-                        rows_aligned(x, prm.x_s, es, 2 * es) && (!gate_bias || aligned(gate_bias, 8)) &&
-                        (!initial_state || aligned(initial_state, 8));
+    const bool vec_in = dims->dim % 4 == 0 && rows_aligned(gate, prm.gate_s, es, 4 * es) &&
+                        rows_aligned(x, prm.x_s, es, 4 * es) && (!gate_bias || aligned(gate_bias, 16)) &&
+                        (!initial_state || aligned(initial_state, 16));
     if (recompute) {                    // the forward's states, no outputs
         GatedParams fwd = prm;
         fwd.out = nullptr;
@@ -728,10 +865,19 @@ MAMBA_API mamba_status_t mamba_gated_scan_bwd(
     } else {
         prm.enter = const_cast<float*>(checkpoints);
     }
-    const bool vec = vec_in && rows_aligned(dout, prm.out_s, es, 2 * es) &&
-                     rows_aligned(dgate, prm.dgate_s, es, 2 * es) && rows_aligned(dx, prm.dx_s, es, 2 * es) &&
-                     (!dlast_state || aligned(dlast_state, 8)) && (!dinitial_state || aligned(dinitial_state, 8)) &&
-                     (!checkpoints || aligned(checkpoints, 8));
+    if (w.chain_groups >= kChainMinGroups && chain_tensor_ok(gate, prm.gate_s, es, dims->batch) &&
+        chain_tensor_ok(x, prm.x_s, es, dims->batch) && chain_tensor_ok(dout, prm.out_s, es, dims->batch) &&
+        chain_tensor_ok(dgate, prm.dgate_s, es, dims->batch) && chain_tensor_ok(dx, prm.dx_s, es, dims->batch) &&
+        dims->dim % 4 == 0 && aligned(prm.enter, 16)) {
+        st = run_gated_chain<true>(prm, w, dims, ws, dev, sms, stream);
+        if (st != MAMBA_OK || dgate_bias == nullptr) return st;
+        return status_of(launch_column_sum(reinterpret_cast<float*>(ws + w.chain_bias), dims->batch * w.chain_stretches,
+                                           dims->dim, dims->dim, dgate_bias, nullptr, stream));
+    }
+    const bool vec = vec_in && rows_aligned(dout, prm.out_s, es, 4 * es) &&
+                     rows_aligned(dgate, prm.dgate_s, es, 4 * es) && rows_aligned(dx, prm.dx_s, es, 4 * es) &&
+                     (!dlast_state || aligned(dlast_state, 16)) && (!dinitial_state || aligned(dinitial_state, 16)) &&
+                     (!checkpoints || aligned(checkpoints, 16));
     e = dispatch_gated_tiles<true>(prm, w.warps, bf16, log_decay, vec, dev, sms, stream);
     if (e == cudaSuccess && dgate_bias != nullptr)
         e = launch_column_sum(prm.bias_partial, dims->batch * w.segments, dims->dim, dims->dim, dgate_bias, nullptr, stream);

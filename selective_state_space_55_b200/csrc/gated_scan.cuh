@@ -22,14 +22,14 @@
 // long as the step's arithmetic (two special-function operations for the
 // sigmoid, one for the log decay) and the joins stay below the issue rate.
 //
-// Layout (batch, seqlen, dim): a warp takes a block of 64 steps of 64 channels
-// (a lane two neighbours: rows of 128 or 256 bytes per access), up to 8 warps
+// Layout (batch, seqlen, dim): a warp takes a block of 64 steps of 128 channels
+// (a lane four neighbours: rows of 256 or 512 bytes per access), up to 8 warps
 // side by side in time make a segment of 512 steps.  Phase one walks the block
 // and keeps only its map; the segment's maps are composed through shared
 // memory; segments of a chain are joined by a look-back in fixed groups of 8,
 // so that every state is composed in the same order whatever the timing.  Phase
-// two walks the block again from its true start: its inputs come from L1 and
-// L2 (a segment is 128 KB in bf16, some 70 MB over all resident CTAs), so HBM
+// two walks the block again from its true start: its inputs come from L2 (a
+// segment is 256 KB in bf16), so HBM
 // sees each input once.  The steps' arithmetic is done twice in exchange, in
 // packed fp32x2.  Segments are handed out by a counter, the earliest steps of
 // all chains first, so that every segment's predecessors belong to CTAs that
@@ -48,7 +48,7 @@ namespace mamba {
 
 constexpr int kGatedBlock = 64;                             // steps per warp
 constexpr int kGatedWarps = 8;                              // blocks per segment, at most
-constexpr int kGatedChannels = 64;                          // per CTA, two per lane
+constexpr int kGatedChannels = 128;                         // per CTA, four per lane
 constexpr int kGatedThreads = kGatedWarps * 32;
 constexpr int kGatedJoin = 8;                               // segments folded from one known state
 static_assert(kGatedBlock == MAMBA_GATED_CHECKPOINT_STEPS, "checkpoints are the states entering blocks");
@@ -71,8 +71,8 @@ struct GatedParams {
     float* bias_partial;          // bwd: [batch * segments][dim] (seqlen fastest: [batch][dim]) or null
     // (batch, seqlen, dim)
     float* enter;                 // [batch][blocks][dim], states entering blocks; fwd: written or null
-    float4* maps;                 // [groups][segments][32]: a lane's two (A, H) pairs
-    float2* states;               // [groups][segments / kGatedJoin][32]: states entering a join group
+    float4* maps;                 // [groups][segments][A | H][32]: of a lane's four channels
+    float4* states;               // [groups][segments / kGatedJoin][32]: states entering a join group
     unsigned int* flags;          // [groups][segments]: 0, 1 = map published, 2 = state published
     unsigned int* ticket;         // null: one segment per chain, one CTA per segment
     // (batch, dim, seqlen), bwd: states entering tiles, [chains][tiles]
@@ -81,7 +81,7 @@ struct GatedParams {
     int64_t batch, dim, seqlen, chains;
     int64_t blocks;               // of 64 steps, per chain
     int64_t segments;             // per chain
-    int64_t groups_per_row;       // 64-channel groups per batch row
+    int64_t groups_per_row;       // 128-channel groups per batch row
     int64_t groups;
     int64_t items;                // groups * segments
     int64_t tiles;                // (batch, dim, seqlen): per chain
@@ -90,10 +90,10 @@ struct GatedParams {
 
 constexpr unsigned int kGatedPollLimit = 1u << 19;
 
-// g and a of the sigmoid gate from f log2(e); a = 1 - g to fp32 on both sides.
-// With e = exp(-|f|), small = e / (1 + e) is the smaller of the two and the
-// other is 1 - small, rounded to nearest: a decay close to 1 is applied over
-// about 1 / g steps, and a biased rounding would grow with that memory.
+// g and a of the sigmoid gate from f log2(e).  With e = exp(-f): g = 1 / (1 + e),
+// and a = e g for f >= 0, 1 - g (rounded to nearest) for f < 0: there a is close
+// to 1, it is applied over about 1 / g steps, and a biased rounding would grow
+// with that memory.  e = inf gives g = 0, a = 1.
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -102,11 +102,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 __device__ __forceinline__ void sigmoid_gate2(float2 f2, float2& g, float2& a) {
     const float2 one = make_float2(1.0f, 1.0f);
-    const float2 e = make_float2(ex2_approx(-fabsf(f2.x)), ex2_approx(-fabsf(f2.y)));
+    const float2 e = make_float2(ex2_approx(-f2.x), ex2_approx(-f2.y));
     const float2 d = __fadd2_rn(e, one);
-    const float2 small = __fmul2_rn(e, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
-    const float2 big = __ffma2_rn(small, make_float2(-1.0f, -1.0f), one);
-    g = make_float2(f2.x < 0.0f ? small.x : big.x, f2.y < 0.0f ? small.y : big.y);
+    g = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    const float2 small = __fmul2_rn(e, g);
+    const float2 big = __ffma2_rn(g, make_float2(-1.0f, -1.0f), one);
     a = make_float2(f2.x < 0.0f ? big.x : small.x, f2.y < 0.0f ? big.y : small.y);
 }
 
@@ -164,93 +164,157 @@ __device__ __forceinline__ void store_release(unsigned int* p, unsigned int v) {
 
 // ------------------------------------------------ (batch, seqlen, dim) layout
 
-// Two neighbouring channels of one step; raw bits so that a tile can be
-// requested while the previous one is being worked on.  kVec: both lie in one
-// aligned word; otherwise element by element (c1 says whether the second exists).
-template <typename IoT> struct Pair;
-template <> struct Pair<__nv_bfloat16> {
-    uint32_t v;
-    __device__ __forceinline__ float2 get() const {
-        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+constexpr int kGatedPairs = kGatedChannels / 64;            // pairs of channels per lane
+
+// A lane's channels of one step, as fp32 pairs.  kVec: four neighbours in one
+// aligned word; otherwise channels lane, lane + 32, ... so that single elements
+// still coalesce.
+struct Channels {
+    int64_t d;                    // this lane's first channel
+    int live;                     // how many of its channels exist
+};
+
+template <bool kVec>
+__device__ __forceinline__ Channels gated_channels(int64_t first, int64_t dim, int lane) {
+    Channels c;
+    const int64_t left = dim - first;
+    if constexpr (kVec) {         // dim is a multiple of 4: all or none
+        c.d = first + 4 * lane;
+        c.live = c.d < dim ? 4 : 0;
+    } else {
+        c.d = first + lane;
+        c.live = left <= lane ? 0 : (int)((left - lane + 31) / 32);
+        c.live = c.live > 4 ? 4 : c.live;
+    }
+    return c;
+}
+
+template <typename IoT> struct Quad;
+template <> struct Quad<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ float2 get(int k) const {
+        const uint32_t w = k == 0 ? v.x : v.y;
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
 };
-template <> struct Pair<float> {
-    float2 v;
-    __device__ __forceinline__ float2 get() const { return v; }
+template <> struct Quad<float> {
+    float4 v;
+    __device__ __forceinline__ float2 get(int k) const {
+        return k == 0 ? make_float2(v.x, v.y) : make_float2(v.z, v.w);
+    }
 };
 
 template <typename IoT, bool kVec>
-__device__ __forceinline__ Pair<IoT> load_pair(const IoT* p, bool c0, bool c1) {
-    Pair<IoT> r;
+__device__ __forceinline__ Quad<IoT> load_quad(const IoT* p, int live) {
+    Quad<IoT> r;
     if constexpr (sizeof(IoT) == 2) {
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-        if constexpr (kVec) r.v = c0 ? *reinterpret_cast<const uint32_t*>(p) : 0u;
-        else r.v = (c0 ? (uint32_t)q[0] : 0u) | ((c1 ? (uint32_t)q[1] : 0u) << 16);
+        if constexpr (kVec) {
+            r.v = live > 0 ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
+        } else {
+            const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+            r.v.x = (live > 0 ? (uint32_t)q[0] : 0u) | ((live > 1 ? (uint32_t)q[32] : 0u) << 16);
+            r.v.y = (live > 2 ? (uint32_t)q[64] : 0u) | ((live > 3 ? (uint32_t)q[96] : 0u) << 16);
+        }
     } else {
-        if constexpr (kVec) r.v = c0 ? *reinterpret_cast<const float2*>(p) : make_float2(0.0f, 0.0f);
-        else r.v = make_float2(c0 ? p[0] : 0.0f, c1 ? p[1] : 0.0f);
+        if constexpr (kVec)
+            r.v = live > 0 ? *reinterpret_cast<const float4*>(p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        else
+            r.v = make_float4(live > 0 ? p[0] : 0.0f, live > 1 ? p[32] : 0.0f, live > 2 ? p[64] : 0.0f,
+                              live > 3 ? p[96] : 0.0f);
     }
     return r;
 }
 
 template <typename IoT, bool kVec>
-__device__ __forceinline__ void store_pair(IoT* p, bool c0, bool c1, float2 v) {
+__device__ __forceinline__ void store_quad(IoT* p, int live, float2 a, float2 b) {
     if constexpr (kVec) {
-        if (!c0) return;
-        if constexpr (sizeof(IoT) == 2) *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
-        else *reinterpret_cast<float2*>(p) = v;
+        if (live == 0) return;
+        if constexpr (sizeof(IoT) == 2)
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
+        else
+            *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
     } else {
-        if (c0) DType<IoT>::store(p, v.x);
-        if (c1) DType<IoT>::store(p + 1, v.y);
+        if (live > 0) DType<IoT>::store(p, a.x);
+        if (live > 1) DType<IoT>::store(p + 32, a.y);
+        if (live > 2) DType<IoT>::store(p + 64, b.x);
+        if (live > 3) DType<IoT>::store(p + 96, b.y);
     }
 }
 
-// An fp32 pair of a (.., dim) array.
-template <bool kVec>
-__device__ __forceinline__ float2 load_f2(const float* p, bool c0, bool c1) {
-    if constexpr (kVec) return c0 ? __ldcg(reinterpret_cast<const float2*>(p)) : make_float2(0.0f, 0.0f);
-    else return make_float2(c0 ? __ldcg(p) : 0.0f, c1 ? __ldcg(p + 1) : 0.0f);
+// kN steps; steps from `left` on are not read and give 0.
+template <typename IoT, bool kVec, int kN>
+__device__ __forceinline__ void load_quads(Quad<IoT> (&r)[kN], const IoT* p, int64_t stride, int left, int live) {
+    if (left >= kN) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) r[i] = load_quad<IoT, kVec>(p + i * stride, live);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) r[i] = load_quad<IoT, kVec>(p + i * stride, i < left ? live : 0);
+    }
 }
 
-template <bool kVec>
-__device__ __forceinline__ void store_f2(float* p, bool c0, bool c1, float2 v) {
-    store_pair<float, kVec>(p, c0, c1, v);
+// Affine maps of a lane's four channels.
+struct Maps { float2 A[kGatedPairs], H[kGatedPairs]; };
+static_assert(kGatedPairs == 2, "four channels per lane");
+
+__device__ __forceinline__ Maps identity_maps() {
+    Maps m;
+#pragma unroll
+    for (int k = 0; k < kGatedPairs; ++k) {
+        m.A[k] = make_float2(1.0f, 1.0f);
+        m.H[k] = make_float2(0.0f, 0.0f);
+    }
+    return m;
+}
+
+// first, then second
+__device__ __forceinline__ Maps compose(const Maps& first, const Maps& second) {
+    Maps m;
+#pragma unroll
+    for (int k = 0; k < kGatedPairs; ++k) {
+        m.A[k] = __fmul2_rn(second.A[k], first.A[k]);
+        m.H[k] = __ffma2_rn(second.A[k], first.H[k], second.H[k]);
+    }
+    return m;
+}
+
+struct MapStore { float4 A, H; };
+
+__device__ __forceinline__ MapStore pack_maps(const Maps& m) {
+    return {make_float4(m.A[0].x, m.A[0].y, m.A[1].x, m.A[1].y), make_float4(m.H[0].x, m.H[0].y, m.H[1].x, m.H[1].y)};
+}
+
+__device__ __forceinline__ Maps unpack_maps(const float4& A, const float4& H) {
+    Maps m;
+    m.A[0] = make_float2(A.x, A.y);
+    m.A[1] = make_float2(A.z, A.w);
+    m.H[0] = make_float2(H.x, H.y);
+    m.H[1] = make_float2(H.z, H.w);
+    return m;
 }
 
 // Where a warp's block lies: item = position * groups + group, positions in the
 // order of the scan (kReverse: the last segment of a chain first).
 struct GatedBlockAt {
-    int64_t b, group, pos, segment, block, t, d;    // t: first step; d: this lane's first channel
+    int64_t b, group, pos, segment, block, t;
+    Channels c;
     int left, rows;                                 // steps inside the sequence, inside the tensor
 };
 
-template <bool kReverse>
+template <bool kReverse, bool kVec>
 __device__ __forceinline__ GatedBlockAt gated_block(const GatedParams& p, int64_t item, int warp, int lane) {
     GatedBlockAt at;
     at.pos = item / p.groups;
     at.group = item - at.pos * p.groups;
     at.segment = kReverse ? p.segments - 1 - at.pos : at.pos;
     at.b = at.group / p.groups_per_row;
-    at.d = (at.group - at.b * p.groups_per_row) * kGatedChannels + 2 * lane;
+    at.c = gated_channels<kVec>((at.group - at.b * p.groups_per_row) * kGatedChannels, p.dim, lane);
     at.block = at.segment * (blockDim.x >> 5) + warp;
     at.t = at.block * kGatedBlock;
     const int64_t n = gated_length(p, at.b) - at.t, rows = p.seqlen - at.t;
     at.left = (int)(n < 0 ? 0 : (n > kGatedBlock ? kGatedBlock : n));
     at.rows = (int)(rows < 0 ? 0 : (rows > kGatedBlock ? kGatedBlock : rows));
     return at;
-}
-
-// kN steps of two channels; steps from `left` on are not read and give 0.
-template <typename IoT, bool kVec, int kN>
-__device__ __forceinline__ void load_pairs(Pair<IoT> (&r)[kN], const IoT* p, int64_t stride, int left,
-                                           bool c0, bool c1) {
-    if (left >= kN) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) r[i] = load_pair<IoT, kVec>(p + i * stride, c0, c1);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) r[i] = load_pair<IoT, kVec>(p + i * stride, i < left && c0, i < left && c1);
-    }
 }
 
 // Publishing: every lane has written its part; lane 0 raises the flag.
@@ -264,22 +328,24 @@ __device__ __forceinline__ void gated_publish(const GatedParams& p, unsigned int
 }
 
 // The state entering segment `pos` of a chain (positions in scan order) for
-// this lane's two channels; called by one warp with the segment's own map.
+// this lane's channels; called by one warp with the segment's own map.
 // Positions form groups of kGatedJoin.  The last of a group publishes the state
 // that leaves it, the others their maps; a segment waits for the state entering
 // its group and the maps of the group's earlier segments, and folds them in
-// order.  `start` is the state entering position 0.
-__device__ __forceinline__ float2 gated_join(const GatedParams& p, int64_t group, int64_t pos, int lane,
-                                             float4 map, float2 start) {
+// order.  h is the state entering position 0 and becomes the one entering pos.
+__device__ __forceinline__ void gated_join(const GatedParams& p, int64_t group, int64_t pos, int lane,
+                                           const Maps& map, float2 (&h)[kGatedPairs]) {
     const int64_t join = pos / kGatedJoin, first = join * kGatedJoin;
     const int before = (int)(pos - first);
     unsigned int* flags = p.flags + group * p.segments;
-    float4* maps = p.maps + (group * p.segments) * 32 + lane;
+    float4* maps = p.maps + (group * p.segments) * 64 + lane;       // [segment][A | H][lane]
     const int64_t joins = (p.segments + kGatedJoin - 1) / kGatedJoin;
-    float2* states = p.states + (group * joins) * 32 + lane;
+    float4* states = p.states + (group * joins) * 32 + lane;
     const bool closes = before == kGatedJoin - 1;
     if (!closes && pos + 1 < p.segments) {
-        __stcg(maps + pos * 32, map);
+        const MapStore m = pack_maps(map);
+        __stcg(maps + pos * 64, m.A);
+        __stcg(maps + pos * 64 + 32, m.H);
         gated_publish(p, flags + pos, lane, 1u);
     }
     // lane l < before waits for the map of segment first + l, lane kGatedJoin for the state
@@ -291,30 +357,32 @@ __device__ __forceinline__ float2 gated_join(const GatedParams& p, int64_t group
         if (!ready) ready = load_acquire(mine) >= (wait_state ? 2u : 1u);
         if (__all_sync(0xffffffffu, ready)) break;
     }
-    float2 h = start;
     if (poll == kGatedPollLimit) {
         if (lane == 0) record_device_error(MAMBA_ERR_TIMEOUT);
     } else {
-        float4 m[kGatedJoin - 1];
-#pragma unroll
-        for (int i = 0; i < kGatedJoin - 1; ++i)
-            m[i] = i < before ? __ldcg(maps + (first + i) * 32) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-        if (join > 0) h = __ldcg(states + join * 32);
+        if (join > 0) {
+            const float4 v = __ldcg(states + join * 32);
+            h[0] = make_float2(v.x, v.y);
+            h[1] = make_float2(v.z, v.w);
+        }
 #pragma unroll
         for (int i = 0; i < kGatedJoin - 1; ++i)
             if (i < before) {
-                h.x = fmaf(m[i].x, h.x, m[i].y);
-                h.y = fmaf(m[i].z, h.y, m[i].w);
+                const Maps m = unpack_maps(__ldcg(maps + (first + i) * 64), __ldcg(maps + (first + i) * 64 + 32));
+#pragma unroll
+                for (int k = 0; k < kGatedPairs; ++k) h[k] = __ffma2_rn(m.A[k], h[k], m.H[k]);
             }
     }
     if (closes && pos + 1 < p.segments) {
-        __stcg(states + (join + 1) * 32, make_float2(fmaf(map.x, h.x, map.y), fmaf(map.z, h.y, map.w)));
+        float2 e[kGatedPairs];
+#pragma unroll
+        for (int k = 0; k < kGatedPairs; ++k) e[k] = __ffma2_rn(map.A[k], h[k], map.H[k]);
+        __stcg(states + (join + 1) * 32, make_float4(e[0].x, e[0].y, e[1].x, e[1].y));
         gated_publish(p, flags + pos, lane, 2u);
     }
-    return h;
 }
 
-// The next item of a CTA.  `slot` is written before a barrier and read after it.
+// The first item of a CTA.
 __device__ __forceinline__ int64_t gated_first_item(const GatedParams& p, int64_t* slot) {
     if (p.ticket == nullptr) return blockIdx.x;
     if (threadIdx.x == 0) *slot = atomicAdd(p.ticket, 1u);
@@ -322,230 +390,287 @@ __device__ __forceinline__ int64_t gated_first_item(const GatedParams& p, int64_
     return *slot;
 }
 
-constexpr int kGatedSub = 8;                 // steps requested at a time
+// Joins the warps' maps (in shared memory) and the segments': h, the state
+// entering position 0 of the chain, becomes the one entering this warp's block.
+template <bool kReverse>
+__device__ __forceinline__ void gated_enter(const GatedParams& p, const GatedBlockAt& at, int warp, int lane,
+                                            const float4 (&sA)[kGatedWarps][32], const float4 (&sH)[kGatedWarps][32],
+                                            float4 (&entering)[32], float2 (&h)[kGatedPairs]) {
+    const int warps = blockDim.x >> 5;
+    const int rank = kReverse ? warps - 1 - warp : warp;             // in scan order
+    if (p.ticket != nullptr && warp == 0) {
+        Maps all = identity_maps();
+        for (int v = 0; v < warps; ++v) {
+            const int w = kReverse ? warps - 1 - v : v;
+            all = compose(all, unpack_maps(sA[w][lane], sH[w][lane]));
+        }
+        float2 e[kGatedPairs] = {h[0], h[1]};
+        gated_join(p, at.group, at.pos, lane, all, e);
+        entering[lane] = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
+    }
+    Maps mine = identity_maps();
+    for (int v = 0; v < rank; ++v) {
+        const int w = kReverse ? warps - 1 - v : v;
+        mine = compose(mine, unpack_maps(sA[w][lane], sH[w][lane]));
+    }
+    if (p.ticket != nullptr) {
+        __syncthreads();
+        const float4 e = entering[lane];
+        h[0] = make_float2(e.x, e.y);
+        h[1] = make_float2(e.z, e.w);
+    }
+#pragma unroll
+    for (int k = 0; k < kGatedPairs; ++k) h[k] = __ffma2_rn(mine.A[k], h[k], mine.H[k]);
+}
+
+template <bool kVec>
+__device__ __forceinline__ void load_state(const float* base, int64_t row, int64_t dim, const Channels& c,
+                                           float2 (&h)[kGatedPairs]) {
+    if (base == nullptr) {
+        h[0] = h[1] = make_float2(0.0f, 0.0f);
+        return;
+    }
+    const Quad<float> q = load_quad<float, kVec>(base + row * dim + c.d, c.live);
+    h[0] = q.get(0);
+    h[1] = q.get(1);
+}
+
+#ifndef GSUB
+#define GSUB 4
+#endif
+#ifndef GFMIN
+#define GFMIN 4
+#endif
+#ifndef GBMIN
+#define GBMIN 2
+#endif
+constexpr int kGatedSub = GSUB;                 // steps requested at a time
 
 template <typename IoT, bool kLog, bool kVec>
-__global__ void __launch_bounds__(kGatedThreads)
+__global__ void __launch_bounds__(kGatedThreads, sizeof(IoT) == 2 ? GFMIN : GFMIN > 2 ? 2 : GFMIN)
     gated_scan_fwd_kernel(const __grid_constant__ GatedParams p) {
-    __shared__ float4 maps[kGatedWarps][32];
-    __shared__ float2 entering[32];
+    __shared__ float4 sA[kGatedWarps][32], sH[kGatedWarps][32];
+    __shared__ float4 entering[32];
     __shared__ int64_t first_slot, next_slot;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float2 zero = make_float2(0.0f, 0.0f), one = make_float2(1.0f, 1.0f);
     int64_t item = gated_first_item(p, &first_slot);
     while (item < p.items) {
-        const GatedBlockAt at = gated_block<false>(p, item, warp, lane);
-        const bool c0 = at.d < p.dim, c1 = at.d + 1 < p.dim;
-        float2 bias2 = p.bias != nullptr ? load_f2<kVec>(p.bias + at.d, c0, c1) : zero;
-        bias2 = __fmul2_rn(bias2, make_float2(kLog2e, kLog2e));
-        const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + at.t * p.gate_s.row + at.d;
-        const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.t * p.x_s.row + at.d;
-        float2 h = p.h0 != nullptr ? load_f2<kVec>(p.h0 + at.b * p.dim + at.d, c0, c1) : zero;
+        const GatedBlockAt at = gated_block<false, kVec>(p, item, warp, lane);
+        const int live = at.c.live;
+        float2 bias2[kGatedPairs], h[kGatedPairs];
+        load_state<kVec>(p.bias, 0, p.dim, at.c, bias2);
+        bias2[0] = __fmul2_rn(bias2[0], make_float2(kLog2e, kLog2e));
+        bias2[1] = __fmul2_rn(bias2[1], make_float2(kLog2e, kLog2e));
+        load_state<kVec>(p.h0, at.b, p.dim, at.c, h);
+        const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + at.t * p.gate_s.row + at.c.d;
+        const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.t * p.x_s.row + at.c.d;
         int64_t following = p.items;
         if (p.blocks > 1) {
             if (threadIdx.x == 0 && p.ticket != nullptr) next_slot = atomicAdd(p.ticket, 1u);
-            float2 A = one, H = zero;
+            Maps m = identity_maps();
+            const IoT* gs = gate;
+            const IoT* xs = x;
             for (int s = 0; s < at.left; s += kGatedSub) {
-                Pair<IoT> rf[kGatedSub], rx[kGatedSub];
-                load_pairs<IoT, kVec>(rf, gate + s * p.gate_s.row, p.gate_s.row, at.left - s, c0, c1);
-                load_pairs<IoT, kVec>(rx, x + s * p.x_s.row, p.x_s.row, at.left - s, c0, c1);
-                float2 a[kGatedSub], u[kGatedSub];
+                Quad<IoT> rf[kGatedSub], rx[kGatedSub];
+                load_quads<IoT, kVec>(rf, gs, p.gate_s.row, at.left - s, live);
+                load_quads<IoT, kVec>(rx, xs, p.x_s.row, at.left - s, live);
+                gs += kGatedSub * p.gate_s.row;
+                xs += kGatedSub * p.x_s.row;
+                float2 a[kGatedSub][kGatedPairs], u[kGatedSub][kGatedPairs];
 #pragma unroll
                 for (int i = 0; i < kGatedSub; ++i)
-                    gated_terms2<kLog>(rf[i].get(), bias2, rx[i].get(), a[i], u[i]);
+#pragma unroll
+                    for (int k = 0; k < kGatedPairs; ++k)
+                        gated_terms2<kLog>(rf[i].get(k), bias2[k], rx[i].get(k), a[i][k], u[i][k]);
                 if (at.left - s < kGatedSub)
 #pragma unroll
                     for (int i = 0; i < kGatedSub; ++i)
-                        if (s + i >= at.left) a[i] = one;       // u is 0: x was not read
-#pragma unroll
-                for (int i = 0; i < kGatedSub; ++i) {
-                    H = __ffma2_rn(a[i], H, u[i]);
-                    A = __fmul2_rn(A, a[i]);
-                }
-            }
-            maps[warp][lane] = make_float4(A.x, H.x, A.y, H.y);
-            __syncthreads();
-            if (p.ticket != nullptr) {
-                following = next_slot;
-                if (warp == 0) {
-                    float2 At = one, Ht = zero;
-                    for (int v = 0; v < warps; ++v) {
-                        const float4 m = maps[v][lane];
-                        Ht = __ffma2_rn(make_float2(m.x, m.z), Ht, make_float2(m.y, m.w));
-                        At = __fmul2_rn(At, make_float2(m.x, m.z));
-                    }
-                    entering[lane] = gated_join(p, at.group, at.pos, lane, make_float4(At.x, Ht.x, At.y, Ht.y), h);
-                }
-            }
-            float2 Ap = one, Hp = zero;
-            for (int v = 0; v < warp; ++v) {
-                const float4 m = maps[v][lane];
-                Hp = __ffma2_rn(make_float2(m.x, m.z), Hp, make_float2(m.y, m.w));
-                Ap = __fmul2_rn(Ap, make_float2(m.x, m.z));
-            }
-            if (p.ticket != nullptr) {
-                __syncthreads();
-                h = entering[lane];
-            }
-            h = __ffma2_rn(Ap, h, Hp);
-        }
-        if (at.rows > 0 && p.enter != nullptr)
-            store_f2<kVec>(p.enter + (at.b * p.blocks + at.block) * p.dim + at.d, c0, c1, h);
-        if (p.out != nullptr) {
-            IoT* out = static_cast<IoT*>(p.out) + at.b * p.out_s.batch + at.t * p.out_s.row + at.d;
-            int s = 0;
-            for (; s < at.left; s += kGatedSub) {
-                Pair<IoT> rf[kGatedSub], rx[kGatedSub];
-                load_pairs<IoT, kVec>(rf, gate + s * p.gate_s.row, p.gate_s.row, at.left - s, c0, c1);
-                load_pairs<IoT, kVec>(rx, x + s * p.x_s.row, p.x_s.row, at.left - s, c0, c1);
-                float2 a[kGatedSub], u[kGatedSub];
+                        if (s + i >= at.left) a[i][0] = a[i][1] = one;       // u is 0: x was not read
 #pragma unroll
                 for (int i = 0; i < kGatedSub; ++i)
-                    gated_terms2<kLog>(rf[i].get(), bias2, rx[i].get(), a[i], u[i]);
-                IoT* o = out + s * p.out_s.row;
-                if (at.left - s >= kGatedSub) {
 #pragma unroll
-                    for (int i = 0; i < kGatedSub; ++i) {
-                        h = __ffma2_rn(a[i], h, u[i]);
-                        store_pair<IoT, kVec>(o + i * p.out_s.row, c0, c1, h);
+                    for (int k = 0; k < kGatedPairs; ++k) {
+                        m.H[k] = __ffma2_rn(a[i][k], m.H[k], u[i][k]);
+                        m.A[k] = __fmul2_rn(m.A[k], a[i][k]);
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kGatedSub; ++i) {
-                        const bool in = s + i < at.left;
-                        if (in) h = __ffma2_rn(a[i], h, u[i]);
-                        if (s + i < at.rows) store_pair<IoT, kVec>(o + i * p.out_s.row, c0, c1, in ? h : zero);
-                    }
-                }
             }
-            for (; s < at.rows; ++s) store_pair<IoT, kVec>(out + s * p.out_s.row, c0, c1, zero);
+            const MapStore ms = pack_maps(m);
+            sA[warp][lane] = ms.A;
+            sH[warp][lane] = ms.H;
+            __syncthreads();
+            if (p.ticket != nullptr) following = next_slot;
+            gated_enter<false>(p, at, warp, lane, sA, sH, entering, h);
+        }
+        if (at.rows > 0 && p.enter != nullptr)
+            store_quad<float, kVec>(p.enter + (at.b * p.blocks + at.block) * p.dim + at.c.d, live, h[0], h[1]);
+        if (p.out != nullptr) {
+            IoT* out = static_cast<IoT*>(p.out) + at.b * p.out_s.batch + at.t * p.out_s.row + at.c.d;
+            int s = 0;
+            for (; s < at.left; s += kGatedSub) {
+                Quad<IoT> rf[kGatedSub], rx[kGatedSub];
+                load_quads<IoT, kVec>(rf, gate, p.gate_s.row, at.left - s, live);
+                load_quads<IoT, kVec>(rx, x, p.x_s.row, at.left - s, live);
+                gate += kGatedSub * p.gate_s.row;
+                x += kGatedSub * p.x_s.row;
+                float2 a[kGatedSub][kGatedPairs], u[kGatedSub][kGatedPairs];
+#pragma unroll
+                for (int i = 0; i < kGatedSub; ++i)
+#pragma unroll
+                    for (int k = 0; k < kGatedPairs; ++k)
+                        gated_terms2<kLog>(rf[i].get(k), bias2[k], rx[i].get(k), a[i][k], u[i][k]);
+#pragma unroll
+                for (int i = 0; i < kGatedSub; ++i) {
+                    const bool in = s + i < at.left;
+                    if (in) {
+                        h[0] = __ffma2_rn(a[i][0], h[0], u[i][0]);
+                        h[1] = __ffma2_rn(a[i][1], h[1], u[i][1]);
+                    }
+                    if (s + i < at.rows)
+                        store_quad<IoT, kVec>(out + i * p.out_s.row, live, in ? h[0] : zero, in ? h[1] : zero);
+                }
+                out += kGatedSub * p.out_s.row;
+            }
+            for (; s < at.rows; ++s, out += p.out_s.row) store_quad<IoT, kVec>(out, live, zero, zero);
             if (p.last != nullptr && at.block == p.blocks - 1)
-                store_f2<kVec>(p.last + at.b * p.dim + at.d, c0, c1, h);
+                store_quad<float, kVec>(p.last + at.b * p.dim + at.c.d, live, h[0], h[1]);
         }
         item = following;
     }
 }
 
 // Backward.  Phase one walks a block forward from its checkpoint, keeps the
-// state every kGatedBack steps in shared memory and accumulates the block's map
+// state every kGatedSub steps in shared memory and accumulates the block's map
 // of r, R = sum_t (prod_{s <= t} a_s) dout_t; phase two walks it backward.
-constexpr int kGatedBack = 4;
+constexpr int kGatedKept = kGatedBlock / kGatedSub;
+constexpr int kGatedBwdSmem = kGatedWarps * kGatedKept * 32 * (int)sizeof(float4);
 
 template <typename IoT, bool kLog, bool kVec>
-__global__ void __launch_bounds__(kGatedThreads, 2)
+__global__ void __launch_bounds__(kGatedThreads, GBMIN)
     gated_scan_bwd_kernel(const __grid_constant__ GatedParams p) {
-    __shared__ float4 maps[kGatedWarps][32];
-    __shared__ float2 entering[32];
-    __shared__ float2 bias_sums[kGatedWarps][32];
-    __shared__ float2 kept[kGatedWarps][kGatedBlock / kGatedBack][32];
+    __shared__ float4 sA[kGatedWarps][32], sH[kGatedWarps][32];
+    __shared__ float4 entering[32];
     __shared__ int64_t first_slot, next_slot;
+    extern __shared__ float4 kept_all[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    float4* kept = kept_all + warp * kGatedKept * 32 + lane;
     const float2 zero = make_float2(0.0f, 0.0f), one = make_float2(1.0f, 1.0f);
     int64_t item = gated_first_item(p, &first_slot);
     while (item < p.items) {
-        const GatedBlockAt at = gated_block<true>(p, item, warp, lane);
-        const bool c0 = at.d < p.dim, c1 = at.d + 1 < p.dim;
-        float2 bias2 = p.bias != nullptr ? load_f2<kVec>(p.bias + at.d, c0, c1) : zero;
-        bias2 = __fmul2_rn(bias2, make_float2(kLog2e, kLog2e));
-        const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + at.t * p.gate_s.row + at.d;
-        const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.t * p.x_s.row + at.d;
-        const IoT* dout = static_cast<const IoT*>(p.dout) + at.b * p.out_s.batch + at.t * p.out_s.row + at.d;
-        int64_t following = p.items;
+        const GatedBlockAt at = gated_block<true, kVec>(p, item, warp, lane);
+        const int live = at.c.live;
+        float2 bias2[kGatedPairs], h[kGatedPairs];
+        load_state<kVec>(p.bias, 0, p.dim, at.c, bias2);
+        bias2[0] = __fmul2_rn(bias2[0], make_float2(kLog2e, kLog2e));
+        bias2[1] = __fmul2_rn(bias2[1], make_float2(kLog2e, kLog2e));
+        const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + at.t * p.gate_s.row + at.c.d;
+        const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.t * p.x_s.row + at.c.d;
+        const IoT* dout = static_cast<const IoT*>(p.dout) + at.b * p.out_s.batch + at.t * p.out_s.row + at.c.d;
         if (threadIdx.x == 0 && p.ticket != nullptr) next_slot = atomicAdd(p.ticket, 1u);
-        float2 h = at.rows > 0 ? load_f2<kVec>(p.enter + (at.b * p.blocks + at.block) * p.dim + at.d, c0, c1) : zero;
-        float2 P = one, R = zero;
+        load_state<kVec>(at.rows > 0 ? p.enter : nullptr, at.b * p.blocks + at.block, p.dim, at.c, h);
+        Maps m = identity_maps();
         for (int s = 0; s < at.left; s += kGatedSub) {
-            Pair<IoT> rf[kGatedSub], rx[kGatedSub], rd[kGatedSub];
-            load_pairs<IoT, kVec>(rf, gate + s * p.gate_s.row, p.gate_s.row, at.left - s, c0, c1);
-            load_pairs<IoT, kVec>(rx, x + s * p.x_s.row, p.x_s.row, at.left - s, c0, c1);
-            load_pairs<IoT, kVec>(rd, dout + s * p.out_s.row, p.out_s.row, at.left - s, c0, c1);
+            Quad<IoT> rf[kGatedSub], rx[kGatedSub], rd[kGatedSub];
+            load_quads<IoT, kVec>(rf, gate, p.gate_s.row, at.left - s, live);
+            load_quads<IoT, kVec>(rx, x, p.x_s.row, at.left - s, live);
+            load_quads<IoT, kVec>(rd, dout, p.out_s.row, at.left - s, live);
+            gate += kGatedSub * p.gate_s.row;
+            x += kGatedSub * p.x_s.row;
+            dout += kGatedSub * p.out_s.row;
+            kept[s / kGatedSub * 32] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
 #pragma unroll
-            for (int i = 0; i < kGatedSub; ++i) {
-                if (i % kGatedBack == 0) kept[warp][(s + i) / kGatedBack][lane] = h;
-                float2 a, u;
-                gated_terms2<kLog>(rf[i].get(), bias2, rx[i].get(), a, u);
-                if (s + i >= at.left) a = one;
-                h = __ffma2_rn(a, h, u);
-                P = __fmul2_rn(P, a);
-                R = __ffma2_rn(P, rd[i].get(), R);
-            }
+            for (int i = 0; i < kGatedSub; ++i)
+#pragma unroll
+                for (int k = 0; k < kGatedPairs; ++k) {
+                    float2 a, u;
+                    gated_terms2<kLog>(rf[i].get(k), bias2[k], rx[i].get(k), a, u);
+                    if (s + i >= at.left) a = one;              // u and dout are 0: not read
+                    h[k] = __ffma2_rn(a, h[k], u);
+                    m.A[k] = __fmul2_rn(m.A[k], a);
+                    m.H[k] = __ffma2_rn(m.A[k], rd[i].get(k), m.H[k]);
+                }
         }
-        maps[warp][lane] = make_float4(P.x, R.x, P.y, R.y);
+        const MapStore ms = pack_maps(m);
+        sA[warp][lane] = ms.A;
+        sH[warp][lane] = ms.H;
         __syncthreads();
-        float2 r = p.dlast != nullptr ? load_f2<kVec>(p.dlast + at.b * p.dim + at.d, c0, c1) : zero;
-        if (p.ticket != nullptr) {
-            following = next_slot;
-            if (warp == 0) {
-                float2 At = one, Rt = zero;
-                for (int v = warps - 1; v >= 0; --v) {
-                    const float4 m = maps[v][lane];
-                    Rt = __ffma2_rn(make_float2(m.x, m.z), Rt, make_float2(m.y, m.w));
-                    At = __fmul2_rn(At, make_float2(m.x, m.z));
-                }
-                entering[lane] = gated_join(p, at.group, at.pos, lane, make_float4(At.x, Rt.x, At.y, Rt.y), r);
-            }
-        }
-        float2 Ap = one, Rp = zero;
-        for (int v = warps - 1; v > warp; --v) {
-            const float4 m = maps[v][lane];
-            Rp = __ffma2_rn(make_float2(m.x, m.z), Rp, make_float2(m.y, m.w));
-            Ap = __fmul2_rn(Ap, make_float2(m.x, m.z));
-        }
-        if (p.ticket != nullptr) {
-            __syncthreads();
-            r = entering[lane];
-        }
-        r = __ffma2_rn(Ap, r, Rp);
+        const int64_t following = p.ticket != nullptr ? next_slot : p.items;
+        float2 r[kGatedPairs];
+        load_state<kVec>(p.dlast, at.b, p.dim, at.c, r);
+        gated_enter<true>(p, at, warp, lane, sA, sH, entering, r);
 
-        float2 db = zero;
-        IoT* dgate = static_cast<IoT*>(p.dgate) + at.b * p.dgate_s.batch + at.t * p.dgate_s.row + at.d;
-        IoT* dx = static_cast<IoT*>(p.dx) + at.b * p.dx_s.batch + at.t * p.dx_s.row + at.d;
+        float2 db[kGatedPairs] = {zero, zero};
+        IoT* dgate = static_cast<IoT*>(p.dgate) + at.b * p.dgate_s.batch + at.t * p.dgate_s.row + at.c.d;
+        IoT* dx = static_cast<IoT*>(p.dx) + at.b * p.dx_s.batch + at.t * p.dx_s.row + at.c.d;
         for (int s = at.left; s < at.rows; ++s) {
-            store_pair<IoT, kVec>(dgate + s * p.dgate_s.row, c0, c1, zero);
-            store_pair<IoT, kVec>(dx + s * p.dx_s.row, c0, c1, zero);
+            store_quad<IoT, kVec>(dgate + s * p.dgate_s.row, live, zero, zero);
+            store_quad<IoT, kVec>(dx + s * p.dx_s.row, live, zero, zero);
         }
-        for (int s = (at.left - 1) & ~(kGatedBack - 1); s >= 0; s -= kGatedBack) {
+        const int top = (at.left + kGatedSub - 1) / kGatedSub * kGatedSub;
+        dgate += top * p.dgate_s.row;
+        dx += top * p.dx_s.row;
+        for (int s = top - kGatedSub; s >= 0; s -= kGatedSub) {
             const int left = at.left - s;
-            Pair<IoT> rf[kGatedBack], rx[kGatedBack], rd[kGatedBack];
-            load_pairs<IoT, kVec>(rf, gate + s * p.gate_s.row, p.gate_s.row, left, c0, c1);
-            load_pairs<IoT, kVec>(rx, x + s * p.x_s.row, p.x_s.row, left, c0, c1);
-            load_pairs<IoT, kVec>(rd, dout + s * p.out_s.row, p.out_s.row, left, c0, c1);
-            float2 a[kGatedBack], g[kGatedBack], before[kGatedBack];
-            h = kept[warp][s / kGatedBack][lane];
+            Quad<IoT> rf[kGatedSub], rx[kGatedSub], rd[kGatedSub];
+            gate -= kGatedSub * p.gate_s.row;
+            x -= kGatedSub * p.x_s.row;
+            dout -= kGatedSub * p.out_s.row;
+            dgate -= kGatedSub * p.dgate_s.row;
+            dx -= kGatedSub * p.dx_s.row;
+            load_quads<IoT, kVec>(rf, gate, p.gate_s.row, left, live);
+            load_quads<IoT, kVec>(rx, x, p.x_s.row, left, live);
+            load_quads<IoT, kVec>(rd, dout, p.out_s.row, left, live);
+            float2 a[kGatedSub][kGatedPairs], g[kGatedSub][kGatedPairs], before[kGatedSub][kGatedPairs];
+            const float4 hk = kept[s / kGatedSub * 32];
+            h[0] = make_float2(hk.x, hk.y);
+            h[1] = make_float2(hk.z, hk.w);
 #pragma unroll
-            for (int i = 0; i < kGatedBack; ++i) {
-                gated_gains2<kLog>(rf[i].get(), bias2, g[i], a[i]);
-                before[i] = h;
-                h = __ffma2_rn(a[i], h, kLog ? rx[i].get() : __fmul2_rn(g[i], rx[i].get()));
-            }
+            for (int i = 0; i < kGatedSub; ++i)
 #pragma unroll
-            for (int i = kGatedBack - 1; i >= 0; --i)
+                for (int k = 0; k < kGatedPairs; ++k) {
+                    gated_gains2<kLog>(rf[i].get(k), bias2[k], g[i][k], a[i][k]);
+                    before[i][k] = h[k];
+                    h[k] = __ffma2_rn(a[i][k], h[k], kLog ? rx[i].get(k) : __fmul2_rn(g[i][k], rx[i].get(k)));
+                }
+#pragma unroll
+            for (int i = kGatedSub - 1; i >= 0; --i)
                 if (i < left) {
-                    const float2 l = __fadd2_rn(rd[i].get(), r);
-                    r = __fmul2_rn(a[i], l);
-                    float2 df, dv;
-                    if constexpr (kLog) {
-                        dv = l;
-                        df = __fmul2_rn(r, before[i]);
-                    } else {
-                        const float2 diff = __ffma2_rn(before[i], make_float2(-1.0f, -1.0f), rx[i].get());
-                        dv = __fmul2_rn(g[i], l);
-                        df = __fmul2_rn(__fmul2_rn(g[i], r), diff);
+                    float2 df[kGatedPairs], dv[kGatedPairs];
+#pragma unroll
+                    for (int k = 0; k < kGatedPairs; ++k) {
+                        const float2 l = __fadd2_rn(rd[i].get(k), r[k]);
+                        r[k] = __fmul2_rn(a[i][k], l);
+                        if constexpr (kLog) {
+                            dv[k] = l;
+                            df[k] = __fmul2_rn(r[k], before[i][k]);
+                        } else {
+                            const float2 diff = __ffma2_rn(before[i][k], make_float2(-1.0f, -1.0f), rx[i].get(k));
+                            dv[k] = __fmul2_rn(g[i][k], l);
+                            df[k] = __fmul2_rn(__fmul2_rn(g[i][k], r[k]), diff);
+                        }
+                        db[k] = __fadd2_rn(db[k], df[k]);
                     }
-                    db = __fadd2_rn(db, df);
-                    store_pair<IoT, kVec>(dgate + (s + i) * p.dgate_s.row, c0, c1, df);
-                    store_pair<IoT, kVec>(dx + (s + i) * p.dx_s.row, c0, c1, dv);
+                    store_quad<IoT, kVec>(dgate + i * p.dgate_s.row, live, df[0], df[1]);
+                    store_quad<IoT, kVec>(dx + i * p.dx_s.row, live, dv[0], dv[1]);
                 }
         }
-        if (p.dh0 != nullptr && at.block == 0) store_f2<kVec>(p.dh0 + at.b * p.dim + at.d, c0, c1, r);
+        if (p.dh0 != nullptr && at.block == 0)
+            store_quad<float, kVec>(p.dh0 + at.b * p.dim + at.c.d, live, r[0], r[1]);
         if (p.bias_partial != nullptr) {
-            bias_sums[warp][lane] = db;
+            // the warps' sums, in order; kept is free again (each lane's own entries)
+            kept[0] = make_float4(db[0].x, db[0].y, db[1].x, db[1].y);
             __syncthreads();
             if (warp == 0) {
-                float2 sum = zero;
-                for (int v = 0; v < warps; ++v) sum = __fadd2_rn(sum, bias_sums[v][lane]);
-                store_f2<kVec>(p.bias_partial + (at.b * p.segments + at.segment) * p.dim + at.d, c0, c1, sum);
+                float2 sum[kGatedPairs] = {zero, zero};
+                for (int v = 0; v < warps; ++v) {
+                    const float4 q = kept[v * kGatedKept * 32];
+                    sum[0] = __fadd2_rn(sum[0], make_float2(q.x, q.y));
+                    sum[1] = __fadd2_rn(sum[1], make_float2(q.z, q.w));
+                }
+                store_quad<float, kVec>(p.bias_partial + (at.b * p.segments + at.segment) * p.dim + at.c.d, live,
+                                        sum[0], sum[1]);
             }
+            __syncthreads();
         }
         item = following;
     }

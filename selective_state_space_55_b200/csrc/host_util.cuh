@@ -1,9 +1,12 @@
 // Host-side helpers shared by the library's translation units.
 #pragma once
 
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
+
+#include <mutex>
 
 #include "mamba_ssm.h"
 #include "ssm_device.cuh"
@@ -33,6 +36,28 @@ inline int current_sm_count(int* device_out) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
     if (dev >= 0 && dev < kMaxDevices) cached[dev] = sms;
     return sms;
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+template <typename Kernel>
+cudaError_t ensure_smem_attr(Kernel kernel, int bytes, bool* done_per_device, int dev) {
+    if (dev >= 0 && dev < kMaxDevices && done_per_device[dev]) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done_per_device[dev] = true;
+    return e;
 }
 
 // Read and clear this translation unit's device status word.

@@ -2,8 +2,6 @@
 // descriptor set-up and kernel dispatch of the scans, the state update, the
 // convolution and the Mamba-2 layer.  block_ops.cu holds the layer norm, the
 // gated recurrence and the convolution's backward.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cstring>
 #include <mutex>
@@ -37,20 +35,6 @@ mamba_status_t check_dims(const mamba_dims_t* dims, bool scan) {
     return MAMBA_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
 // 3-D map over a row-major (d2, d1, d0) tensor, d0 innermost, box (box0, box1, 1).
 bool encode_map_3d(CUtensorMap* map, const void* base, int esize, uint64_t d0, uint64_t d1,
                    uint64_t d2, uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle) {
@@ -66,14 +50,6 @@ bool encode_map_3d(CUtensorMap* map, const void* base, int esize, uint64_t d0, u
                               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
-}
-
-template <typename Kernel>
-cudaError_t ensure_smem_attr(Kernel kernel, int bytes, bool* done_per_device, int dev) {
-    if (dev >= 0 && dev < kMaxDevices && done_per_device[dev]) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done_per_device[dev] = true;
-    return e;
 }
 
 template <typename IoT, int kCpl, bool kHasZ, bool kSoftplus, bool kZoh, bool kBld, bool kLookback>

@@ -10,6 +10,8 @@ the library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from pathlib import Path
 
 import torch
@@ -143,27 +145,21 @@ def library(path: Path | str | None = None) -> ctypes.CDLL:
     lib.mamba_selective_state_update.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, dims_p, vp]
     lib.mamba_ssd_chunk_scan_fwd.restype = i32
     lib.mamba_ssd_chunk_scan_fwd.argtypes = [vp] * 11 + [ctypes.POINTER(SsdDims), vp]
-    gated_p, norm_p = ctypes.POINTER(GatedDims), ctypes.POINTER(NormDims)
-    lib.mamba_causal_conv1d_bwd_workspace_bytes.restype = ctypes.c_size_t
-    lib.mamba_causal_conv1d_bwd_workspace_bytes.argtypes = [dims_p, i32]
-    lib.mamba_causal_conv1d_bwd.restype = i32
-    lib.mamba_causal_conv1d_bwd.argtypes = [vp] * 4 + [i32, i32] + [vp] * 6 + [dims_p, vp]
-    lib.mamba_gated_scan_workspace_bytes.restype = ctypes.c_size_t
-    lib.mamba_gated_scan_workspace_bytes.argtypes = [gated_p]
-    lib.mamba_gated_scan_fwd.restype = i32
-    lib.mamba_gated_scan_fwd.argtypes = [vp] * 7 + [gated_p, vp]
-    lib.mamba_gated_scan_bwd_workspace_bytes.restype = ctypes.c_size_t
-    lib.mamba_gated_scan_bwd_workspace_bytes.argtypes = [gated_p, i32]
-    lib.mamba_gated_scan_bwd.restype = i32
-    lib.mamba_gated_scan_bwd.argtypes = [vp] * 11 + [gated_p, vp]
-    lib.mamba_gated_state_update.restype = i32
-    lib.mamba_gated_state_update.argtypes = [vp] * 5 + [gated_p, vp]
-    lib.mamba_layer_norm_fwd.restype = i32
-    lib.mamba_layer_norm_fwd.argtypes = [vp] * 8 + [norm_p, vp]
-    lib.mamba_layer_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
-    lib.mamba_layer_norm_bwd_workspace_bytes.argtypes = [norm_p]
-    lib.mamba_layer_norm_bwd.restype = i32
-    lib.mamba_layer_norm_bwd.argtypes = [vp] * 10 + [norm_p, vp]
+    # the sizes of these go over as a pointer to their packed bytes (or byref)
+    size_t = ctypes.c_size_t
+    for name, restype, argtypes in (
+            ("causal_conv1d_bwd_workspace_bytes", size_t, [vp, i32]),
+            ("causal_conv1d_bwd", i32, [vp] * 4 + [i32, i32] + [vp] * 8),
+            ("gated_scan_workspace_bytes", size_t, [vp]),
+            ("gated_scan_fwd", i32, [vp] * 9),
+            ("gated_scan_bwd_workspace_bytes", size_t, [vp, i32]),
+            ("gated_scan_bwd", i32, [vp] * 13),
+            ("gated_state_update", i32, [vp] * 7),
+            ("layer_norm_fwd", i32, [vp] * 10),
+            ("layer_norm_bwd_workspace_bytes", size_t, [vp]),
+            ("layer_norm_bwd", i32, [vp] * 12)):
+        fn = getattr(lib, "mamba_" + name)
+        fn.restype, fn.argtypes = restype, argtypes
     lib.mamba_device_status.restype = i32
     lib.mamba_device_status.argtypes = []
     lib.mamba_status_string.restype = ctypes.c_char_p
@@ -604,42 +600,33 @@ def ssd_chunk_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
 # Operators around a recurrent block's projections.  These run on the device of
 # their first tensor, whichever device is current, and every other tensor has
 # to be there too.  Outputs and workspaces are allocated on the stream that the
-# kernels run on.
+# kernels run on.  A decode step calls them for every layer and token, so the
+# way to the library is kept short: sizes go over as packed bytes, and the
+# workspace sizes (functions of the sizes alone) are remembered per problem.
 
 _FLOATS = (torch.float32, torch.bfloat16)
 _F32 = (torch.float32,)
+_GATED = struct.Struct("@3q4iQ10qQQ")       # the fields of GatedDims
+_NORM = struct.Struct("@2q3if5qQQ")         # the fields of NormDims
+_DIMS = struct.Struct("@4q6iQQ")            # the fields of MambaDims
+assert _DIMS.size == ctypes.sizeof(MambaDims)
+assert _GATED.size == ctypes.sizeof(GatedDims) and _NORM.size == ctypes.sizeof(NormDims)
+_PACKED = (0, 0)
 
 
-def _on(device, stream, call):
-    """``call(stream handle)`` with ``device`` and ``stream`` (default: the
-    device's current stream) current."""
+def _elsewhere(fn, device, stream, *args, **kwargs):
+    """``fn`` again with ``device`` and ``stream`` (default: its current one) made current."""
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return call(torch.cuda.current_stream().cuda_stream)
         with torch.cuda.device(device):
-            return call(torch.cuda.current_stream().cuda_stream)
+            return fn(*args, **kwargs)
     if stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
     with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        return fn(*args, **kwargs)
 
 
 def _check(name, t, dtypes, shape, device):
-    """Packed tensor of the given dtype and shape on ``device`` (None passes)."""
-    if t is None:
-        return
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _check_rows(name, t, dtypes, shape, device):
-    """A (rows, dim) view whose rows are contiguous; returns the distance of rows."""
+    """Packed tensor of the given dtype and shape on ``device``; returns its address (None: 0)."""
     if t is None:
         return 0
     if t.device != device or not t.is_cuda:
@@ -648,6 +635,25 @@ def _check_rows(name, t, dtypes, shape, device):
         raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _check_view(name, t, dtypes, shape, device):
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+
+
+def _check_rows(name, t, dtypes, shape, device):
+    """A view whose rows (last dimension) are contiguous; returns the distance of rows (0: packed)."""
+    if t is None:
+        return 0
+    _check_view(name, t, dtypes, shape, device)
     if t.is_contiguous():
         return 0
     dim = shape[-1]
@@ -666,15 +672,10 @@ def _check_rows(name, t, dtypes, shape, device):
 
 
 def _check_strided(name, t, dtypes, shape, device):
-    """A 3-dimensional tensor with a contiguous last dimension; returns its Strides."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    """A 3-dimensional tensor with a contiguous last dimension; returns its distances."""
+    _check_view(name, t, dtypes, shape, device)
     if t.is_contiguous():
-        return Strides(0, 0)
+        return _PACKED
     n = shape[-1]
     sb, sr, si = t.stride()
     if n > 1 and si != 1:
@@ -682,32 +683,46 @@ def _check_strided(name, t, dtypes, shape, device):
     if (shape[0] > 1 and sb < n) or (shape[1] > 1 and sr < n):
         raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
     # distances along dimensions of size 1 are arbitrary: give them a harmless value
-    return Strides(sb if shape[0] > 1 else max(n, 1), sr if shape[1] > 1 else max(n, 1))
+    return (sb if shape[0] > 1 else max(n, 1), sr if shape[1] > 1 else max(n, 1))
 
 
-def _raise_on(name, rc):
-    if rc != MAMBA_OK:
-        raise MambaError(name, rc)
-
-
-def _workspace(workspace, need, device, name):
-    """The caller's workspace, or a new one of ``need`` bytes; None when nothing is needed."""
+@functools.lru_cache(maxsize=4096)
+def _workspace_need(call, device_index, dims, *more):
+    """Bytes that ``call`` reports for the packed sizes ``dims`` on a device."""
+    need = getattr(library(), call)(dims, *more)
     if need == ctypes.c_size_t(-1).value:
-        raise MambaError(name, -1)
+        raise MambaError(call, -1)
+    return need
+
+
+def _workspace(workspace, need, device):
+    """The caller's workspace, or a new one of ``need`` bytes; None when nothing is needed."""
     if workspace is not None:
         _check("workspace", workspace, (torch.uint8,), workspace.shape, device)
         return workspace
     return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
 
 
-def _set_workspace(dims, ws):
-    if ws is not None:
-        dims.workspace = ws.data_ptr()
-        dims.workspace_bytes = ws.numel()
+def _needs_cuda(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _FLOATS:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {_FLOATS}")
+    return t.device, t.dtype, t.shape
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
+def _like(t):
+    """A packed tensor of t's shape and dtype (cheaper than torch.empty)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _finish(name, rc):
+    if rc != MAMBA_OK:
+        raise MambaError(name, rc)
+
+
+def _handle(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False, out=None,
@@ -723,42 +738,43 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False
     residual_out, (out, residual_out); with ``return_stats``, mean (None for
     ``rms``) and rstd, fp32 in x's leading shape, are appended.
     """
-    if x.dim() < 1:
+    device, io, shape = _needs_cuda("x", x)
+    if stream is not None or device.index != torch._C._cuda_getDevice():
+        return _elsewhere(layer_norm_fwd, device, stream, x, weight, bias, residual, eps, rms, out,
+                          residual_out, return_stats)
+    if len(shape) < 1:
         raise ValueError("x must have at least one dimension")
-    device, io, shape = x.device, x.dtype, x.shape
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
     dim = shape[-1]
     rdt = (residual if residual is not None else residual_out if residual_out is not None else x).dtype
-    dims = NormDims(dim=dim, rms=int(bool(rms)), eps=eps)
-    dims.x_stride = _check_rows("x", x, _FLOATS, shape, device)
-    dims.residual_stride = _check_rows("residual", residual, (io, torch.float32), shape, device)
-    _check("weight", weight, _F32, (dim,), device)
-    _check("bias", bias, _F32, (dim,), device)
-    dims.rows = x.numel() // dim if dim else 0
-    dims.io_dtype, dims.residual_dtype = _DTYPE_CODE[io], _DTYPE_CODE[rdt]
-
-    def call(handle):
-        y = torch.empty(shape, dtype=io, device=device) if out is None else out
-        s = residual_out
-        if s is None and residual is not None:
-            s = torch.empty(shape, dtype=rdt, device=device)
-        dims.out_stride = _check_rows("out", y, (io,), shape, device)
-        dims.residual_out_stride = _check_rows("residual_out", s, (rdt,), shape, device)
-        mean = rstd = None
-        if return_stats:
-            rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-            mean = None if rms else torch.empty(shape[:-1], dtype=torch.float32, device=device)
-        rc = library().mamba_layer_norm_fwd(
-            x.data_ptr(), _address(residual), _address(weight), _address(bias), y.data_ptr(),
-            _address(s), _address(mean), _address(rstd), ctypes.byref(dims), handle)
-        _raise_on("mamba_layer_norm_fwd", rc)
-        r = (y,) if s is None else (y, s)
-        if return_stats:
-            r += (mean, rstd)
-        return r if len(r) > 1 else y
-
-    return _on(device, stream, call)
+    xs = _check_rows("x", x, _FLOATS, shape, device)
+    rs = _check_rows("residual", residual, (io, torch.float32), shape, device)
+    wp = _check("weight", weight, _F32, (dim,), device)
+    bp = _check("bias", bias, _F32, (dim,), device)
+    if out is None:
+        out, ys = _like(x), 0
+    else:
+        ys = _check_rows("out", out, (io,), shape, device)
+    ss = 0
+    if residual_out is not None:
+        ss = _check_rows("residual_out", residual_out, (rdt,) if residual is not None else (io, torch.float32),
+                         shape, device)
+    elif residual is not None:
+        residual_out = _like(residual)
+    mean = rstd = None
+    if return_stats:
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+        mean = None if rms else _like(rstd)
+    dims = _NORM.pack(x.numel() // dim if dim else 0, dim, _DTYPE_CODE[io], _DTYPE_CODE[rdt], bool(rms), eps,
+                      xs, ys, rs, ss, 0, 0, 0)
+    _finish("mamba_layer_norm_fwd", library().mamba_layer_norm_fwd(
+        x.data_ptr(), residual.data_ptr() if residual is not None else 0, wp, bp, out.data_ptr(),
+        residual_out.data_ptr() if residual_out is not None else 0,
+        mean.data_ptr() if mean is not None else 0, rstd.data_ptr() if return_stats else 0, dims,
+        _handle(device)))
+    r = (out,) if residual_out is None else (out, residual_out)
+    if return_stats:
+        r += (mean, rstd)
+    return r if len(r) > 1 else out
 
 
 def layer_norm_bwd(dout, s, rstd, mean=None, weight=None, bias=None, dresidual_out=None, rms=False,
@@ -773,72 +789,71 @@ def layer_norm_bwd(dout, s, rstd, mean=None, weight=None, bias=None, dresidual_o
     residual of the same dtype), dresidual (s's dtype) when that differs or a
     buffer is given, dweight and dbias (fp32) for the weight and bias given.
     """
-    device, io, shape = dout.device, dout.dtype, dout.shape
-    if not dout.is_cuda:
-        raise ValueError("dout must be a CUDA tensor")
-    if dout.dim() < 1:
+    device, io, shape = _needs_cuda("dout", dout)
+    if stream is not None or device.index != torch._C._cuda_getDevice():
+        return _elsewhere(layer_norm_bwd, device, stream, dout, s, rstd, mean, weight, bias,
+                          dresidual_out, rms, dx, dresidual, workspace)
+    if len(shape) < 1:
         raise ValueError("dout must have at least one dimension")
-    dim = shape[-1]
-    rdt = s.dtype
-    dims = NormDims(dim=dim, rms=int(bool(rms)))
-    dims.out_stride = _check_rows("dout", dout, _FLOATS, shape, device)
-    dims.x_stride = _check_rows("s", s, (io, torch.float32), shape, device)
-    dims.residual_out_stride = _check_rows("dresidual_out", dresidual_out, (rdt,), shape, device)
-    lead = shape[:-1]
-    _check("rstd", rstd, _F32, lead, device)
+    dim, lead, rdt = shape[-1], shape[:-1], s.dtype
+    ys = _check_rows("dout", dout, _FLOATS, shape, device)
+    xs = _check_rows("s", s, (io, torch.float32), shape, device)
+    drs = _check_rows("dresidual_out", dresidual_out, (rdt,), shape, device)
+    rp = _check("rstd", rstd, _F32, lead, device)
+    mp = 0
     if not rms:
         if mean is None:
             raise ValueError("mean is needed (unless rms)")
-        _check("mean", mean, _F32, lead, device)
-    _check("weight", weight, _F32, (dim,), device)
+        mp = _check("mean", mean, _F32, lead, device)
+    wp = _check("weight", weight, _F32, (dim,), device)
     _check("bias", bias, _F32, (dim,), device)
-    dims.rows = dout.numel() // dim if dim else 0
-    dims.io_dtype, dims.residual_dtype = _DTYPE_CODE[io], _DTYPE_CODE[rdt]
+    gs = rs = 0
+    g = {}
+    if dx is None:
+        dx = _like(dout)
+    else:
+        gs = _check_rows("dx", dx, (io,), shape, device)
+    g["dx"] = dx
+    if dresidual is not None:
+        rs = _check_rows("dresidual", dresidual, (rdt,), shape, device)
+        g["dresidual"] = dresidual
+    elif rdt != io:
+        g["dresidual"] = dresidual = _like(s)
+    dwp = dbp = 0
+    if weight is not None:
+        g["dweight"] = _like(weight)
+        dwp = g["dweight"].data_ptr()
+    if bias is not None:
+        g["dbias"] = _like(bias)
+        dbp = g["dbias"].data_ptr()
+    sizes = (dout.numel() // dim if dim else 0, dim, _DTYPE_CODE[io], _DTYPE_CODE[rdt], bool(rms), 0.0,
+             xs, ys, rs, drs, gs)
+    ws = None
+    if dwp or dbp:
+        need = _workspace_need("mamba_layer_norm_bwd_workspace_bytes", device.index, _NORM.pack(*sizes, 0, 0))
+        ws = _workspace(workspace, need, device)
+    dims = _NORM.pack(*sizes, 0, 0) if ws is None else _NORM.pack(*sizes, ws.data_ptr(), ws.numel())
+    _finish("mamba_layer_norm_bwd", library().mamba_layer_norm_bwd(
+        s.data_ptr(), wp, mp, rp, dout.data_ptr(),
+        dresidual_out.data_ptr() if dresidual_out is not None else 0, dx.data_ptr(),
+        dresidual.data_ptr() if dresidual is not None else 0, dwp, dbp, dims, _handle(device)))
+    return g
 
-    def call(handle):
-        g = {"dx": torch.empty(shape, dtype=io, device=device) if dx is None else dx}
-        if dresidual is not None:
-            g["dresidual"] = dresidual
-        elif rdt != io:
-            g["dresidual"] = torch.empty(shape, dtype=rdt, device=device)
-        dims.dx_stride = _check_rows("dx", g["dx"], (io,), shape, device)
-        dims.residual_stride = _check_rows("dresidual", g.get("dresidual"), (rdt,), shape, device)
-        if weight is not None:
-            g["dweight"] = torch.empty((dim,), dtype=torch.float32, device=device)
-        if bias is not None:
-            g["dbias"] = torch.empty((dim,), dtype=torch.float32, device=device)
-        ws = None
-        if weight is not None or bias is not None:
-            need = library().mamba_layer_norm_bwd_workspace_bytes(ctypes.byref(dims))
-            ws = _workspace(workspace, need, device, "mamba_layer_norm_bwd_workspace_bytes")
-            _set_workspace(dims, ws)
-        rc = library().mamba_layer_norm_bwd(
-            s.data_ptr(), _address(weight), None if rms else mean.data_ptr(), rstd.data_ptr(),
-            dout.data_ptr(), _address(dresidual_out), g["dx"].data_ptr(),
-            _address(g.get("dresidual")), _address(g.get("dweight")), _address(g.get("dbias")),
-            ctypes.byref(dims), handle)
-        _raise_on("mamba_layer_norm_bwd", rc)
-        return g
 
-    return _on(device, stream, call)
-
-
-def _gated_sizes(gate, layout):
+def _gated_sizes(shape, layout):
     if layout not in ("bdl", "bld"):
         raise ValueError(f"layout must be 'bdl' or 'bld', not {layout!r}")
-    if gate.dim() != 3:
-        raise ValueError(f"gate must have 3 dimensions, got shape {tuple(gate.shape)}")
-    if not gate.is_cuda:
-        raise ValueError("gate must be a CUDA tensor")
+    if len(shape) != 3:
+        raise ValueError(f"gate must have 3 dimensions, got shape {tuple(shape)}")
     if layout == "bld":
-        batch, L, dim = gate.shape
+        batch, L, dim = shape
         return batch, dim, L, MAMBA_FLAG_LAYOUT_BLD
-    batch, dim, L = gate.shape
+    batch, dim, L = shape
     return batch, dim, L, 0
 
 
-def _checkpoint_shape(batch, dim, L):
-    return (batch, -(-L // MAMBA_GATED_CHECKPOINT_STEPS), dim)
+def _check_checkpoints(t, batch, dim, L, device):
+    return _check("checkpoints", t, _F32, (batch, -(-L // MAMBA_GATED_CHECKPOINT_STEPS), dim), device)
 
 
 def gated_scan_fwd(gate, x, gate_bias=None, initial_state=None, seqlens=None, log_decay=False,
@@ -855,47 +870,44 @@ def gated_scan_fwd(gate, x, gate_bias=None, initial_state=None, seqlens=None, lo
     state (batch, dim) fp32 and, layout "bld" only, the states entering each block
     of 64 steps, (batch, ceil(L / 64), dim) fp32, when asked for or given.
     """
-    batch, dim, L, lay = _gated_sizes(gate, layout)
-    device, io, shape = gate.device, gate.dtype, gate.shape
-    dims = GatedDims(batch=batch, dim=dim, seqlen=L, log_decay=int(bool(log_decay)), flags=flags | lay)
-    dims.gate = _check_strided("gate", gate, _FLOATS, shape, device)
-    dims.x = _check_strided("x", x, (io,), shape, device)
-    dims.io_dtype = _DTYPE_CODE[io]
-    _check("gate_bias", gate_bias, _F32, (dim,), device)
-    _check("initial_state", initial_state, _F32, (batch, dim), device)
-    _check("seqlens", seqlens, (torch.int32,), (batch,), device)
-    dims.seqlens = _address(seqlens)
+    device, io, shape = _needs_cuda("gate", gate)
+    if stream is not None or device.index != torch._C._cuda_getDevice():
+        return _elsewhere(gated_scan_fwd, device, stream, gate, x, gate_bias, initial_state, seqlens,
+                          log_decay, out, last_state, return_last_state, checkpoints,
+                          return_checkpoints, workspace, None, layout, flags)
+    batch, dim, L, lay = _gated_sizes(shape, layout)
+    fs = _check_strided("gate", gate, _FLOATS, shape, device)
+    xs = _check_strided("x", x, (io,), shape, device)
+    bp = _check("gate_bias", gate_bias, _F32, (dim,), device)
+    hp = _check("initial_state", initial_state, _F32, (batch, dim), device)
+    np_ = _check("seqlens", seqlens, (torch.int32,), (batch,), device)
+    if out is None:
+        out, ys = _like(gate), _PACKED
+    else:
+        ys = _check_strided("out", out, (io,), shape, device)
+    if last_state is None and return_last_state:
+        last_state = torch.empty((batch, dim), dtype=torch.float32, device=device)
+    lp = _check("last_state", last_state, _F32, (batch, dim), device)
+    cp = 0
     want_ck = return_checkpoints or checkpoints is not None
-    if want_ck and layout != "bld":
-        raise ValueError("checkpoints are for layout 'bld'")
-
-    def call(handle):
-        y = torch.empty(shape, dtype=io, device=device) if out is None else out
-        dims.out = _check_strided("out", y, (io,), shape, device)
-        last, ck = last_state, checkpoints
-        if last is None and return_last_state:
-            last = torch.empty((batch, dim), dtype=torch.float32, device=device)
-        _check("last_state", last, _F32, (batch, dim), device)
-        if want_ck:
-            cs = _checkpoint_shape(batch, dim, L)
-            if ck is None:
-                ck = torch.empty(cs, dtype=torch.float32, device=device)
-            _check("checkpoints", ck, _F32, cs, device)
-        need = library().mamba_gated_scan_workspace_bytes(ctypes.byref(dims))
-        ws = _workspace(workspace, need, device, "mamba_gated_scan_workspace_bytes")
-        _set_workspace(dims, ws)
-        rc = library().mamba_gated_scan_fwd(
-            gate.data_ptr(), x.data_ptr(), _address(gate_bias), _address(initial_state),
-            y.data_ptr(), _address(last), _address(ck), ctypes.byref(dims), handle)
-        _raise_on("mamba_gated_scan_fwd", rc)
-        r = (y,)
-        if last is not None:
-            r += (last,)
-        if want_ck:
-            r += (ck,)
-        return r if len(r) > 1 else y
-
-    return _on(device, stream, call)
+    if want_ck:
+        if not lay:
+            raise ValueError("checkpoints are for layout 'bld'")
+        if checkpoints is None:
+            checkpoints = torch.empty((batch, -(-L // MAMBA_GATED_CHECKPOINT_STEPS), dim),
+                                      dtype=torch.float32, device=device)
+        cp = _check_checkpoints(checkpoints, batch, dim, L, device)
+    sizes = (batch, dim, L, _DTYPE_CODE[io], bool(log_decay), flags | lay, 0)
+    need = _workspace_need("mamba_gated_scan_workspace_bytes", device.index,
+                           _GATED.pack(*sizes, 0, *_PACKED * 5, 0, 0))
+    ws = _workspace(workspace, need, device)
+    wp, wn = (0, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    dims = _GATED.pack(*sizes, np_, *fs, *xs, *ys, 0, 0, 0, 0, wp, wn)
+    _finish("mamba_gated_scan_fwd", library().mamba_gated_scan_fwd(
+        gate.data_ptr(), x.data_ptr(), bp, hp, out.data_ptr(), lp, cp, dims, _handle(device)))
+    if last_state is None and not want_ck:
+        return out
+    return (out,) + (() if last_state is None else (last_state,)) + ((checkpoints,) if want_ck else ())
 
 
 def gated_scan_bwd(gate, x, dout, gate_bias=None, initial_state=None, seqlens=None,
@@ -909,73 +921,76 @@ def gated_scan_bwd(gate, x, dout, gate_bias=None, initial_state=None, seqlens=No
     passed, for instance halves of one tensor), dgate_bias and dinitial_state
     (fp32) for the optional inputs given.
     """
-    batch, dim, L, lay = _gated_sizes(gate, layout)
-    device, io, shape = gate.device, gate.dtype, gate.shape
-    dims = GatedDims(batch=batch, dim=dim, seqlen=L, log_decay=int(bool(log_decay)), flags=flags | lay)
-    dims.gate = _check_strided("gate", gate, _FLOATS, shape, device)
-    dims.x = _check_strided("x", x, (io,), shape, device)
-    dims.out = _check_strided("dout", dout, (io,), shape, device)
-    dims.io_dtype = _DTYPE_CODE[io]
-    _check("gate_bias", gate_bias, _F32, (dim,), device)
-    _check("initial_state", initial_state, _F32, (batch, dim), device)
-    _check("dlast_state", dlast_state, _F32, (batch, dim), device)
-    _check("seqlens", seqlens, (torch.int32,), (batch,), device)
-    dims.seqlens = _address(seqlens)
+    device, io, shape = _needs_cuda("gate", gate)
+    if stream is not None or device.index != torch._C._cuda_getDevice():
+        return _elsewhere(gated_scan_bwd, device, stream, gate, x, dout, gate_bias, initial_state,
+                          seqlens, dlast_state, checkpoints, log_decay, dgate, dx, workspace, None,
+                          layout, flags)
+    batch, dim, L, lay = _gated_sizes(shape, layout)
+    fs = _check_strided("gate", gate, _FLOATS, shape, device)
+    xs = _check_strided("x", x, (io,), shape, device)
+    ys = _check_strided("dout", dout, (io,), shape, device)
+    bp = _check("gate_bias", gate_bias, _F32, (dim,), device)
+    hp = _check("initial_state", initial_state, _F32, (batch, dim), device)
+    lp = _check("dlast_state", dlast_state, _F32, (batch, dim), device)
+    np_ = _check("seqlens", seqlens, (torch.int32,), (batch,), device)
+    cp = 0
     if checkpoints is not None:
-        if layout != "bld":
+        if not lay:
             raise ValueError("checkpoints are for layout 'bld'")
-        _check("checkpoints", checkpoints, _F32, _checkpoint_shape(batch, dim, L), device)
-
-    def call(handle):
-        g = {"dgate": torch.empty(shape, dtype=io, device=device) if dgate is None else dgate,
-             "dx": torch.empty(shape, dtype=io, device=device) if dx is None else dx}
-        dims.dgate = _check_strided("dgate", g["dgate"], (io,), shape, device)
-        dims.dx = _check_strided("dx", g["dx"], (io,), shape, device)
-        if gate_bias is not None:
-            g["dgate_bias"] = torch.empty((dim,), dtype=torch.float32, device=device)
-        if initial_state is not None:
-            g["dinitial_state"] = torch.empty((batch, dim), dtype=torch.float32, device=device)
-        need = library().mamba_gated_scan_bwd_workspace_bytes(ctypes.byref(dims),
-                                                              int(checkpoints is not None))
-        ws = _workspace(workspace, need, device, "mamba_gated_scan_bwd_workspace_bytes")
-        _set_workspace(dims, ws)
-        rc = library().mamba_gated_scan_bwd(
-            gate.data_ptr(), x.data_ptr(), _address(gate_bias), _address(initial_state),
-            _address(checkpoints), dout.data_ptr(), _address(dlast_state), g["dgate"].data_ptr(),
-            g["dx"].data_ptr(), _address(g.get("dgate_bias")), _address(g.get("dinitial_state")),
-            ctypes.byref(dims), handle)
-        _raise_on("mamba_gated_scan_bwd", rc)
-        return g
-
-    return _on(device, stream, call)
+        cp = _check_checkpoints(checkpoints, batch, dim, L, device)
+    dfs = dxs = _PACKED
+    if dgate is None:
+        dgate = _like(gate)
+    else:
+        dfs = _check_strided("dgate", dgate, (io,), shape, device)
+    if dx is None:
+        dx = _like(gate)
+    else:
+        dxs = _check_strided("dx", dx, (io,), shape, device)
+    g = {"dgate": dgate, "dx": dx}
+    dbp = dhp = 0
+    if gate_bias is not None:
+        g["dgate_bias"] = _like(gate_bias)
+        dbp = g["dgate_bias"].data_ptr()
+    if initial_state is not None:
+        g["dinitial_state"] = _like(initial_state)
+        dhp = g["dinitial_state"].data_ptr()
+    sizes = (batch, dim, L, _DTYPE_CODE[io], bool(log_decay), flags | lay, 0)
+    need = _workspace_need("mamba_gated_scan_bwd_workspace_bytes", device.index,
+                           _GATED.pack(*sizes, 0, *_PACKED * 5, 0, 0), int(checkpoints is not None))
+    ws = _workspace(workspace, need, device)
+    wp, wn = (0, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    dims = _GATED.pack(*sizes, np_, *fs, *xs, *ys, *dfs, *dxs, wp, wn)
+    _finish("mamba_gated_scan_bwd", library().mamba_gated_scan_bwd(
+        gate.data_ptr(), x.data_ptr(), bp, hp, cp, dout.data_ptr(), lp, dgate.data_ptr(),
+        dx.data_ptr(), dbp, dhp, dims, _handle(device)))
+    return g
 
 
 def gated_state_update(state, gate, x, gate_bias=None, log_decay=False, out=None, stream=None):
     """One token of the gated recurrence through ``mamba_gated_state_update``;
     ``state`` (batch, dim) fp32 is updated in place.  gate, x: (batch, dim) fp32 or
     bf16, rows contiguous.  Returns ``out``, the new state in x's dtype."""
-    if state.dim() != 2:
-        raise ValueError(f"state must have 2 dimensions, got shape {tuple(state.shape)}")
-    if not state.is_cuda:
-        raise ValueError("state must be a CUDA tensor")
-    device, io, shape = state.device, x.dtype, state.shape
-    dims = GatedDims(batch=shape[0], dim=shape[1], log_decay=int(bool(log_decay)))
-    _check("state", state, _F32, shape, device)
-    dims.x.batch = _check_rows("x", x, _FLOATS, shape, device)
-    dims.gate.batch = _check_rows("gate", gate, (io,), shape, device)
-    _check("gate_bias", gate_bias, _F32, (shape[1],), device)
-    dims.io_dtype = _DTYPE_CODE[io]
-
-    def call(handle):
-        y = torch.empty(shape, dtype=io, device=device) if out is None else out
-        dims.out.batch = _check_rows("out", y, (io,), shape, device)
-        rc = library().mamba_gated_state_update(
-            state.data_ptr(), gate.data_ptr(), x.data_ptr(), _address(gate_bias), y.data_ptr(),
-            ctypes.byref(dims), handle)
-        _raise_on("mamba_gated_state_update", rc)
-        return y
-
-    return _on(device, stream, call)
+    device, io, shape = _needs_cuda("x", x)
+    if stream is not None or device.index != torch._C._cuda_getDevice():
+        return _elsewhere(gated_state_update, device, stream, state, gate, x, gate_bias, log_decay, out)
+    if len(shape) != 2:
+        raise ValueError(f"x must have 2 dimensions, got shape {tuple(shape)}")
+    batch, dim = shape
+    sp = _check("state", state, _F32, shape, device)
+    xs = _check_rows("x", x, _FLOATS, shape, device)
+    fs = _check_rows("gate", gate, (io,), shape, device)
+    bp = _check("gate_bias", gate_bias, _F32, (dim,), device)
+    if out is None:
+        out, ys = _like(x), 0
+    else:
+        ys = _check_rows("out", out, (io,), shape, device)
+    dims = _GATED.pack(batch, dim, 0, _DTYPE_CODE[io], bool(log_decay), 0, 0, 0, fs, 0, xs, 0, ys, 0,
+                       0, 0, 0, 0, 0, 0)
+    _finish("mamba_gated_state_update", library().mamba_gated_state_update(
+        sp, gate.data_ptr(), x.data_ptr(), bp, out.data_ptr(), dims, _handle(device)))
+    return out
 
 
 def causal_conv1d_bwd(x, weight, dout, bias=None, initial_conv_state=None, dfinal_conv_state=None,
@@ -987,40 +1002,38 @@ def causal_conv1d_bwd(x, weight, dout, bias=None, initial_conv_state=None, dfina
     (x's dtype), dweight (fp32), and dbias (fp32) and dinitial_conv_state (x's
     dtype) for the optional inputs given.
     """
-    if x.dim() != 3 or weight.dim() != 2:
+    device, io, shape = _needs_cuda("x", x)
+    if stream is not None or device.index != torch._C._cuda_getDevice():
+        return _elsewhere(causal_conv1d_bwd, device, stream, x, weight, dout, bias,
+                          initial_conv_state, dfinal_conv_state, silu, workspace)
+    if len(shape) != 3 or weight.dim() != 2:
         raise ValueError("x must be (batch, dim, L) and weight (dim, W)")
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    batch, dim, L = x.shape
+    batch, dim, L = shape
     W = weight.shape[1]
-    device, io, shape = x.device, x.dtype, x.shape
-    _check("x", x, _FLOATS, shape, device)
-    _check("dout", dout, (io,), shape, device)
-    _check("weight", weight, _F32, (dim, W), device)
-    _check("bias", bias, _F32, (dim,), device)
-    _check("initial_conv_state", initial_conv_state, (io,), (batch, dim, W), device)
-    _check("dfinal_conv_state", dfinal_conv_state, (io,), (batch, dim, W), device)
-    dims = _conv_dims(batch, dim, L, io)
-
-    def call(handle):
-        g = {"dx": torch.empty(shape, dtype=io, device=device),
-             "dweight": torch.empty((dim, W), dtype=torch.float32, device=device)}
-        if bias is not None:
-            g["dbias"] = torch.empty((dim,), dtype=torch.float32, device=device)
-        if initial_conv_state is not None:
-            g["dinitial_conv_state"] = torch.empty((batch, dim, W), dtype=io, device=device)
-        need = library().mamba_causal_conv1d_bwd_workspace_bytes(ctypes.byref(dims), W)
-        ws = _workspace(workspace, need, device, "mamba_causal_conv1d_bwd_workspace_bytes")
-        _set_workspace(dims, ws)
-        rc = library().mamba_causal_conv1d_bwd(
-            x.data_ptr(), weight.data_ptr(), _address(bias), _address(initial_conv_state), W,
-            int(bool(silu)), dout.data_ptr(), _address(dfinal_conv_state), g["dx"].data_ptr(),
-            g["dweight"].data_ptr(), _address(g.get("dbias")),
-            _address(g.get("dinitial_conv_state")), ctypes.byref(dims), handle)
-        _raise_on("mamba_causal_conv1d_bwd", rc)
-        return g
-
-    return _on(device, stream, call)
+    xp = _check("x", x, _FLOATS, shape, device)
+    yp = _check("dout", dout, (io,), shape, device)
+    wp = _check("weight", weight, _F32, (dim, W), device)
+    bp = _check("bias", bias, _F32, (dim,), device)
+    ip = _check("initial_conv_state", initial_conv_state, (io,), (batch, dim, W), device)
+    fp = _check("dfinal_conv_state", dfinal_conv_state, (io,), (batch, dim, W), device)
+    g = {"dx": _like(x), "dweight": _like(weight)}
+    dbp = dip = 0
+    if bias is not None:
+        g["dbias"] = _like(bias)
+        dbp = g["dbias"].data_ptr()
+    if initial_conv_state is not None:
+        g["dinitial_conv_state"] = _like(initial_conv_state)
+        dip = g["dinitial_conv_state"].data_ptr()
+    code = _DTYPE_CODE[io]
+    sizes = (batch, dim, 1, L, code, code, 0, 0, 0, 0)
+    need = _workspace_need("mamba_causal_conv1d_bwd_workspace_bytes", device.index,
+                           _DIMS.pack(*sizes, 0, 0), W)
+    ws = _workspace(workspace, need, device)
+    dims = _DIMS.pack(*sizes, 0, 0) if ws is None else _DIMS.pack(*sizes, ws.data_ptr(), ws.numel())
+    _finish("mamba_causal_conv1d_bwd", library().mamba_causal_conv1d_bwd(
+        xp, wp, bp, ip, W, bool(silu), yp, fp, g["dx"].data_ptr(), g["dweight"].data_ptr(), dbp, dip,
+        dims, _handle(device)))
+    return g
 
 
 def device_status() -> int:

@@ -340,3 +340,78 @@ def test_withheld_handoff_is_reported():
     assert ops.device_status() == 0
     want = ref.gated(**v, layout="bld")
     assert_close("out", ops.gated_scan_fwd(**v, layout="bld"), *want["out"])
+
+
+CHAINED = [(4, 2048, 1100), (2, 4160, 700), (130, 64, 70), (3, 2728, 130), (9, 1000, 600)]
+
+
+@pytest.mark.parametrize("log_decay", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("batch,dim,L", CHAINED)
+def test_many_chains(batch, dim, L, dtype, log_decay):
+    """128 groups of 64 channels and more: stretches of a chain handed from CTA to CTA."""
+    v, back = make(batch, dim, L, "bld", dtype, log_decay, seed=L)
+    check(v, back, "bld", log_decay)
+
+
+@pytest.mark.parametrize("checkpoints", ["given", "recomputed"])
+@pytest.mark.parametrize("L", [1, 63, 65, 577])
+def test_many_chains_padded(L, checkpoints):
+    v, back = make(10, 840, L, "bld", BF, False, seed=L, ragged=True)
+    outside = (torch.arange(L, device=DEV)[None] >= v["seqlens"][:, None])[:, :, None]
+    for t, bad in ((v["gate"], float("nan")), (v["x"], float("inf")), (back["dout"], float("nan"))):
+        t.copy_(torch.where(outside, torch.full_like(t, bad), t))
+    got, grads = check(v, back, "bld", False, checkpoints)
+    for t in (got[0], grads["dgate"], grads["dx"]):
+        assert (torch.where(outside, t, torch.zeros_like(t)) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_chains_strided(dtype):
+    """Halves of one tensor in and out, time-major memory, neighbours untouched."""
+    v, back = make(4, 2048, 140, "bld", dtype, False, seed=30)
+    both = torch.cat([v["gate"], v["x"]], dim=-1)
+    dboth = torch.full((4, 140, 4096 + 16), 7.0, dtype=dtype, device=DEV)
+    v2 = dict(v, gate=both[..., :2048], x=both[..., 2048:])
+    _, g = check(v2, back, "bld", False,
+                 bwd_kw=dict(dgate=dboth[..., :2048], dx=dboth[..., 2056:4104]))
+    assert (dboth[..., 2048:2056] == 7.0).all() and (dboth[..., 4104:] == 7.0).all()
+    tm = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    v3 = dict(v, gate=tm(v["gate"]), x=tm(v["x"]))
+    check(v3, dict(back, dout=tm(back["dout"])), "bld", False, fwd_kw=dict(out=tm(torch.zeros_like(v["x"]))))
+
+
+def test_many_chains_repeat_bit_for_bit_and_replay():
+    v, back = make(3, 4096, 1300, "bld", BF, False, seed=31)
+    run = lambda: (ops.gated_scan_fwd(**v, layout="bld"), ops.gated_scan_bwd(**v, **back, layout="bld"))  # noqa: E731
+    o, g = run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2, g2 = run()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2)
+        for k in g:
+            assert torch.equal(g[k], g2[k])
+    assert ops.device_status() == 0
+
+
+def test_many_chains_state_in_place():
+    v, _ = make(4, 2048, 700, "bld", F32, False, seed=32)
+    want = ref.gated(**v, layout="bld")
+    state = v["initial_state"].clone()
+    out, _ = ops.gated_scan_fwd(v["gate"], v["x"], v["gate_bias"], initial_state=state, last_state=state, layout="bld")
+    assert_close("out", out, *want["out"])
+    assert_close("last", state, *want["last_state"])
+
+
+def test_many_chains_withheld_handoff_is_reported():
+    v, _ = make(4, 2048, 2000, "bld", BF, False, seed=33)
+    ops.device_status()
+    ops.gated_scan_fwd(**v, layout="bld", flags=ops.MAMBA_FLAG_TEST_WITHHOLD_HANDOFF)
+    assert ops.STATUS_NAMES[ops.device_status()] == "MAMBA_ERR_TIMEOUT"
+    assert ops.device_status() == 0
+    want = ref.gated(**v, layout="bld")
+    assert_close("out", ops.gated_scan_fwd(**v, layout="bld"), *want["out"])
