@@ -151,6 +151,7 @@ mamba_status_t check_gated(const mamba_gated_dims_t* d) {
     if (d->batch >= kLimit31 || d->dim >= kLimit31 || d->seqlen >= kLimit31) return MAMBA_ERR_INVALID_ARG;
     if (!dtype_ok(d->io_dtype)) return MAMBA_ERR_UNSUPPORTED;
     if ((d->flags & ~(MAMBA_FLAG_LAYOUT_BLD | MAMBA_FLAG_TEST_WITHHOLD_HANDOFF)) != 0) return MAMBA_ERR_UNSUPPORTED;
+    if (d->seqlen > kMaxRowSteps) return MAMBA_ERR_UNSUPPORTED;
     // element counts stay far inside 64 bits
     if (d->batch > 0 && d->dim > 0 && d->seqlen > 0 &&
         (d->batch > ((int64_t)1 << 50) / d->dim || d->batch * d->dim > ((int64_t)1 << 50) / d->seqlen))
@@ -382,7 +383,7 @@ mamba_status_t run_gated_chain(const GatedParams& g, const GatedLayout& w, const
 template <typename IoT, bool kLog, bool kBackward>
 cudaError_t launch_gated_rows(const GatedParams& prm, const GatedLayout& w, cudaStream_t stream) {
     const int64_t per_cta = w.warps > 1 ? kGatedWarps / w.warps : (int64_t)kGatedWarps * (32 / w.width);
-    const unsigned grid = (unsigned)((prm.chains + per_cta - 1) / per_cta);
+    const unsigned grid = (unsigned)(((prm.chains + 1) / 2 + per_cta - 1) / per_cta);     // CTAs hold pairs of chains
 #define MAMBA_GATED_ROWS(W)                                                                          \
     if constexpr (kBackward)                                                                         \
         gated_scan_rows_bwd_kernel<IoT, kLog, W><<<grid, kGatedThreads, 0, stream>>>(prm, w.width); \
@@ -473,17 +474,18 @@ cudaError_t copy_or_zero(float* dst, const float* src, size_t bytes, cudaStream_
 
 struct ConvBwdPlan { int64_t stretch_tiles, stretches; size_t bytes; };
 
-// A warp per row; rows are cut into stretches of whole tiles while that leaves
-// fewer than 48 warps per SM.
+// A warp per pair of rows; rows are cut into stretches of whole tiles while
+// that leaves fewer than 48 warps per SM.
 mamba_status_t plan_conv_bwd(const mamba_dims_t* d, int width, int sms, ConvBwdPlan* n) {
     const int64_t chains = d->batch * d->dim;
     const int es = dtype_bytes(d->io_dtype);
     const int64_t tiles = std::max<int64_t>(1, (d->seqlen + 16 / es - 1 + kWarpSteps - 1) / kWarpSteps);
-    const int64_t want = chains > 0 ? ((int64_t)sms * 48 + chains - 1) / chains : 1;
+    const int64_t pairs = (chains + 1) / 2;
+    const int64_t want = pairs > 0 ? ((int64_t)sms * CONVW + pairs - 1) / pairs : 1;
     n->stretches = std::max<int64_t>(1, std::min<int64_t>(tiles, want));
     n->stretch_tiles = (tiles + n->stretches - 1) / n->stretches;
     n->stretches = (tiles + n->stretch_tiles - 1) / n->stretch_tiles;
-    if (chains * n->stretches / kConvBwdWarps >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
+    if (pairs * n->stretches / kConvBwdWarps >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
     n->bytes = align256((size_t)d->batch * n->stretches * (width + 1) * d->dim * sizeof(float));
     return MAMBA_OK;
 }
@@ -494,21 +496,29 @@ mamba_status_t check_conv_bwd(const mamba_dims_t* d, int width) {
     if (width < 1 || width > MAMBA_MAX_CONV_WIDTH) return MAMBA_ERR_UNSUPPORTED;
     if (!dtype_ok(d->io_dtype)) return MAMBA_ERR_UNSUPPORTED;
     if (d->batch >= kLimit31 || d->dim >= kLimit31 || d->seqlen >= kLimit31) return MAMBA_ERR_INVALID_ARG;
-    if (d->batch * d->dim >= ((int64_t)1 << 40)) return MAMBA_ERR_UNSUPPORTED;
+    if (d->batch * d->dim >= ((int64_t)1 << 40) || d->seqlen > kMaxRowSteps) return MAMBA_ERR_UNSUPPORTED;
     return MAMBA_OK;
 }
 
-template <typename IoT>
-cudaError_t launch_conv_bwd(const ConvBwdParams& prm, int width, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((prm.chains * prm.stretches + kConvBwdWarps - 1) / kConvBwdWarps);
-    constexpr int kThreads = kConvBwdWarps * 32;
-    switch (width) {
-        case 1: causal_conv1d_bwd_kernel<IoT, 1><<<grid, kThreads, 0, stream>>>(prm); break;
-        case 2: causal_conv1d_bwd_kernel<IoT, 2><<<grid, kThreads, 0, stream>>>(prm); break;
-        case 3: causal_conv1d_bwd_kernel<IoT, 3><<<grid, kThreads, 0, stream>>>(prm); break;
-        default: causal_conv1d_bwd_kernel<IoT, 4><<<grid, kThreads, 0, stream>>>(prm); break;
-    }
+template <typename IoT, int kW>
+cudaError_t launch_conv_bwd_width(const ConvBwdParams& prm, int dev, cudaStream_t stream) {
+    static bool attr_done[kMaxDevices] = {false};
+    constexpr int smem = ConvRing<IoT>::kBytes;
+    const cudaError_t e = ensure_smem_attr(causal_conv1d_bwd_kernel<IoT, kW>, smem, attr_done, dev);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((prm.pairs * prm.stretches + kConvBwdWarps - 1) / kConvBwdWarps);
+    causal_conv1d_bwd_kernel<IoT, kW><<<grid, kConvBwdWarps * 32, smem, stream>>>(prm);
     return cudaGetLastError();
+}
+
+template <typename IoT>
+cudaError_t launch_conv_bwd(const ConvBwdParams& prm, int width, int dev, cudaStream_t stream) {
+    switch (width) {
+        case 1: return launch_conv_bwd_width<IoT, 1>(prm, dev, stream);
+        case 2: return launch_conv_bwd_width<IoT, 2>(prm, dev, stream);
+        case 3: return launch_conv_bwd_width<IoT, 3>(prm, dev, stream);
+        default: return launch_conv_bwd_width<IoT, 4>(prm, dev, stream);
+    }
 }
 
 }  // namespace
@@ -687,7 +697,8 @@ MAMBA_API mamba_status_t mamba_causal_conv1d_bwd(
         (dinitial_conv_state != nullptr &&
          (dinitial_conv_state == initial_conv_state || dinitial_conv_state == dfinal_conv_state)))
         return MAMBA_ERR_INVALID_ARG;
-    const int sms = current_sm_count(nullptr);
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
     ConvBwdPlan n;
     st = plan_conv_bwd(dims, width, sms, &n);
@@ -707,11 +718,12 @@ MAMBA_API mamba_status_t mamba_causal_conv1d_bwd(
     prm.dim = dims->dim;
     prm.seqlen = dims->seqlen;
     prm.chains = chains;
+    prm.pairs = (chains + 1) / 2;
     prm.stretch_tiles = n.stretch_tiles;
     prm.stretches = n.stretches;
     prm.silu = silu != 0;
-    cudaError_t e = dims->io_dtype == MAMBA_BF16 ? launch_conv_bwd<__nv_bfloat16>(prm, width, stream)
-                                                 : launch_conv_bwd<float>(prm, width, stream);
+    cudaError_t e = dims->io_dtype == MAMBA_BF16 ? launch_conv_bwd<__nv_bfloat16>(prm, width, dev, stream)
+                                                 : launch_conv_bwd<float>(prm, width, dev, stream);
     if (e == cudaSuccess)
         e = launch_column_sum(prm.partial, dims->batch * n.stretches, (int64_t)(width + 1) * dims->dim,
                               (int64_t)width * dims->dim, dweight, dbias, stream);

@@ -8,11 +8,14 @@
 //
 // where x at negative times is the initial conv state (its gradient is the
 // same sum at those times).  HBM-bound: x and dout are read and dx is written
-// once.  A warp owns a stretch of one row and walks it from its end, 256 steps
-// at a time, eight per lane: the W-1 inputs before a lane's steps come from the
-// lane below by shuffle, the W-1 dpre after them from the lane above, or, for
-// the last lane, from the tile done before.  Only at the two ends of a stretch
-// are neighbours recomputed.  The weight and bias sums stay in registers until
+// once.  A warp owns a stretch of two neighbouring rows (one per half of its
+// packed fp32x2 arithmetic) and walks it from its end, 256 steps at a time,
+// eight per lane: the W-1 inputs before a lane's steps come from the lane below
+// by shuffle, the W-1 dpre after them from the lane above, or, for the last
+// lane, from the tile done before.  Only at the two ends of a stretch are
+// neighbours recomputed.  Each lane brings its own vectors of the coming tiles
+// into shared memory (cp.async), three or four tiles deep, so that loads are
+// under way while it computes.  The weight and bias sums stay in registers until
 // the stretch ends; each stretch leaves one partial per sum, and a second
 // launch adds the partials in a fixed order.
 #pragma once
@@ -22,6 +25,12 @@
 
 namespace mamba {
 
+#ifndef CONVMIN
+#define CONVMIN 2
+#endif
+#ifndef CONVW
+#define CONVW 48
+#endif
 constexpr int kConvBwdWarps = 8;
 
 struct ConvBwdParams {
@@ -35,178 +44,283 @@ struct ConvBwdParams {
     void* dinit;               // (batch, dim, W) or null
     float* partial;            // [batch * stretches][dim W | dim]: weight sums, then bias sums
     int64_t dim, seqlen, chains;
+    int64_t pairs;             // of rows
     int64_t stretch_tiles;     // tiles of 256 steps per stretch
     int64_t stretches;         // per row
     int silu;
 };
 
-template <int kW>
-__device__ __forceinline__ float conv_dpre(float pre, float dout, int silu) {
+// dout act'(pre) of two rows.
+__device__ __forceinline__ float2 conv_dpre2(float2 pre, float2 dout, int silu) {
     if (!silu) return dout;
-    const float sg = __fdividef(1.0f, 1.0f + ex2_approx(-pre * kLog2e));
-    return dout * sg * fmaf(pre, 1.0f - sg, 1.0f);
+    const float2 one = make_float2(1.0f, 1.0f);
+    const float2 t = __fmul2_rn(pre, make_float2(-kLog2e, -kLog2e));
+    const float2 e = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), one);
+    const float2 sg = make_float2(rcp_approx(e.x), rcp_approx(e.y));
+    const float2 rest = __ffma2_rn(sg, make_float2(-1.0f, -1.0f), one);
+    return __fmul2_rn(__fmul2_rn(dout, sg), __ffma2_rn(pre, rest, one));
 }
 
-// dpre at one step, everything read from memory (0 outside the row).
+// One row of a warp's pair.
 template <typename IoT, int kW>
-__device__ __forceinline__ float conv_dpre_at(const ConvBwdParams& p, const IoT* x, const IoT* dout,
-                                              const IoT* init, const float (&w)[kW], float b,
-                                              int64_t t) {
-    if (t < 0 || t >= p.seqlen) return 0.0f;
-    float pre = b;
-#pragma unroll
-    for (int k = 0; k < kW; ++k) {
-        const int64_t s = t - (kW - 1) + k;
-        const float xs = s >= 0 ? DType<IoT>::load(x + s)
-                                : (init != nullptr ? DType<IoT>::load(init + kW + s) : 0.0f);
-        pre = fmaf(w[k], xs, pre);
+struct ConvRow {
+    const IoT *x, *dout, *init, *dfinal;
+    IoT* dx;
+    int64_t chain, d;
+    int begin, lo, hi;                     // begin: the stretch's first step, before the row's start if negative
+    bool live;
+
+    __device__ __forceinline__ ConvRow(const ConvBwdParams& p, int64_t c, int64_t stretch) {
+        live = c < p.chains;
+        chain = live ? c : p.chains - 1;
+        d = chain % p.dim;
+        const int64_t at = chain * p.seqlen;
+        x = static_cast<const IoT*>(p.x) + at;
+        dout = static_cast<const IoT*>(p.dout) + at;
+        dx = static_cast<IoT*>(p.dx) + at;
+        init = p.init != nullptr ? static_cast<const IoT*>(p.init) + chain * kW : nullptr;
+        dfinal = p.dfinal != nullptr ? static_cast<const IoT*>(p.dfinal) + chain * kW : nullptr;
+        begin = (int)(stretch * p.stretch_tiles * kWarpSteps) - row_phase(x);
+        const int end = begin + (int)p.stretch_tiles * kWarpSteps, L = (int)p.seqlen;
+        lo = begin > 0 ? begin : 0;
+        hi = live ? (end < L ? end : L) : lo;
     }
-    return conv_dpre<kW>(pre, DType<IoT>::load(dout + t), p.silu);
-}
+
+    // x_s at any time: the row, the initial state before it, 0 elsewhere
+    __device__ __forceinline__ float input(int s, int L) const {
+        if (s >= 0) return s < L && live ? DType<IoT>::load(x + s) : 0.0f;
+        return init != nullptr && s >= -kW ? DType<IoT>::load(init + kW + s) : 0.0f;
+    }
+
+    // dpre at one step, everything read from memory (0 outside the row)
+    __device__ __forceinline__ float dpre(const ConvBwdParams& p, const float (&w)[kW], float b, int t) const {
+        if (t < 0 || t >= p.seqlen || !live) return 0.0f;
+        float pre = b;
+#pragma unroll
+        for (int k = 0; k < kW; ++k) pre = fmaf(w[k], input(t - (kW - 1) + k, (int)p.seqlen), pre);
+        const float g = DType<IoT>::load(dout + t);
+        return conv_dpre2(make_float2(pre, 0.0f), make_float2(g, 0.0f), p.silu).x;
+    }
+
+    // gradient of the initial state's entry j, and the stretch's sums
+    __device__ __forceinline__ void finish(const ConvBwdParams& p, const float (&w)[kW], float b, int64_t stretch,
+                                           int lane, const float (&dw)[kW], float db) const {
+        if (p.dinit != nullptr && stretch == 0 && lane < kW && live) {
+            float acc = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kW; ++k) acc = fmaf(w[k], dpre(p, w, b, lane - 1 - k), acc);
+            if (dfinal != nullptr && lane >= p.seqlen) acc += DType<IoT>::load(dfinal + (lane - p.seqlen));
+            DType<IoT>::store(static_cast<IoT*>(p.dinit) + chain * kW + lane, acc);
+        }
+        float* part = p.partial + ((chain / p.dim) * p.stretches + stretch) * (kW + 1) * p.dim;
+#pragma unroll
+        for (int k = 0; k <= kW; ++k) {
+            float v = k < kW ? dw[k < kW ? k : 0] : db;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0 && live) part[k < kW ? d * kW + k : p.dim * kW + d] = v;
+        }
+    }
+};
+
+// A warp's ring: per stage x and dout of both rows, a lane's vectors side by side.
+template <typename IoT>
+struct ConvRing {
+    static constexpr int kStages = sizeof(IoT) == 2 ? 4 : 3;
+    static constexpr int kVecs = (int)sizeof(IoT) / 2;           // of 16 bytes, per lane and tensor
+    static constexpr int kBytes = kConvBwdWarps * kStages * 4 * kVecs * 32 * 16;
+};
 
 template <typename IoT, int kW>
-__global__ void __launch_bounds__(kConvBwdWarps * 32)
+__global__ void __launch_bounds__(kConvBwdWarps * 32, CONVMIN)
     causal_conv1d_bwd_kernel(const __grid_constant__ ConvBwdParams p) {
     constexpr int H = kW > 1 ? kW - 1 : 1;               // neighbours on each side
+    using Ring = ConvRing<IoT>;
+    extern __shared__ uint4 ring_all[];                  // [warp][stage][x0, x1, dout0, dout1][vector][lane]
     const int lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * kConvBwdWarps + (threadIdx.x >> 5);
-    if (unit >= p.chains * p.stretches) return;          // whole warp leaves together
-    const int64_t chain = unit / p.stretches, stretch = unit % p.stretches;
-    const int64_t d = chain % p.dim, L = p.seqlen;
-    const IoT* x = static_cast<const IoT*>(p.x) + chain * L;
-    const IoT* dout = static_cast<const IoT*>(p.dout) + chain * L;
-    IoT* dx = static_cast<IoT*>(p.dx) + chain * L;
-    const IoT* init = p.init != nullptr ? static_cast<const IoT*>(p.init) + chain * kW : nullptr;
-    const IoT* dfinal = p.dfinal != nullptr ? static_cast<const IoT*>(p.dfinal) + chain * kW : nullptr;
-    float w[kW];
+    if (unit >= p.pairs * p.stretches) return;           // whole warp leaves together
+    uint4* ring = ring_all + (threadIdx.x >> 5) * (Ring::kStages * 4 * Ring::kVecs * 32);
+    const int64_t pair = unit / p.stretches, stretch = unit % p.stretches;
+    const int L = (int)p.seqlen;
+    const ConvRow<IoT, kW> r0(p, 2 * pair, stretch), r1(p, 2 * pair + 1, stretch);
+    const float2 zero = make_float2(0.0f, 0.0f);
+    float2 w[kW], dw[kW], db = zero;
 #pragma unroll
-    for (int k = 0; k < kW; ++k) w[k] = p.weight[d * kW + k];
-    const float b = p.bias != nullptr ? p.bias[d] : 0.0f;
-
-    // Stretch in steps: tiles start at multiples of 256 minus the row's phase.
-    const int phase = row_phase(x);
-    const int64_t begin = stretch * p.stretch_tiles * kWarpSteps - phase;
-    const int64_t end = begin + p.stretch_tiles * kWarpSteps;
-    const int64_t lo = begin > 0 ? begin : 0;
-    const int64_t hi = end < L ? end : L;
-
-    float dw[kW], db = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kW; ++k) dw[k] = 0.0f;
-    float later[H];                                      // the first H dpre after the tile (lane 31)
-#pragma unroll
-    for (int i = 0; i < H; ++i) later[i] = 0.0f;
-    if (kW > 1 && hi > lo && hi < L) {
-        const float mine = lane < kW - 1 ? conv_dpre_at<IoT, kW>(p, x, dout, init, w, b, hi + lane) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < kW - 1; ++i) later[i] = __shfl_sync(0xffffffffu, mine, i);
+    for (int k = 0; k < kW; ++k) {
+        w[k] = make_float2(p.weight[r0.d * kW + k], p.weight[r1.d * kW + k]);
+        dw[k] = zero;
     }
-    const int64_t tiles = hi > lo ? (hi - begin + kWarpSteps - 1) / kWarpSteps : 0;
-    for (int64_t tile = tiles - 1; tile >= 0; --tile) {
-        const int64_t t0 = begin + tile * kWarpSteps + lane * kLaneSteps;
-        float xv[8], dv[8], before[H];
-        load_steps(x, t0, lo, hi, 0.0f, xv);
-        load_steps(dout, t0, lo, hi, 0.0f, dv);
+    const float2 b = p.bias != nullptr ? make_float2(p.bias[r0.d], p.bias[r1.d]) : zero;
+    float w0[kW], w1[kW];
 #pragma unroll
-        for (int i = 0; i < H; ++i) before[i] = 0.0f;
+    for (int k = 0; k < kW; ++k) {
+        w0[k] = w[k].x;
+        w1[k] = w[k].y;
+    }
+
+    float2 later[H];                                     // the first H dpre after the tile (lane 31)
+#pragma unroll
+    for (int i = 0; i < H; ++i) later[i] = zero;
+    if (kW > 1 && ((r0.live && r0.hi < L) || (r1.live && r1.hi < L))) {   // a row goes on after the stretch
+        const bool ask = lane < kW - 1;
+        const float2 mine = make_float2(ask ? r0.dpre(p, w0, b.x, r0.hi + lane) : 0.0f,
+                                        ask ? r1.dpre(p, w1, b.y, r1.hi + lane) : 0.0f);
+#pragma unroll
+        for (int i = 0; i < kW - 1; ++i) later[i] = shfl2(mine, i);
+    }
+    const int span0 = r0.hi > r0.lo ? r0.hi - r0.begin : 0, span1 = r1.hi > r1.lo ? r1.hi - r1.begin : 0;
+    const int tiles = ((span0 > span1 ? span0 : span1) + kWarpSteps - 1) / kWarpSteps;
+    const int64_t total = p.chains * p.seqlen * (int64_t)sizeof(IoT);
+    const Span xspan{static_cast<const unsigned char*>(p.x), static_cast<const unsigned char*>(p.x) + total};
+    const Span dspan{static_cast<const unsigned char*>(p.dout), static_cast<const unsigned char*>(p.dout) + total};
+    // A vector travels through the ring when it is aligned and inside the tensor.
+    auto in_ring = [&](const IoT* q, const Span& span) {
+        return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && span.holds(q, 8 * (int)sizeof(IoT));
+    };
+    auto request = [&](int tile) {                   // one group per call, empty before the stretch
+        if (tile >= 0) {
+            uint4* slot = ring + (tile % Ring::kStages) * (4 * Ring::kVecs * 32) + lane;
+            const int o0 = r0.begin + tile * kWarpSteps + lane * kLaneSteps;
+            const int o1 = r1.begin + tile * kWarpSteps + lane * kLaneSteps;
+            const IoT* src[4] = {r0.x + o0, r1.x + o1, r0.dout + o0, r1.dout + o1};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in_ring(src[j], j < 2 ? xspan : dspan))
+#pragma unroll
+                    for (int v = 0; v < Ring::kVecs; ++v)
+                        copy_async16(smem_u32(slot + (j * Ring::kVecs + v) * 32), reinterpret_cast<const uint4*>(src[j]) + v);
+        }
+        copy_async_commit();
+    };
+    // A lane's eight steps of one tensor; masked to [lo, hi) by the caller.
+    auto take = [&](int tile, int j, const IoT* row, const Span& span, int t, int lo, int hi, float (&v)[8]) {
+        if (in_ring(row + t, span)) {
+            const uint4* slot = ring + (tile % Ring::kStages) * (4 * Ring::kVecs * 32) + lane;
+            uint4 raw[Ring::kVecs];
+#pragma unroll
+            for (int k = 0; k < Ring::kVecs; ++k) raw[k] = slot[(j * Ring::kVecs + k) * 32];
+            unpack_steps<IoT>(raw, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = (t + i >= lo && t + i < hi) ? DType<IoT>::load(row + t + i) : 0.0f;
+        }
+    };
+    // Input x_s of the tile before: its lane 31's vector holds steps base - 8 .. base - 1.
+    auto from_before = [&](int tile, int j, int i) {
+        const uint4* slot = ring + ((tile - 1) % Ring::kStages) * (4 * Ring::kVecs * 32) + 31;
+        const int e = 8 - (kW - 1) + i;
+        const IoT* q = reinterpret_cast<const IoT*>(slot + (j * Ring::kVecs + e * (int)sizeof(IoT) / 16) * 32);
+        return DType<IoT>::load(q + (e * (int)sizeof(IoT) % 16) / (int)sizeof(IoT));
+    };
+#pragma unroll
+    for (int k = 0; k < Ring::kStages - 1; ++k) request(tiles - 1 - k);
+    for (int tile = tiles - 1; tile >= 0; --tile) {
+        copy_async_wait<Ring::kStages - 3>();            // this tile and the one before it are here
+        __syncwarp();
+        const int b0 = r0.begin + tile * kWarpSteps, b1 = r1.begin + tile * kWarpSteps;
+        const int t0 = b0 + lane * kLaneSteps, t1 = b1 + lane * kLaneSteps;
+        // inside both rows, with neighbours before and no final state to add
+        const bool inner = b0 >= r0.lo && b1 >= r1.lo && b0 >= H && b1 >= H && b0 + kWarpSteps <= r0.hi &&
+                           b1 + kWarpSteps <= r1.hi && (p.dfinal == nullptr || (b0 + kWarpSteps <= L - kW && b1 + kWarpSteps <= L - kW));
+        float2 xv[8], dp[8], before[H], after[H];
+        {
+            float v0[8], v1[8], g0[8], g1[8];
+            take(tile, 0, r0.x, xspan, t0, r0.lo, r0.hi, v0);
+            take(tile, 1, r1.x, xspan, t1, r1.lo, r1.hi, v1);
+            take(tile, 2, r0.dout, dspan, t0, r0.lo, r0.hi, g0);
+            take(tile, 3, r1.dout, dspan, t1, r1.lo, r1.hi, g1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                xv[i] = make_float2(v0[i], v1[i]);
+                dp[i] = make_float2(g0[i], g1[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) before[i] = after[i] = zero;
+        if (!inner) {
+            // before the row's start: the initial state; behind its end: nothing
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (t0 + i < r0.lo || t0 + i >= r0.hi) xv[i].x = t0 + i < r0.lo ? r0.input(t0 + i, L) : 0.0f;
+                if (t1 + i < r1.lo || t1 + i >= r1.hi) xv[i].y = t1 + i < r1.lo ? r1.input(t1 + i, L) : 0.0f;
+            }
+        }
         if (kW > 1) {
-            // The kW-1 inputs before t0.  Lane 0, and the lane that holds the row's
-            // or the stretch's first steps, read them from memory.
-            float mem[H];
-            const bool edge = lane == 0 || (t0 - (kW - 1) < lo);
 #pragma unroll
-            for (int i = 0; i < kW - 1; ++i) {
-                mem[i] = 0.0f;
-                const int64_t s = t0 - (kW - 1) + i;
-                if (edge && s < hi) {
-                    if (s >= 0) mem[i] = DType<IoT>::load(x + s);
-                    else if (init != nullptr && s >= -kW) mem[i] = DType<IoT>::load(init + kW + s);
-                }
-            }
+            for (int i = 0; i < kW - 1; ++i) before[i] = shfl_up2(xv[8 - (kW - 1) + i], 1);
+            if (lane == 0)
 #pragma unroll
-            for (int i = 0; i < kW - 1; ++i) {
-                const float up = __shfl_up_sync(0xffffffffu, xv[8 - (kW - 1) + i], 1);
-                before[i] = edge ? mem[i] : up;
-            }
-            // A lane whose steps start before the row (phase > 0) sees the initial
-            // state inside its own eight.
-            if (t0 < 0 && init != nullptr)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t s = t0 + i;
-                    if (s < 0 && s >= -kW) xv[i] = DType<IoT>::load(init + kW + s);
+                for (int i = 0; i < kW - 1; ++i) {
+                    const int s0 = t0 - (kW - 1) + i, s1 = t1 - (kW - 1) + i;
+                    if (inner && tile > 0)
+                        before[i] = make_float2(from_before(tile, 0, i), from_before(tile, 1, i));
+                    else
+                        before[i] = make_float2(s0 < r0.hi ? r0.input(s0, L) : 0.0f, s1 < r1.hi ? r1.input(s1, L) : 0.0f);
                 }
         }
-        float dp[8];
+        __syncwarp();                                    // the slots read above are free again
+        request(tile - (Ring::kStages - 1));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float pre = b;
+            float2 pre = b;
 #pragma unroll
             for (int k = 0; k < kW; ++k) {
                 const int j = i - (kW - 1) + k;
-                pre = fmaf(w[k], j >= 0 ? xv[j] : before[kW - 1 + j], pre);
+                pre = __ffma2_rn(w[k], j >= 0 ? xv[j] : before[kW - 1 + j], pre);
             }
-            // steps outside [lo, hi) have dout 0 (pre may be anything there)
-            const bool in = t0 + i >= lo && t0 + i < hi;
-            dp[i] = in ? conv_dpre<kW>(pre, dv[i], p.silu) : 0.0f;
-            db += dp[i];
-#pragma unroll
-            for (int k = 0; k < kW; ++k) {
-                const int j = i - (kW - 1) + k;
-                const float xs = j >= 0 ? xv[j] : before[kW - 1 + j];
-                if (in) dw[k] = fmaf(dp[i], xs, dw[k]);
+            dp[i] = conv_dpre2(pre, dp[i], p.silu);
+            if (!inner) {                                // outside: dout was not read, x may be anything
+                if (t0 + i < r0.lo || t0 + i >= r0.hi) dp[i].x = 0.0f;
+                if (t1 + i < r1.lo || t1 + i >= r1.hi) dp[i].y = 0.0f;
             }
         }
-        // dpre after this lane's steps: the lane above, or the tile done before.
-        float after[H];
 #pragma unroll
-        for (int i = 0; i < H; ++i) after[i] = 0.0f;
+        for (int i = 0; i < 8; ++i) {
+            db = __fadd2_rn(db, dp[i]);
+#pragma unroll
+            for (int k = 0; k < kW; ++k) {
+                const int j = i - (kW - 1) + k;
+                dw[k] = __ffma2_rn(dp[i], j >= 0 ? xv[j] : before[kW - 1 + j], dw[k]);
+            }
+        }
+        // dpre after this lane's steps: the lane above, or the tile done before
         if (kW > 1) {
 #pragma unroll
             for (int i = 0; i < kW - 1; ++i) {
-                const float down = __shfl_down_sync(0xffffffffu, dp[i], 1);
+                const float2 down = shfl_down2(dp[i], 1);
                 after[i] = lane == 31 ? later[i] : down;
+                later[i] = shfl2(dp[i], 0);
             }
-#pragma unroll
-            for (int i = 0; i < kW - 1; ++i) later[i] = __shfl_sync(0xffffffffu, dp[i], 0);
         }
-        float o[8];
+        float2 o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float acc = 0.0f;
+            o[i] = zero;
 #pragma unroll
             for (int k = 0; k < kW; ++k) {
                 const int j = i + kW - 1 - k;
-                acc = fmaf(w[k], j < 8 ? dp[j] : after[j - 8 < H ? j - 8 : 0], acc);
+                o[i] = __ffma2_rn(w[k], j < 8 ? dp[j] : after[j - 8 < H ? j - 8 : 0], o[i]);
             }
-            o[i] = acc;
         }
-        if (dfinal != nullptr && t0 + 8 > L - kW)
+        if (!inner && p.dfinal != nullptr) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int64_t t = t0 + i;
-                if (t >= L - kW && t >= 0 && t < L) o[i] += DType<IoT>::load(dfinal + (t + kW - L));
+                const int f0 = t0 + i + kW - L, f1 = t1 + i + kW - L;
+                if (f0 >= 0 && f0 < kW && t0 + i >= 0) o[i].x += DType<IoT>::load(r0.dfinal + f0);
+                if (f1 >= 0 && f1 < kW && t1 + i >= 0) o[i].y += DType<IoT>::load(r1.dfinal + f1);
             }
-        store_steps(dx, t0, lo, hi, o);
+        }
+        store_steps2(r0.dx, t0, r0.lo, r0.hi, r1.dx, t1, r1.lo, r1.hi, o);
     }
-    // Gradient of the initial state: the same sum at times -W .. -1.
-    if (p.dinit != nullptr && stretch == 0 && lane < kW) {
-        const int64_t s = lane - kW;
-        float acc = 0.0f;
+    float s0[kW], s1[kW];
 #pragma unroll
-        for (int k = 0; k < kW; ++k)
-            acc = fmaf(w[k], conv_dpre_at<IoT, kW>(p, x, dout, init, w, b, s + kW - 1 - k), acc);
-        if (dfinal != nullptr && lane >= L) acc += DType<IoT>::load(dfinal + (lane - L));
-        DType<IoT>::store(static_cast<IoT*>(p.dinit) + chain * kW + lane, acc);
+    for (int k = 0; k < kW; ++k) {
+        s0[k] = dw[k].x;
+        s1[k] = dw[k].y;
     }
-    float* part = p.partial + ((chain / p.dim) * p.stretches + stretch) * (kW + 1) * p.dim;
-#pragma unroll
-    for (int k = 0; k <= kW; ++k) {
-        float v = k < kW ? dw[k < kW ? k : 0] : db;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) part[k < kW ? d * kW + k : p.dim * kW + d] = v;
-    }
+    r0.finish(p, w0, b.x, stretch, lane, s0, db.x);
+    r1.finish(p, w1, b.y, stretch, lane, s1, db.y);
 }
 
 }  // namespace mamba

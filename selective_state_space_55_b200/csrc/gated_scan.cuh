@@ -35,9 +35,9 @@
 // all chains first, so that every segment's predecessors belong to CTAs that
 // are running or done; the wait is bounded all the same.
 //
-// Layout (batch, dim, seqlen): a lane takes 8 consecutive steps of one chain,
-// the warp composes its lanes' maps by shuffles, and 1 to 8 warps per chain
-// share a tile through shared memory.  Chains are plentiful here (one per
+// Layout (batch, dim, seqlen): a lane takes 8 consecutive steps of two
+// neighbouring chains, the warp composes its lanes' maps by shuffles, and 1 to 8
+// warps share a tile of a pair through shared memory.  Chains are plentiful here (one per
 // channel instead of one per 64), so a chain stays with its warps and nothing
 // waits.
 #pragma once
@@ -94,12 +94,6 @@ constexpr unsigned int kGatedPollLimit = 1u << 19;
 // and a = e g for f >= 0, 1 - g (rounded to nearest) for f < 0: there a is close
 // to 1, it is applied over about 1 / g steps, and a biased rounding would grow
 // with that memory.  e = inf gives g = 0, a = 1.
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void sigmoid_gate2(float2 f2, float2& g, float2& a) {
     const float2 one = make_float2(1.0f, 1.0f);
     const float2 e = make_float2(ex2_approx(-f2.x), ex2_approx(-f2.y));
@@ -677,231 +671,308 @@ __global__ void __launch_bounds__(kGatedThreads, GBMIN)
 }
 
 // ------------------------------------------------ (batch, dim, seqlen) layout
+// Two neighbouring chains side by side, one per half of the packed arithmetic.
 
-// Inclusive compositions over the first lanes of a team of `width` lanes
-// (kReverse: from the team's last lane down): on return (A, H) is the map of
-// every lane before this one in scan order, (At, Ht) of the whole team.
+// Compositions over a team of `width` lanes in scan order (kReverse: from the
+// team's last lane down): on return (A, H) is the map of every lane before this
+// one, (At, Ht) of the whole team.
 template <bool kReverse>
-__device__ __forceinline__ void team_scan(float& A, float& H, float& At, float& Ht, int lane, int width) {
+__device__ __forceinline__ void team_scan(float2& A, float2& H, float2& At, float2& Ht, int lane, int width) {
     const int rank = lane & (width - 1);
     const int first = kReverse ? width - 1 : 0;
-    for (int o = 1; o < width; o <<= 1) {
-        const float Ao = kReverse ? __shfl_down_sync(0xffffffffu, A, o, width) : __shfl_up_sync(0xffffffffu, A, o, width);
-        const float Ho = kReverse ? __shfl_down_sync(0xffffffffu, H, o, width) : __shfl_up_sync(0xffffffffu, H, o, width);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        if (o >= width) break;
+        const float2 Ao = kReverse ? shfl_down2(A, o, width) : shfl_up2(A, o, width);
+        const float2 Ho = kReverse ? shfl_down2(H, o, width) : shfl_up2(H, o, width);
         if (kReverse ? rank + o < width : rank >= o) {
-            H = fmaf(A, Ho, H);
-            A *= Ao;
+            H = __ffma2_rn(A, Ho, H);
+            A = __fmul2_rn(A, Ao);
         }
     }
-    At = __shfl_sync(0xffffffffu, A, width - 1 - first, width);
-    Ht = __shfl_sync(0xffffffffu, H, width - 1 - first, width);
-    const float Ae = kReverse ? __shfl_down_sync(0xffffffffu, A, 1, width) : __shfl_up_sync(0xffffffffu, A, 1, width);
-    const float He = kReverse ? __shfl_down_sync(0xffffffffu, H, 1, width) : __shfl_up_sync(0xffffffffu, H, 1, width);
-    A = rank == first ? 1.0f : Ae;
-    H = rank == first ? 0.0f : He;
+    At = shfl2(A, width - 1 - first, width);
+    Ht = shfl2(H, width - 1 - first, width);
+    const float2 Ae = kReverse ? shfl_down2(A, 1, width) : shfl_up2(A, 1, width);
+    const float2 He = kReverse ? shfl_down2(H, 1, width) : shfl_up2(H, 1, width);
+    A = rank == first ? make_float2(1.0f, 1.0f) : Ae;
+    H = rank == first ? make_float2(0.0f, 0.0f) : He;
 }
 
-// Composes the maps of the kWarps warps that share a chain: (A, H) gains the
-// maps of the warps before this one in scan order, (At, Ht) becomes the map of
-// the whole tile.  `buf` is [kGatedWarps] shared pairs; two of them used in turn.
+// Composes the maps of the kWarps warps that share a pair of chains: (A, H)
+// gains the maps of the warps before this one in scan order, (At, Ht) becomes
+// the map of the whole tile.  `buf` holds one entry per warp of the CTA; two of
+// them are used in turn.
 template <int kWarps, bool kReverse>
-__device__ __forceinline__ void join_warps(float& A, float& H, float& At, float& Ht, float2* buf,
+__device__ __forceinline__ void join_warps(float2& A, float2& H, float2& At, float2& Ht, float4* buf,
                                            int warp, int lane) {
     if constexpr (kWarps > 1) {
-        if (lane == 0) buf[warp] = make_float2(At, Ht);
+        if (lane == 0) buf[warp] = make_float4(At.x, At.y, Ht.x, Ht.y);
         __syncthreads();
         const int base = warp / kWarps * kWarps, rank = warp - base;
-        float2 mine = make_float2(1.0f, 0.0f), all = make_float2(1.0f, 0.0f);
+        float2 mA = make_float2(1.0f, 1.0f), mH = make_float2(0.0f, 0.0f), aA = mA, aH = mH;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
             const int v = kReverse ? kWarps - 1 - k : k;
-            if (v == rank) mine = all;
-            const float2 m = buf[base + v];
-            all.y = fmaf(m.x, all.y, m.y);
-            all.x *= m.x;
+            if (v == rank) {
+                mA = aA;
+                mH = aH;
+            }
+            const float4 m = buf[base + v];
+            aH = __ffma2_rn(make_float2(m.x, m.y), aH, make_float2(m.z, m.w));
+            aA = __fmul2_rn(aA, make_float2(m.x, m.y));
         }
-        H = fmaf(A, mine.y, H);
-        A *= mine.x;
-        At = all.x;
-        Ht = all.y;
+        H = __ffma2_rn(A, mH, H);
+        A = __fmul2_rn(A, mA);
+        At = aA;
+        Ht = aH;
     }
 }
 
-// A lane's place: kWarps warps per chain; with one, `width` lanes per chain.
-template <int kWarps>
-struct GatedChainAt {
-    int64_t chain, b, d, n, step;     // step: time steps per tile
-    int64_t offset;                   // first step of this lane in tile 0, before the phase
-    bool live;
-    __device__ __forceinline__ GatedChainAt(const GatedParams& p, int warp, int lane, int width) {
+// A lane's place: kWarps warps per pair of chains; with one, `width` lanes per pair.
+struct GatedRow {
+    int64_t chain, b, d;
+    int n, hi, shift;                       // steps of the sequence, of the tensor; first step of this
+    bool live;                              // lane in tile 0
+};
+
+template <typename IoT>
+__device__ __forceinline__ GatedRow gated_row(const GatedParams& p, int64_t chain, int offset) {
+    GatedRow r;
+    r.live = chain < p.chains;
+    r.chain = r.live ? chain : p.chains - 1;
+    r.b = r.chain / p.dim;
+    r.d = r.chain - r.b * p.dim;
+    r.n = r.live ? (int)gated_length(p, r.b) : 0;
+    r.hi = r.live ? (int)p.seqlen : 0;
+    r.shift = offset - row_phase(static_cast<const IoT*>(p.gate) + r.b * p.gate_s.batch + r.d * p.gate_s.row);
+    return r;
+}
+
+template <typename IoT>
+__device__ __forceinline__ const IoT* row_of(const void* base, const GatedStrides& s, const GatedRow& r) {
+    return static_cast<const IoT*>(base) + r.b * s.batch + r.d * s.row;
+}
+
+// The bytes between a tensor's first and last element, (batch, dim) rows of seqlen.
+template <typename IoT>
+__device__ __forceinline__ Span gated_span(const GatedParams& p, const void* base, const GatedStrides& s) {
+    const unsigned char* b = static_cast<const unsigned char*>(base);
+    return {b, b + ((p.batch - 1) * s.batch + (p.dim - 1) * s.row + p.seqlen) * (int64_t)sizeof(IoT)};
+}
+
+template <int kWarps, typename IoT>
+struct GatedRows {
+    int step, offset;                       // steps per tile; this lane's place in it
+    GatedRow r0, r1;
+    __device__ __forceinline__ GatedRows(const GatedParams& p, int warp, int lane, int width) {
+        int64_t pair;
         if (kWarps > 1) {
-            chain = (int64_t)blockIdx.x * (kGatedWarps / kWarps) + warp / kWarps;
+            pair = (int64_t)blockIdx.x * (kGatedWarps / kWarps) + warp / kWarps;
             offset = (warp % kWarps) * kWarpSteps + lane * kLaneSteps;
             step = kWarps * kWarpSteps;
         } else {
-            const int64_t teams = 32 / width;
-            chain = ((int64_t)blockIdx.x * kGatedWarps + warp) * teams + lane / width;
+            pair = ((int64_t)blockIdx.x * kGatedWarps + warp) * (32 / width) + lane / width;
             offset = (lane & (width - 1)) * kLaneSteps;
-            step = (int64_t)width * kLaneSteps;
+            step = width * kLaneSteps;
         }
-        live = chain < p.chains;
-        if (!live) chain = p.chains - 1;
-        b = chain / p.dim;
-        d = chain - b * p.dim;
-        n = live ? gated_length(p, b) : 0;
+        r0 = gated_row<IoT>(p, 2 * pair, offset);
+        r1 = gated_row<IoT>(p, 2 * pair + 1, offset);
+    }
+    __device__ __forceinline__ float2 pick(const float* v, int64_t i0, int64_t i1) const {
+        return v != nullptr ? make_float2(v[i0], v[i1]) : make_float2(0.0f, 0.0f);
+    }
+    // one value per chain
+    __device__ __forceinline__ void put(float* v, float2 x) const {
+        if (v == nullptr || offset != 0) return;
+        if (r0.live) v[r0.chain] = x.x;
+        if (r1.live) v[r1.chain] = x.y;
     }
 };
+
+// Gains of a lane's eight steps; steps outside a sequence pass the state on.
+template <bool kLog>
+__device__ __forceinline__ void row_gains(float2 (&a)[8], float2 (&g)[8], float2 bias2, int t0, int n0, int t1,
+                                          int n1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gated_gains2<kLog>(a[i], bias2, g[i], a[i]);
+    if (t0 < 0 || t1 < 0 || t0 + 8 > n0 || t1 + 8 > n1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (t0 + i < 0 || t0 + i >= n0) {
+                a[i].x = 1.0f;
+                g[i].x = 0.0f;
+            }
+            if (t1 + i < 0 || t1 + i >= n1) {
+                a[i].y = 1.0f;
+                g[i].y = 0.0f;
+            }
+        }
+}
 
 template <typename IoT, bool kLog, int kWarps>
 __global__ void __launch_bounds__(kGatedThreads)
     gated_scan_rows_fwd_kernel(const __grid_constant__ GatedParams p, int width) {
-    __shared__ float2 buf[2][kGatedWarps];
+    __shared__ float4 buf[2][kGatedWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const GatedChainAt<kWarps> at(p, warp, lane, width);
-    const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + at.d * p.gate_s.row;
-    const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.d * p.x_s.row;
-    IoT* out = static_cast<IoT*>(p.out) + at.b * p.out_s.batch + at.d * p.out_s.row;
-    const int64_t hi = at.live ? p.seqlen : 0;
-    const float bias = p.bias != nullptr ? p.bias[at.d] : 0.0f;
-    float carry = p.h0 != nullptr ? p.h0[at.chain] : 0.0f;
-    const int64_t shift = at.offset - row_phase(gate);
-    for (int64_t tile = 0; tile < p.tiles; ++tile) {
-        const int64_t t0 = tile * at.step + shift;
-        float a[8], u[8], x8[8];
-        load_steps(gate, t0, 0, at.n, 0.0f, a);
-        load_steps(x, t0, 0, at.n, 0.0f, x8);
-        float A = 1.0f, H = 0.0f, At, Ht;
+    const GatedRows<kWarps, IoT> at(p, warp, lane, width);
+    const int tiles = (int)p.tiles;
+    const IoT *gate0 = row_of<IoT>(p.gate, p.gate_s, at.r0), *gate1 = row_of<IoT>(p.gate, p.gate_s, at.r1);
+    const IoT *x0 = row_of<IoT>(p.x, p.x_s, at.r0), *x1 = row_of<IoT>(p.x, p.x_s, at.r1);
+    const Span gspan = gated_span<IoT>(p, p.gate, p.gate_s), xspan = gated_span<IoT>(p, p.x, p.x_s);
+    IoT* out0 = const_cast<IoT*>(row_of<IoT>(p.out, p.out_s, at.r0));
+    IoT* out1 = const_cast<IoT*>(row_of<IoT>(p.out, p.out_s, at.r1));
+    const float2 bias2 = __fmul2_rn(at.pick(p.bias, at.r0.d, at.r1.d), make_float2(kLog2e, kLog2e));
+    float2 carry = at.pick(p.h0, at.r0.chain, at.r1.chain);
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int t0 = tile * at.step + at.r0.shift, t1 = tile * at.step + at.r1.shift;
+        float2 a[8], u[8], g[8];
+        load_steps2(gate0, t0, 0, at.r0.n, gate1, t1, 0, at.r1.n, gspan, a);
+        load_steps2(x0, t0, 0, at.r0.n, x1, t1, 0, at.r1.n, xspan, u);
+        row_gains<kLog>(a, g, bias2, t0, at.r0.n, t1, at.r1.n);
+        float2 A = make_float2(1.0f, 1.0f), H = make_float2(0.0f, 0.0f), At, Ht;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            gated_terms<kLog>(a[i], bias, x8[i], a[i], u[i]);
-            if (t0 + i < 0 || t0 + i >= at.n) {
-                a[i] = 1.0f;
-                u[i] = 0.0f;
-            }
-            H = fmaf(a[i], H, u[i]);
-            A *= a[i];
+            if constexpr (!kLog) u[i] = __fmul2_rn(g[i], u[i]);
+            H = __ffma2_rn(a[i], H, u[i]);
+            A = __fmul2_rn(A, a[i]);
         }
         team_scan<false>(A, H, At, Ht, lane, width);
         join_warps<kWarps, false>(A, H, At, Ht, buf[tile & 1], warp, lane);
-        float h = fmaf(A, carry, H);
-        carry = fmaf(At, carry, Ht);
+        float2 h = __ffma2_rn(A, carry, H);
+        carry = __ffma2_rn(At, carry, Ht);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            h = fmaf(a[i], h, u[i]);
-            u[i] = t0 + i < at.n ? h : 0.0f;
+            h = __ffma2_rn(a[i], h, u[i]);
+            u[i] = h;
         }
-        store_steps(out, t0, 0, hi, u);
+        if (t0 + 8 > at.r0.n || t1 + 8 > at.r1.n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (t0 + i >= at.r0.n) u[i].x = 0.0f;
+                if (t1 + i >= at.r1.n) u[i].y = 0.0f;
+            }
+        store_steps2(out0, t0, 0, at.r0.hi, out1, t1, 0, at.r1.hi, u);
     }
-    if (p.last != nullptr && at.live && at.offset == 0) p.last[at.chain] = carry;
+    at.put(p.last, carry);
 }
 
 // Backward: with more than one tile per chain, a first sweep keeps the states
 // entering the tiles; the second runs from the last tile to the first and reads
 // gate and x again (from L2 while the chains in flight fit there).
 template <typename IoT, bool kLog, int kWarps>
-__global__ void __launch_bounds__(kGatedThreads)
+__global__ void __launch_bounds__(kGatedThreads, 2)
     gated_scan_rows_bwd_kernel(const __grid_constant__ GatedParams p, int width) {
-    __shared__ float2 buf[2][kGatedWarps];
-    __shared__ float2 back[2][kGatedWarps];
+    __shared__ float4 buf[2][kGatedWarps];
+    __shared__ float4 back[2][kGatedWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const GatedChainAt<kWarps> at(p, warp, lane, width);
-    const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + at.d * p.gate_s.row;
-    const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.d * p.x_s.row;
-    const IoT* dout = static_cast<const IoT*>(p.dout) + at.b * p.out_s.batch + at.d * p.out_s.row;
-    IoT* dgate = static_cast<IoT*>(p.dgate) + at.b * p.dgate_s.batch + at.d * p.dgate_s.row;
-    IoT* dx = static_cast<IoT*>(p.dx) + at.b * p.dx_s.batch + at.d * p.dx_s.row;
-    const int64_t hi = at.live ? p.seqlen : 0;
-    const float bias = p.bias != nullptr ? p.bias[at.d] : 0.0f;
-    const int64_t shift = at.offset - row_phase(gate);
-    float* states = p.chain_states + at.chain * p.tiles;
-    float carry = p.h0 != nullptr ? p.h0[at.chain] : 0.0f;
-    for (int64_t tile = 0; tile + 1 < p.tiles; ++tile) {
-        const int64_t t0 = tile * at.step + shift;
-        float f[8], x8[8];
-        load_steps(gate, t0, 0, at.n, 0.0f, f);
-        load_steps(x, t0, 0, at.n, 0.0f, x8);
-        float A = 1.0f, H = 0.0f, At, Ht;
+    const float2 one = make_float2(1.0f, 1.0f), zero = make_float2(0.0f, 0.0f);
+    const GatedRows<kWarps, IoT> at(p, warp, lane, width);
+    const int tiles = (int)p.tiles;
+    const IoT *gate0 = row_of<IoT>(p.gate, p.gate_s, at.r0), *gate1 = row_of<IoT>(p.gate, p.gate_s, at.r1);
+    const IoT *x0 = row_of<IoT>(p.x, p.x_s, at.r0), *x1 = row_of<IoT>(p.x, p.x_s, at.r1);
+    const Span gspan = gated_span<IoT>(p, p.gate, p.gate_s), xspan = gated_span<IoT>(p, p.x, p.x_s);
+    const float2 bias2 = __fmul2_rn(at.pick(p.bias, at.r0.d, at.r1.d), make_float2(kLog2e, kLog2e));
+    float* states0 = p.chain_states + at.r0.chain * p.tiles;
+    float* states1 = p.chain_states + at.r1.chain * p.tiles;
+    float2 carry = at.pick(p.h0, at.r0.chain, at.r1.chain);
+    for (int tile = 0; tile + 1 < tiles; ++tile) {
+        const int t0 = tile * at.step + at.r0.shift, t1 = tile * at.step + at.r1.shift;
+        float2 a[8], x[8], g[8];
+        load_steps2(gate0, t0, 0, at.r0.n, gate1, t1, 0, at.r1.n, gspan, a);
+        load_steps2(x0, t0, 0, at.r0.n, x1, t1, 0, at.r1.n, xspan, x);
+        row_gains<kLog>(a, g, bias2, t0, at.r0.n, t1, at.r1.n);
+        float2 A = one, H = zero, At, Ht;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float a, u;
-            gated_terms<kLog>(f[i], bias, x8[i], a, u);
-            if (t0 + i < 0 || t0 + i >= at.n) {
-                a = 1.0f;
-                u = 0.0f;
-            }
-            H = fmaf(a, H, u);
-            A *= a;
+            H = __ffma2_rn(a[i], H, kLog ? x[i] : __fmul2_rn(g[i], x[i]));
+            A = __fmul2_rn(A, a[i]);
         }
         team_scan<false>(A, H, At, Ht, lane, width);
         join_warps<kWarps, false>(A, H, At, Ht, buf[tile & 1], warp, lane);
-        if (at.live && at.offset == 0) states[tile] = carry;
-        carry = fmaf(At, carry, Ht);
+        if (at.offset == 0) {
+            if (at.r0.live) states0[tile] = carry.x;
+            if (at.r1.live) states1[tile] = carry.y;
+        }
+        carry = __ffma2_rn(At, carry, Ht);
     }
     if (kWarps > 1) __syncthreads();
     else __syncwarp();
-    float r_carry = p.dlast != nullptr ? p.dlast[at.chain] : 0.0f;
-    float db = 0.0f;
-    for (int64_t tile = p.tiles - 1; tile >= 0; --tile) {
-        const int64_t t0 = tile * at.step + shift;
-        float a[8], g[8], x8[8], d8[8], before[8];
-        load_steps(gate, t0, 0, at.n, 0.0f, a);
-        load_steps(x, t0, 0, at.n, 0.0f, x8);
-        load_steps(dout, t0, 0, at.n, 0.0f, d8);
-        if (tile + 1 < p.tiles) carry = states[tile];
-        float A = 1.0f, H = 0.0f, At, Ht;
+    const IoT *dout0 = row_of<IoT>(p.dout, p.out_s, at.r0), *dout1 = row_of<IoT>(p.dout, p.out_s, at.r1);
+    const Span dspan = gated_span<IoT>(p, p.dout, p.out_s);
+    IoT* dgate0 = const_cast<IoT*>(row_of<IoT>(p.dgate, p.dgate_s, at.r0));
+    IoT* dgate1 = const_cast<IoT*>(row_of<IoT>(p.dgate, p.dgate_s, at.r1));
+    IoT* dx0 = const_cast<IoT*>(row_of<IoT>(p.dx, p.dx_s, at.r0));
+    IoT* dx1 = const_cast<IoT*>(row_of<IoT>(p.dx, p.dx_s, at.r1));
+    float2 r_carry = at.pick(p.dlast, at.r0.chain, at.r1.chain);
+    float2 db = zero;
+    for (int tile = tiles - 1; tile >= 0; --tile) {
+        const int t0 = tile * at.step + at.r0.shift, t1 = tile * at.step + at.r1.shift;
+        float2 a[8], g[8], x[8], dd[8];
+        load_steps2(gate0, t0, 0, at.r0.n, gate1, t1, 0, at.r1.n, gspan, a);
+        load_steps2(x0, t0, 0, at.r0.n, x1, t1, 0, at.r1.n, xspan, x);
+        load_steps2(dout0, t0, 0, at.r0.n, dout1, t1, 0, at.r1.n, dspan, dd);
+        if (tile + 1 < tiles) carry = make_float2(states0[tile], states1[tile]);
+        row_gains<kLog>(a, g, bias2, t0, at.r0.n, t1, at.r1.n);
+        float2 A = one, H = zero, At, Ht;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            gated_gains<kLog>(a[i], bias, g[i], a[i]);
-            if (t0 + i < 0 || t0 + i >= at.n) {
-                a[i] = 1.0f;
-                g[i] = 0.0f;
-            }
-            H = fmaf(a[i], H, g[i] * x8[i]);
-            A *= a[i];
+            H = __ffma2_rn(a[i], H, kLog ? x[i] : __fmul2_rn(g[i], x[i]));
+            A = __fmul2_rn(A, a[i]);
         }
-        float B = A, R = 0.0f, Bt, Rt;
+        float2 B = A, R = zero, Bt, Rt;
 #pragma unroll
-        for (int i = 7; i >= 0; --i) R = a[i] * (d8[i] + R);
+        for (int i = 7; i >= 0; --i) R = __fmul2_rn(a[i], __fadd2_rn(dd[i], R));
         team_scan<false>(A, H, At, Ht, lane, width);
         team_scan<true>(B, R, Bt, Rt, lane, width);
-        // the reverse join's barrier covers the forward one's buffer as well
         join_warps<kWarps, false>(A, H, At, Ht, buf[tile & 1], warp, lane);
         join_warps<kWarps, true>(B, R, Bt, Rt, back[tile & 1], warp, lane);
-        float h = fmaf(A, carry, H);
-        float r = fmaf(B, r_carry, R);
-        r_carry = fmaf(Bt, r_carry, Rt);
+        float2 h = __ffma2_rn(A, carry, H);
+        float2 r = __ffma2_rn(B, r_carry, R);
+        r_carry = __ffma2_rn(Bt, r_carry, Rt);
+        // x becomes what the decay's gradient multiplies: x_t - h_{t-1}, or h_{t-1}
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            before[i] = h;
-            h = fmaf(a[i], h, g[i] * x8[i]);
+            const float2 u = kLog ? x[i] : __fmul2_rn(g[i], x[i]);
+            x[i] = kLog ? h : __ffma2_rn(h, make_float2(-1.0f, -1.0f), x[i]);
+            h = __ffma2_rn(a[i], h, u);
         }
 #pragma unroll
         for (int i = 7; i >= 0; --i) {
-            const float l = d8[i] + r;
-            r = a[i] * l;
-            const bool in = t0 + i >= 0 && t0 + i < at.n;
-            const float df = kLog ? r * before[i] : g[i] * r * (x8[i] - before[i]);
-            const float dv = kLog ? l : g[i] * l;
-            d8[i] = in ? df : 0.0f;
-            x8[i] = in ? dv : 0.0f;
-            db += d8[i];
+            const float2 l = __fadd2_rn(dd[i], r);
+            r = __fmul2_rn(a[i], l);
+            dd[i] = __fmul2_rn(r, x[i]);
+            x[i] = l;
+            if constexpr (!kLog) {
+                dd[i] = __fmul2_rn(g[i], dd[i]);
+                x[i] = __fmul2_rn(g[i], l);
+            }
         }
-        store_steps(dgate, t0, 0, hi, d8);
-        store_steps(dx, t0, 0, hi, x8);
+        if (t0 < 0 || t1 < 0 || t0 + 8 > at.r0.n || t1 + 8 > at.r1.n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (t0 + i < 0 || t0 + i >= at.r0.n) dd[i].x = x[i].x = 0.0f;
+                if (t1 + i < 0 || t1 + i >= at.r1.n) dd[i].y = x[i].y = 0.0f;
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) db = __fadd2_rn(db, dd[i]);
+        store_steps2(dgate0, t0, 0, at.r0.hi, dgate1, t1, 0, at.r1.hi, dd);
+        store_steps2(dx0, t0, 0, at.r0.hi, dx1, t1, 0, at.r1.hi, x);
     }
-    if (p.dh0 != nullptr && at.live && at.offset == 0) p.dh0[at.chain] = r_carry;
+    at.put(p.dh0, r_carry);
     if (p.bias_partial != nullptr) {
-        for (int o = width / 2; o > 0; o >>= 1) db += __shfl_xor_sync(0xffffffffu, db, o, width);
+        for (int o = width / 2; o > 0; o >>= 1)
+            db = __fadd2_rn(db, make_float2(__shfl_xor_sync(0xffffffffu, db.x, o, width),
+                                            __shfl_xor_sync(0xffffffffu, db.y, o, width)));
         if constexpr (kWarps > 1) {
             __syncthreads();
-            if (lane == 0) buf[0][warp].x = db;
+            if (lane == 0) buf[0][warp] = make_float4(db.x, db.y, 0.0f, 0.0f);
             __syncthreads();
-            db = 0.0f;
+            db = zero;
             const int base = warp / kWarps * kWarps;
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) db += buf[0][base + v].x;
+            for (int v = 0; v < kWarps; ++v) db = __fadd2_rn(db, make_float2(buf[0][base + v].x, buf[0][base + v].y));
         }
-        if (at.live && at.offset == 0) p.bias_partial[at.chain] = db;
+        at.put(p.bias_partial, db);
     }
 }
 
@@ -936,12 +1007,12 @@ __global__ void __launch_bounds__(kGatedUpdateThreads)
     IoT* out = static_cast<IoT*>(p.out) + b * p.out_stride + d;
     if constexpr (kN == 8) {
         float h[8], f[8], v[8], bias[8];
-        load_steps(state, 0, 0, 8, 0.0f, h);
-        load_steps(gate, 0, 0, 8, 0.0f, f);
-        load_steps(x, 0, 0, 8, 0.0f, v);
+        load_eight(state, h);
+        load_eight(gate, f);
+        load_eight(x, v);
 #pragma unroll
         for (int k = 0; k < 8; ++k) bias[k] = 0.0f;
-        if (p.bias != nullptr) load_steps(p.bias + d, 0, 0, 8, 0.0f, bias);
+        if (p.bias != nullptr) load_eight(p.bias + d, bias);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             float a, u;

@@ -235,13 +235,6 @@ __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// 1/x on the MUFU pipe (rcp.approx, flush-to-zero); 0 for x = +inf.
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // a ~ hi + lo and b likewise: hi = bf16(v), lo = bf16(v - hi), each pair
 // packed into one word with a in the low half.  v - hi is exact in fp32
 // (hi holds v's leading 8 significant bits), so only lo's own rounding is

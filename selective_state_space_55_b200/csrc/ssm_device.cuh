@@ -36,6 +36,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// 1 / x on the MUFU pipe (rcp.approx, flush-to-zero); 1 / inf = 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // 2^x with unbiased rounding near x = 0.  For |x| < 1/16 the Taylor series
 // 1 + x ln2 + (x ln2)^2/2! + (x ln2)^3/3! + (x ln2)^4/4! (truncation below
 // 1.3e-9) is evaluated with FMAs whose final rounding is to nearest; elsewhere

@@ -415,3 +415,11 @@ def test_many_chains_withheld_handoff_is_reported():
     assert ops.device_status() == 0
     want = ref.gated(**v, layout="bld")
     assert_close("out", ops.gated_scan_fwd(**v, layout="bld"), *want["out"])
+
+
+@pytest.mark.parametrize("L", [5, 100, 700, 2100])
+@pytest.mark.parametrize("batch,dim", [(1, 1), (3, 5), (5, 13)])
+def test_rows_layout_odd_chain_counts(batch, dim, L):
+    """A pair of chains with a missing second one, and pairs across two batch rows."""
+    v, back = make(batch, dim, L, "bdl", BF, False, seed=L + dim, ragged=batch > 1)
+    check(v, back, "bdl", False)
