@@ -40,34 +40,49 @@ cudaError_t launch_column_sum(const float* partial, int64_t rows, int64_t cols, 
 // ------------------------------------------------------------------ layer norm
 
 struct NormPlan {
-    bool wide;          // rows beyond a CTA's registers
-    int chunks;         // of 8 elements per thread (register kernels)
-    int threads;        // per row
-    int teams;          // rows side by side in a CTA
+    bool wide;          // rows beyond a team's registers
+    int chunks;         // of 8 elements per lane
+    int warps;          // of a team (one row)
+    int teams;          // side by side in a CTA
     int64_t ctas;
     int64_t slices;     // wide backward: row slices of the column sums
 };
 
-// Rows up to 512 elements: a warp each, 8 to a CTA, 8 or 16 elements per lane.
-// Up to 8192: a CTA of dim / 8 threads.  Beyond: 1024 threads that re-read.
+// Rows with a team each.  Few rows (fewer than two per SM) are spread over many
+// warps, one or two chunks of 8 elements per lane, for the shortest way through;
+// many rows take as many chunks per lane as waste the fewest lanes, the larger
+// number first (2560 columns: 5 chunks on 2 warps forward, 2 on 5 backward).
 NormPlan plan_norm(int64_t rows, int64_t dim, int sms, bool backward) {
     NormPlan n{};
-    n.teams = 1;
-    if (dim <= kNormWarpDim) {
-        n.chunks = dim <= 32 * kNormElems ? 1 : 2;
-        n.threads = 32;
-        n.teams = rows >= (int64_t)sms * kNormRowsPerCta ? kNormRowsPerCta : 1;
-    } else if (dim <= kNormCtaDim) {
-        n.chunks = 1;
-        n.threads = (int)((dim + kNormElems * 32 - 1) / (kNormElems * 32) * 32);
-    } else {
-        n.wide = true;
-        n.threads = kNormWideThreads;
+    const int64_t units = (dim + 255) / 256;               // chunks of a whole warp
+    const int most = backward || rows < 2 * (int64_t)sms ? kNormFewChunks : kNormFwdChunks;
+    int64_t best = 0;
+    for (int v = most; v >= 1; --v) {
+        if (v == 7) continue;                               // not built
+        const int64_t warps = (units + v - 1) / v;
+        if (warps > (v <= kNormFewChunks ? kNormFewWarps : kNormCtaWarps)) continue;
+        const bool few = rows < 2 * (int64_t)sms;
+        if (n.chunks == 0 || few || warps * v < best) {     // few rows: the smallest number that fits
+            n.chunks = v;
+            best = warps * v;
+        }
     }
-    // As many CTAs as 2048 threads per SM (the backward holds twice the registers:
-    // 1024), each walking rows with its weights in registers.
-    const int per_sm = std::max(1, (backward ? 1024 : 2048) / (n.threads * n.teams));
-    n.ctas = std::max<int64_t>(1, std::min<int64_t>((rows + n.teams - 1) / n.teams, (int64_t)sms * std::min(per_sm, 16)));
+    if (n.chunks == 0 && !backward && units <= kNormFwdChunks * kNormCtaWarps) {
+        n.chunks = kNormFwdChunks;                          // few wide rows
+    }
+    if (n.chunks == 0) {
+        n.wide = true;
+        n.warps = kNormWideThreads / 32;
+        n.teams = 1;
+    } else {
+        n.warps = (int)((units + n.chunks - 1) / n.chunks);
+        n.teams = std::max(1, kNormCtaWarps / n.warps);
+        if (rows < (int64_t)sms * n.teams) n.teams = 1;
+    }
+    // As many CTAs as stay resident (64 registers a thread with one chunk and in
+    // the wide kernels, 128 otherwise), each walking rows with its weights at hand.
+    const int per_sm = std::max(1, (n.wide || n.chunks == 1 ? 1024 : 512) / (n.warps * 32 * n.teams));
+    n.ctas = std::max<int64_t>(1, std::min<int64_t>((rows + n.teams - 1) / n.teams, (int64_t)sms * per_sm));
     const int64_t col_blocks = (dim + kNormColThreads - 1) / kNormColThreads;
     n.slices = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(rows, 1024), (int64_t)sms * 8 / col_blocks));
     return n;
@@ -93,32 +108,62 @@ bool norm_vec(const void* p, int64_t stride, int es) {
     return p == nullptr || (aligned(p, 16) && (stride * es) % 16 == 0);
 }
 
-template <typename IoT, bool kVec>
-cudaError_t launch_norm_fwd(const NormParams& prm, const NormPlan& n, cudaStream_t stream) {
-    const dim3 block(n.threads, n.teams);
-    const unsigned grid = (unsigned)n.ctas;
-    if (n.wide) layer_norm_fwd_wide_kernel<IoT, kVec><<<grid, block, 0, stream>>>(prm);
-    else if (n.chunks == 1) layer_norm_fwd_kernel<IoT, 1, kVec><<<grid, block, 0, stream>>>(prm);
-    else layer_norm_fwd_kernel<IoT, 2, kVec><<<grid, block, 0, stream>>>(prm);
+template <typename IoT, typename ResT, int kV, bool kVec, bool kBackward>
+cudaError_t launch_norm_chunks(const NormParams& prm, const NormPlan& n, int dev, cudaStream_t stream) {
+    static bool attr_done[kMaxDevices] = {false};
+    auto kernel = layer_norm_fwd_kernel<IoT, ResT, kV, kVec>;
+    if constexpr (kBackward) kernel = layer_norm_bwd_kernel<IoT, ResT, kV, kVec>;
+    // weights (and bias) beyond a lane's registers, and the backward's sums of several teams
+    const size_t width = (size_t)kV * 8 * 32 * n.warps * sizeof(float);
+    const size_t smem = kV > 1 || (kBackward && n.teams > 1) ? 2 * width : 0;
+    constexpr int most = 2 * kV * 8 * 32 * (kV <= kNormFewChunks ? kNormFewWarps : kNormCtaWarps) * (int)sizeof(float);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = ensure_smem_attr(kernel, most, attr_done, dev);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<(unsigned)n.ctas, dim3(n.warps * 32, n.teams), smem, stream>>>(prm);
     return cudaGetLastError();
 }
 
+template <typename IoT, typename ResT, bool kVec>
+cudaError_t dispatch_norm_fwd(const NormParams& prm, const NormPlan& n, int dev, cudaStream_t stream) {
+    switch (n.chunks) {
+        case 1: return launch_norm_chunks<IoT, ResT, 1, kVec, false>(prm, n, dev, stream);
+        case 2: return launch_norm_chunks<IoT, ResT, 2, kVec, false>(prm, n, dev, stream);
+        case 3: return launch_norm_chunks<IoT, ResT, 3, kVec, false>(prm, n, dev, stream);
+        case 4: return launch_norm_chunks<IoT, ResT, 4, kVec, false>(prm, n, dev, stream);
+        case 5: return launch_norm_chunks<IoT, ResT, 5, kVec, false>(prm, n, dev, stream);
+        case 6: return launch_norm_chunks<IoT, ResT, 6, kVec, false>(prm, n, dev, stream);
+        default: return launch_norm_chunks<IoT, ResT, 8, kVec, false>(prm, n, dev, stream);
+    }
+}
+
 template <typename IoT, bool kVec>
-cudaError_t launch_norm_bwd(const NormParams& prm, const NormPlan& n, cudaStream_t stream) {
-    const dim3 block(n.threads, n.teams);
-    const unsigned grid = (unsigned)n.ctas;
+cudaError_t launch_norm_fwd(const NormParams& prm, const NormPlan& n, int dev, cudaStream_t stream) {
+    if (n.wide) {
+        layer_norm_fwd_wide_kernel<IoT, kVec><<<(unsigned)n.ctas, kNormWideThreads, 0, stream>>>(prm);
+        return cudaGetLastError();
+    }
+    if (sizeof(IoT) == 2 && prm.res_f32 && (prm.residual != nullptr || prm.residual_out != nullptr))
+        return dispatch_norm_fwd<IoT, float, kVec>(prm, n, dev, stream);
+    return dispatch_norm_fwd<IoT, IoT, kVec>(prm, n, dev, stream);
+}
+
+template <typename IoT, bool kVec>
+cudaError_t launch_norm_bwd(const NormParams& prm, const NormPlan& n, int dev, cudaStream_t stream) {
     if (n.wide) {                       // sums first: dx may replace dout
         if (prm.partial != nullptr) {
             const dim3 cols((unsigned)((prm.dim + kNormColThreads - 1) / kNormColThreads), (unsigned)n.slices);
             layer_norm_bwd_cols_kernel<IoT><<<cols, kNormColThreads, 0, stream>>>(prm);
         }
-        layer_norm_bwd_wide_kernel<IoT, kVec><<<grid, block, 0, stream>>>(prm);
+        layer_norm_bwd_wide_kernel<IoT, kVec><<<(unsigned)n.ctas, kNormWideThreads, 0, stream>>>(prm);
         return cudaGetLastError();
     }
-    const size_t smem = n.teams > 1 ? (size_t)n.teams * 2 * prm.dim * sizeof(float) : 0;
-    if (n.chunks == 1) layer_norm_bwd_kernel<IoT, 1, kVec><<<grid, block, smem, stream>>>(prm);
-    else layer_norm_bwd_kernel<IoT, 2, kVec><<<grid, block, smem, stream>>>(prm);
-    return cudaGetLastError();
+    if (sizeof(IoT) == 2 && prm.res_f32)
+        return n.chunks == 1 ? launch_norm_chunks<IoT, float, 1, kVec, true>(prm, n, dev, stream)
+                             : launch_norm_chunks<IoT, float, 2, kVec, true>(prm, n, dev, stream);
+    return n.chunks == 1 ? launch_norm_chunks<IoT, IoT, 1, kVec, true>(prm, n, dev, stream)
+                         : launch_norm_chunks<IoT, IoT, 2, kVec, true>(prm, n, dev, stream);
 }
 
 // ------------------------------------------------------------------ gated recurrence
@@ -566,7 +611,8 @@ MAMBA_API mamba_status_t mamba_layer_norm_fwd(const void* x, const void* residua
          (residual_out == x || residual_out == out ||
           (residual_out == residual && prm.residual_out_stride != prm.residual_stride))))
         return MAMBA_ERR_INVALID_ARG;
-    const int sms = current_sm_count(nullptr);
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
     const NormPlan n = plan_norm(dims->rows, dims->dim, sms, false);
     const bool vec = dims->dim % kNormElems == 0 && norm_vec(x, prm.x_stride, es) &&
@@ -574,10 +620,10 @@ MAMBA_API mamba_status_t mamba_layer_norm_fwd(const void* x, const void* residua
                      norm_vec(residual_out, prm.residual_out_stride, rs) && norm_vec(weight, 0, 4) &&
                      norm_vec(bias, 0, 4);
     if (dims->io_dtype == MAMBA_BF16)
-        return status_of(vec ? launch_norm_fwd<__nv_bfloat16, true>(prm, n, stream)
-                             : launch_norm_fwd<__nv_bfloat16, false>(prm, n, stream));
-    return status_of(vec ? launch_norm_fwd<float, true>(prm, n, stream)
-                         : launch_norm_fwd<float, false>(prm, n, stream));
+        return status_of(vec ? launch_norm_fwd<__nv_bfloat16, true>(prm, n, dev, stream)
+                             : launch_norm_fwd<__nv_bfloat16, false>(prm, n, dev, stream));
+    return status_of(vec ? launch_norm_fwd<float, true>(prm, n, dev, stream)
+                         : launch_norm_fwd<float, false>(prm, n, dev, stream));
 }
 
 MAMBA_API size_t mamba_layer_norm_bwd_workspace_bytes(const mamba_norm_dims_t* dims) {
@@ -631,7 +677,8 @@ MAMBA_API mamba_status_t mamba_layer_norm_bwd(const void* s, const float* weight
     prm.res_f32 = dims->residual_dtype == MAMBA_F32;
     prm.has_dw = dweight != nullptr;
     prm.has_db = dbias != nullptr;
-    const int sms = current_sm_count(nullptr);
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
     const NormPlan n = plan_norm(dims->rows, dims->dim, sms, true);
     // buffers may coincide only element for element
@@ -653,10 +700,10 @@ MAMBA_API mamba_status_t mamba_layer_norm_bwd(const void* s, const float* weight
                      norm_vec(weight, 0, 4);
     cudaError_t e;
     if (dims->io_dtype == MAMBA_BF16)
-        e = vec ? launch_norm_bwd<__nv_bfloat16, true>(prm, n, stream)
-                : launch_norm_bwd<__nv_bfloat16, false>(prm, n, stream);
+        e = vec ? launch_norm_bwd<__nv_bfloat16, true>(prm, n, dev, stream)
+                : launch_norm_bwd<__nv_bfloat16, false>(prm, n, dev, stream);
     else
-        e = vec ? launch_norm_bwd<float, true>(prm, n, stream) : launch_norm_bwd<float, false>(prm, n, stream);
+        e = vec ? launch_norm_bwd<float, true>(prm, n, dev, stream) : launch_norm_bwd<float, false>(prm, n, dev, stream);
     if (e == cudaSuccess && sums > 0)
         e = launch_column_sum(prm.partial, n.wide ? n.slices : n.ctas, (int64_t)sums * dims->dim,
                               prm.has_dw ? dims->dim : 0, dweight, dbias, stream);

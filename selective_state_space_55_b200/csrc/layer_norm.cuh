@@ -11,23 +11,34 @@
 //   ds = rstd (q - c1 - xh c2) + dresidual_out;  dw = sum_rows dout xh;  db = sum_rows dout.
 //
 // All of it is HBM-bound: a few operations per element against 4 to 16 bytes.
-// A row stays in the registers of one team of threads (a warp, or a CTA of
-// dim / 8 threads), so each tensor crosses HBM once; the variance is summed
-// from (s - mean)^2 in a second reduction over the registers, so an offset far
-// above the spread costs no digits.  The backward's column sums stay in the
-// registers of the thread that owns the columns while the CTA walks its rows;
-// each CTA leaves one partial row per sum, and a second launch adds the
-// partial rows in a fixed order (no atomics: results repeat bit for bit).
+// A row stays in the registers of one team of warps, kV chunks of 8 elements per
+// lane, so each tensor crosses HBM once and all of a row's loads are under way
+// together; the fewer warps share a row, the fewer reductions, barriers and
+// addresses per element (2560 columns, 16384 rows bf16: 5 chunks on 2 warps
+// against 1 chunk on 10, see the plan).  The variance is summed from
+// (s - mean)^2 in a second reduction over the registers, so an offset far above
+// the spread costs no digits.  The backward's column sums stay in the registers
+// of the lane that owns the columns while the CTA walks its rows; each CTA
+// leaves one partial row per sum, and a second launch adds the partial rows in
+// a fixed order (no atomics: results repeat bit for bit).
 #pragma once
 
-#include "ssm_device.cuh"
+#include "row_vectors.cuh"
 
 namespace mamba {
 
-constexpr int kNormElems = 8;            // consecutive elements per thread and chunk
-constexpr int kNormWarpDim = 512;        // dims up to here: one warp per row
-constexpr int kNormCtaDim = 8192;        // dims up to here: one CTA per row, in registers
-constexpr int kNormRowsPerCta = 8;       // rows side by side in a CTA, one warp each
+#ifndef NBAHEAD
+#define NBAHEAD 12
+#endif
+#ifndef NFAHEAD
+#define NFAHEAD 2
+#endif
+constexpr int kNormElems = 8;            // consecutive elements per lane and chunk
+constexpr int kNormFwdChunks = 8;        // most chunks per lane, forward and backward
+constexpr int kNormBwdChunks = 2;
+constexpr int kNormFewChunks = 2;        // up to here a team may have kNormFewWarps warps
+constexpr int kNormCtaWarps = 8;         // warps of a CTA: whole teams side by side
+constexpr int kNormFewWarps = 16;        // of a team with few chunks per lane
 constexpr int kNormWideThreads = 1024;   // wider rows: threads of a CTA that re-reads the row
 
 struct NormParams {
@@ -65,15 +76,47 @@ __device__ __forceinline__ int norm_col(int c, int i, int tid, int n) {
     return kVec ? (c * n + tid) * kNormElems + i : (c * kNormElems + i) * n + tid;
 }
 
-template <typename T>
-__device__ __forceinline__ void load8_vec(const T* p, float (&v)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        unpack16(*reinterpret_cast<const uint4*>(p), v);
-    } else {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// The team's size again, in a way that keeps the element path's 8 kV addresses
+// per tensor from being kept in registers from row to row.
+template <bool kVec>
+__device__ __forceinline__ int norm_opaque(int n) {
+    if constexpr (!kVec) asm volatile("" : "+r"(n));
+    return n;
+}
+
+// Chunk c of a row as it lies in memory (columns from dim on: 0).
+template <typename T, bool kVec>
+struct NormRaw {
+    uint4 q[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* row, int dim, int c, int tid, int n) {
+        const int col = norm_col<true>(c, 0, tid, n);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            q[i] = col < dim ? reinterpret_cast<const uint4*>(row + col)[i] : make_uint4(0, 0, 0, 0);
     }
+    __device__ __forceinline__ void get(float (&v)[8]) const { unpack_steps<T>(q, v); }
+};
+
+template <typename T>
+struct NormRaw<T, false> {
+    float q[8];
+    __device__ __forceinline__ void load(const T* row, int dim, int c, int tid, int n) {
+        int col = norm_col<false>(c, 0, tid, n);
+        const T* at = row + col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, col += n, at += n) q[i] = col < dim ? DType<T>::load(at) : 0.0f;
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = q[i];
+    }
+};
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void norm_load(const T* row, int dim, int c, int tid, int n, float (&v)[8]) {
+    NormRaw<T, kVec> r;
+    r.load(row, dim, c, tid, n);
+    r.get(v);
 }
 
 template <typename T>
@@ -86,25 +129,6 @@ __device__ __forceinline__ void store8_vec(T* p, const float (&v)[8]) {
     }
 }
 
-// Chunk c of a row (columns beyond dim read as `fill`).
-template <typename T, bool kVec>
-__device__ __forceinline__ void norm_load(const T* row, int dim, int c, int tid, int n, float fill,
-                                          float (&v)[8]) {
-    if constexpr (kVec) {
-        const int col = norm_col<true>(c, 0, tid, n);
-        if (col < dim) load8_vec(row + col, v);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fill;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int col = norm_col<false>(c, i, tid, n);
-            v[i] = col < dim ? DType<T>::load(row + col) : fill;
-        }
-    }
-}
-
 template <typename T, bool kVec>
 __device__ __forceinline__ void norm_store(T* row, int dim, int c, int tid, int n,
                                            const float (&v)[8]) {
@@ -112,11 +136,11 @@ __device__ __forceinline__ void norm_store(T* row, int dim, int c, int tid, int 
         const int col = norm_col<true>(c, 0, tid, n);
         if (col < dim) store8_vec(row + col, v);
     } else {
+        int col = norm_col<false>(c, 0, tid, n);
+        T* at = row + col;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int col = norm_col<false>(c, i, tid, n);
-            if (col < dim) DType<T>::store(row + col, v[i]);
-        }
+        for (int i = 0; i < 8; ++i, col += n, at += n)
+            if (col < dim) DType<T>::store(at, v[i]);
     }
 }
 
@@ -124,8 +148,8 @@ __device__ __forceinline__ void norm_store(T* row, int dim, int c, int tid, int 
 template <typename IoT, bool kVec>
 __device__ __forceinline__ void norm_load_res(const void* base, int64_t offset, int f32, int dim,
                                               int c, int tid, int n, float (&v)[8]) {
-    if (f32) norm_load<float, kVec>(static_cast<const float*>(base) + offset, dim, c, tid, n, 0.0f, v);
-    else norm_load<IoT, kVec>(static_cast<const IoT*>(base) + offset, dim, c, tid, n, 0.0f, v);
+    if (f32) norm_load<float, kVec>(static_cast<const float*>(base) + offset, dim, c, tid, n, v);
+    else norm_load<IoT, kVec>(static_cast<const IoT*>(base) + offset, dim, c, tid, n, v);
 }
 
 template <typename IoT, bool kVec>
@@ -135,9 +159,9 @@ __device__ __forceinline__ void norm_store_res(void* base, int64_t offset, int f
     else norm_store<IoT, kVec>(static_cast<IoT*>(base) + offset, dim, c, tid, n, v);
 }
 
-// Sums of kN values over the team (the warp, or the CTA when blockDim.x > 32);
-// every thread gets them.  `buf` is [2][32 kN] shared floats used in turn, so
-// one barrier per call is enough.
+// Sums of kN values over the team: blockDim.x threads (threadIdx.y numbers the
+// CTA's teams); every thread gets them.  `buf` is [2][32 kN] shared floats used
+// in turn, so one barrier per call is enough.
 template <int kN>
 __device__ __forceinline__ void team_sum(float (&v)[kN], float* buf, int& turn) {
 #pragma unroll
@@ -145,12 +169,12 @@ __device__ __forceinline__ void team_sum(float (&v)[kN], float* buf, int& turn) 
 #pragma unroll
         for (int k = 0; k < kN; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     if (blockDim.x > 32) {
-        float* b = buf + turn * 32 * kN;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        float* b = buf + (turn * 32 + threadIdx.y * warps) * kN;
         if (lane == 0)
 #pragma unroll
-            for (int k = 0; k < kN; ++k) b[warp * kN + k] = v[k];
-        __syncthreads();
+            for (int k = 0; k < kN; ++k) b[(threadIdx.x >> 5) * kN + k] = v[k];
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
 #pragma unroll
         for (int k = 0; k < kN; ++k) v[k] = lane < warps ? b[lane * kN + k] : 0.0f;
 #pragma unroll
@@ -161,48 +185,136 @@ __device__ __forceinline__ void team_sum(float (&v)[kN], float* buf, int& turn) 
     }
 }
 
-// Forward, the row in registers: blockDim.x threads per row, blockDim.y rows
-// side by side (more than one only with warps), kV chunks of 8 per thread.
-template <typename IoT, int kV, bool kVec>
-__global__ void __launch_bounds__(kV == 1 ? 1024 : 32 * kNormRowsPerCta, 1)
-    layer_norm_fwd_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float buf[2 * 32];
-    const int tid = threadIdx.x, n = blockDim.x;
-    int turn = 0;
-    float w[kV][8], b[kV][8];
-#pragma unroll
-    for (int c = 0; c < kV; ++c) {
-        if (p.weight != nullptr) norm_load<float, kVec>(p.weight, p.dim, c, tid, n, 0.0f, w[c]);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[c][i] = 1.0f;
-        if (p.bias != nullptr) norm_load<float, kVec>(p.bias, p.dim, c, tid, n, 0.0f, b[c]);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) b[c][i] = 0.0f;
-    }
-    const float inv_dim = 1.0f / (float)p.dim;
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < p.rows; row += step) {
-        float s[kV][8];
-        const IoT* x = static_cast<const IoT*>(p.x) + row * p.x_stride;
-#pragma unroll
-        for (int c = 0; c < kV; ++c) norm_load<IoT, kVec>(x, p.dim, c, tid, n, 0.0f, s[c]);
-        if (p.residual != nullptr) {
+// A lane's weights: in registers for a single chunk, else in shared memory,
+// padded to whole chunks.
+template <int kV, bool kVec>
+struct NormWeights {
+    static constexpr bool kRegs = kV == 1;
+    float reg[kRegs ? kV : 1][8];
+    const float* shared;
+
+    // `fill` where there are no weights; every thread of the CTA calls it.
+    __device__ __forceinline__ void init(const float* w, float fill, float* room, int dim, int tid, int n) {
+        shared = room;
+        if constexpr (kRegs) {
 #pragma unroll
             for (int c = 0; c < kV; ++c) {
-                float r[8];
-                norm_load_res<IoT, kVec>(p.residual, row * p.residual_stride, p.res_f32, p.dim, c,
-                                         tid, n, r);
+                if (w != nullptr) norm_load<float, kVec>(w, dim, c, tid, n, reg[c]);
+                else
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[c][i] += r[i];
+                    for (int i = 0; i < 8; ++i) reg[c][i] = fill;
             }
+        } else {
+            const int threads = blockDim.x * blockDim.y, me = threadIdx.y * blockDim.x + threadIdx.x;
+            for (int j = me; j < kV * 8 * n; j += threads) room[j] = j < dim ? (w != nullptr ? w[j] : fill) : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void get(int c, int tid, int n, float (&v)[8]) const {
+        if constexpr (kRegs) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = reg[c][i];
+        } else if constexpr (kVec) {
+            const float4* q = reinterpret_cast<const float4*>(shared + norm_col<true>(c, 0, tid, n));
+            const float4 a = q[0], b = q[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = shared[norm_col<false>(c, i, tid, n)];
+        }
+    }
+};
+
+// A team's row as it lies in memory.  ResT: the residual stream's type.
+template <typename IoT, typename ResT, int kV, bool kVec>
+struct NormFwdRow {
+    NormRaw<IoT, kVec> x[kV];
+    NormRaw<ResT, kVec> r[kV];
+    __device__ __forceinline__ void load(const NormParams& p, int64_t row, int tid, int n) {
+#pragma unroll
+        for (int c = 0; c < kV; ++c)
+            x[c].load(static_cast<const IoT*>(p.x) + row * p.x_stride, p.dim, c, tid, n);
+        if (p.residual != nullptr)
+#pragma unroll
+            for (int c = 0; c < kV; ++c)
+                r[c].load(static_cast<const ResT*>(p.residual) + row * p.residual_stride, p.dim, c, tid, n);
+    }
+    // Loads and sum at once: fewer registers than load, then get.
+    static __device__ __forceinline__ void fetch(const NormParams& p, int64_t row, int tid, int n, float (&s)[kV][8]) {
+        NormRaw<IoT, kVec> x[kV];
+#pragma unroll
+        for (int c = 0; c < kV; ++c)
+            x[c].load(static_cast<const IoT*>(p.x) + row * p.x_stride, p.dim, c, tid, n);
+        if (p.residual == nullptr) {
+#pragma unroll
+            for (int c = 0; c < kV; ++c) x[c].get(s[c]);
+            return;
+        }
+        const ResT* res = static_cast<const ResT*>(p.residual) + row * p.residual_stride;
+        NormRaw<ResT, kVec> r[kV];
+#pragma unroll
+        for (int c = 0; c < kV; ++c) r[c].load(res, p.dim, c, tid, n);
+#pragma unroll
+        for (int c = 0; c < kV; ++c) {
+            float v[8];
+            r[c].get(s[c]);
+            x[c].get(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[c][i] += v[i];
+        }
+    }
+    __device__ __forceinline__ void get(const NormParams& p, float (&s)[kV][8]) const {
+        if (p.residual == nullptr) {
+#pragma unroll
+            for (int c = 0; c < kV; ++c) x[c].get(s[c]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < kV; ++c) {
+                float v[8];
+                x[c].get(v);
+                r[c].get(s[c]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[c][i] += v[i];
+            }
+        }
+    }
+};
+
+// Forward, the row in registers: a team of blockDim.x threads per row,
+// blockDim.y teams side by side.  With few chunks per lane the next row is
+// requested before this one is reduced.
+template <typename IoT, typename ResT, int kV, bool kVec>
+__global__ void __launch_bounds__(32 * (kV <= kNormFewChunks ? kNormFewWarps : kNormCtaWarps),
+                                  kV <= kNormFewChunks ? 1 : 2)
+    layer_norm_fwd_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float buf[2 * 32];
+    extern __shared__ float4 room[];                 // weights and bias, when not in registers
+    constexpr bool kAhead = kV <= NFAHEAD;
+    const int tid = threadIdx.x;
+    int n = blockDim.x, turn = 0;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    NormFwdRow<IoT, ResT, kV, kVec> ahead;
+    if (kAhead && row < p.rows) ahead.load(p, row, tid, n);
+    NormWeights<kV, kVec> w, b;
+    w.init(p.weight, 1.0f, reinterpret_cast<float*>(room), p.dim, tid, n);
+    b.init(p.bias, 0.0f, reinterpret_cast<float*>(room) + kV * 8 * n, p.dim, tid, n);
+    if constexpr (!NormWeights<kV, kVec>::kRegs) __syncthreads();
+    const float inv_dim = 1.0f / (float)p.dim;
+    for (; row < p.rows; row += step) {
+        n = norm_opaque<kVec>(n);
+        float s[kV][8];
+        if constexpr (kAhead) {
+            ahead.get(p, s);
+            if (row + step < p.rows) ahead.load(p, row + step, tid, n);
+        } else {
+            NormFwdRow<IoT, ResT, kV, kVec>::fetch(p, row, tid, n, s);
         }
         if (p.residual_out != nullptr)
 #pragma unroll
             for (int c = 0; c < kV; ++c)
-                norm_store_res<IoT, kVec>(p.residual_out, row * p.residual_out_stride, p.res_f32,
-                                          p.dim, c, tid, n, s[c]);
+                norm_store<ResT, kVec>(static_cast<ResT*>(p.residual_out) + row * p.residual_out_stride,
+                                       p.dim, c, tid, n, s[c]);
         float mean = 0.0f;
         if (!p.rms) {
             float sum[1] = {0.0f};
@@ -215,13 +327,17 @@ __global__ void __launch_bounds__(kV == 1 ? 1024 : 32 * kNormRowsPerCta, 1)
         }
         float sq[1] = {0.0f};
 #pragma unroll
-        for (int c = 0; c < kV; ++c)
+        for (int c = 0; c < kV; ++c) {
+            // columns from dim on hold 0, not the mean: they stay out
+            if constexpr (kVec) {
+                if (norm_col<true>(c, 0, tid, n) >= p.dim) continue;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float d = s[c][i] - mean;
-                s[c][i] = d;
-                if (norm_col<kVec>(c, i, tid, n) < p.dim) sq[0] = fmaf(d, d, sq[0]);
+                s[c][i] -= mean;
+                if (kVec || norm_col<false>(c, i, tid, n) < p.dim) sq[0] = fmaf(s[c][i], s[c][i], sq[0]);
             }
+        }
         team_sum(sq, buf, turn);
         const float rstd = 1.0f / sqrtf(fmaf(sq[0], inv_dim, p.eps));
         if (tid == 0) {
@@ -231,8 +347,11 @@ __global__ void __launch_bounds__(kV == 1 ? 1024 : 32 * kNormRowsPerCta, 1)
         IoT* out = static_cast<IoT*>(p.out) + row * p.out_stride;
 #pragma unroll
         for (int c = 0; c < kV; ++c) {
+            float wv[8], bv[8];
+            w.get(c, tid, n, wv);
+            b.get(c, tid, n, bv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[c][i] = fmaf(s[c][i] * rstd, w[c][i], b[c][i]);
+            for (int i = 0; i < 8; ++i) s[c][i] = fmaf(s[c][i] * rstd, wv[i], bv[i]);
             norm_store<IoT, kVec>(out, p.dim, c, tid, n, s[c]);
         }
     }
@@ -251,7 +370,7 @@ __global__ void __launch_bounds__(kNormWideThreads)
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const IoT* x = static_cast<const IoT*>(p.x) + row * p.x_stride;
         auto load = [&](int c, float (&s)[8]) {
-            norm_load<IoT, kVec>(x, p.dim, c, tid, n, 0.0f, s);
+            norm_load<IoT, kVec>(x, p.dim, c, tid, n, s);
             if (p.residual != nullptr) {
                 float r[8];
                 norm_load_res<IoT, kVec>(p.residual, row * p.residual_stride, p.res_f32, p.dim, c,
@@ -295,8 +414,8 @@ __global__ void __launch_bounds__(kNormWideThreads)
                 norm_store_res<IoT, kVec>(p.residual_out, row * p.residual_out_stride, p.res_f32,
                                           p.dim, c, tid, n, s);
             float w[8], b[8];
-            if (p.weight != nullptr) norm_load<float, kVec>(p.weight, p.dim, c, tid, n, 0.0f, w);
-            if (p.bias != nullptr) norm_load<float, kVec>(p.bias, p.dim, c, tid, n, 0.0f, b);
+            if (p.weight != nullptr) norm_load<float, kVec>(p.weight, p.dim, c, tid, n, w);
+            if (p.bias != nullptr) norm_load<float, kVec>(p.bias, p.dim, c, tid, n, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 s[i] = fmaf((s[i] - mean) * rstd, p.weight != nullptr ? w[i] : 1.0f,
@@ -306,103 +425,138 @@ __global__ void __launch_bounds__(kNormWideThreads)
     }
 }
 
-// Backward, the row in registers; teams as in the forward.  Every CTA writes
-// its column sums to partial[blockIdx.x] (dw then db, those asked for).
-template <typename IoT, int kV, bool kVec>
-__global__ void __launch_bounds__(kV == 1 ? 1024 : 32 * kNormRowsPerCta, 1)
-    layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float buf[2 * 64];
-    extern __shared__ float cols[];          // several rows per CTA: [blockDim.y][2][dim]
-    const int tid = threadIdx.x, n = blockDim.x;
-    int turn = 0;
-    float w[kV][8], dw[kV][8], db[kV][8];
-#pragma unroll
-    for (int c = 0; c < kV; ++c) {
-        if (p.weight != nullptr) norm_load<float, kVec>(p.weight, p.dim, c, tid, n, 0.0f, w[c]);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[c][i] = 1.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0.0f;
-    }
-    const float inv_dim = 1.0f / (float)p.dim;
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < p.rows; row += step) {
-        const float mean = p.rms ? 0.0f : p.mean_in[row];
-        const float rstd = p.rstd_in[row];
-        float xh[kV][8], q[kV][8];
+template <typename IoT, typename ResT, int kV, bool kVec>
+struct NormBwdRow {
+    NormRaw<IoT, kVec> d[kV];
+    NormRaw<ResT, kVec> s[kV], r[kV];
+    float mean, rstd;
+    __device__ __forceinline__ void load(const NormParams& p, int64_t row, int tid, int n) {
+        mean = p.rms ? 0.0f : p.mean_in[row];
+        rstd = p.rstd_in[row];
 #pragma unroll
         for (int c = 0; c < kV; ++c) {
-            norm_load_res<IoT, kVec>(p.x, row * p.x_stride, p.res_f32, p.dim, c, tid, n, xh[c]);
-            norm_load<IoT, kVec>(static_cast<const IoT*>(p.dout) + row * p.out_stride, p.dim, c, tid,
-                                 n, 0.0f, q[c]);
+            d[c].load(static_cast<const IoT*>(p.dout) + row * p.out_stride, p.dim, c, tid, n);
+            s[c].load(static_cast<const ResT*>(p.x) + row * p.x_stride, p.dim, c, tid, n);
         }
-        float sum[2] = {0.0f, 0.0f};
+    }
+    __device__ __forceinline__ void load_res(const NormParams& p, int64_t row, int tid, int n) {
+        if (p.dresidual_out == nullptr) return;
 #pragma unroll
         for (int c = 0; c < kV; ++c)
+            r[c].load(static_cast<const ResT*>(p.dresidual_out) + row * p.residual_out_stride, p.dim, c, tid, n);
+    }
+};
+
+// Backward, the row in registers; teams as in the forward, the next row
+// requested while this one is reduced.  Every CTA writes its column sums to
+// partial[blockIdx.x] (dw then db, those asked for), the teams' sums added in
+// order.
+template <typename IoT, typename ResT, int kV, bool kVec>
+__global__ void __launch_bounds__(32 * kNormFewWarps, 1)
+    layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float buf[2 * 64];
+    extern __shared__ float4 room[];         // weights while rows go by, then the teams' column sums
+    // registers for the next row: up to 24 of them
+    constexpr bool kAhead = kV * (sizeof(IoT) + 2 * sizeof(ResT)) <= NBAHEAD;
+    const int tid = threadIdx.x;
+    int n = blockDim.x, turn = 0;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    NormBwdRow<IoT, ResT, kV, kVec> ahead;
+    if (kAhead && row < p.rows) {
+        ahead.load(p, row, tid, n);
+        ahead.load_res(p, row, tid, n);
+    }
+    NormWeights<kV, kVec> w;
+    w.init(p.weight, 1.0f, reinterpret_cast<float*>(room), p.dim, tid, n);
+    if constexpr (!NormWeights<kV, kVec>::kRegs) __syncthreads();
+    float dw[kV][8], db[kV][8];
+#pragma unroll
+    for (int c = 0; c < kV; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0.0f;
+    const float inv_dim = 1.0f / (float)p.dim;
+    for (; row < p.rows; row += step) {
+        n = norm_opaque<kVec>(n);
+        NormBwdRow<IoT, ResT, kV, kVec> here;
+        if (!kAhead) {
+            here.load(p, row, tid, n);
+            here.load_res(p, row, tid, n);
+        }
+        NormBwdRow<IoT, ResT, kV, kVec>& in = kAhead ? ahead : here;
+        const float rstd = in.rstd, mean = in.mean;
+        float xh[kV][8], q[kV][8];
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < kV; ++c) {
+            float wv[8];
+            in.d[c].get(q[c]);               // 0 from dim on: nothing is added there
+            in.s[c].get(xh[c]);
+            w.get(c, tid, n, wv);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float h = (xh[c][i] - mean) * rstd;
                 xh[c][i] = h;
                 dw[c][i] = fmaf(q[c][i], h, dw[c][i]);
                 db[c][i] += q[c][i];
-                q[c][i] *= w[c][i];
-                if (norm_col<kVec>(c, i, tid, n) < p.dim) {
-                    sum[0] += q[c][i];
-                    sum[1] = fmaf(q[c][i], h, sum[1]);
-                }
+                q[c][i] *= wv[i];
+                sum[0] += q[c][i];
+                sum[1] = fmaf(q[c][i], h, sum[1]);
             }
+        }
+        if (kAhead && row + step < p.rows) in.load(p, row + step, tid, n);
         team_sum(sum, buf, turn);
         const float c1 = p.rms ? 0.0f : sum[0] * inv_dim;
         const float c2 = sum[1] * inv_dim;
 #pragma unroll
-        for (int c = 0; c < kV; ++c) {
-            float ds[8];
+        for (int c = 0; c < kV; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ds[i] = rstd * (q[c][i] - fmaf(xh[c][i], c2, c1));
-            if (p.dresidual_out != nullptr) {
-                float r[8];
-                norm_load_res<IoT, kVec>(p.dresidual_out, row * p.residual_out_stride, p.res_f32,
-                                         p.dim, c, tid, n, r);
+            for (int i = 0; i < 8; ++i) q[c][i] = rstd * (q[c][i] - fmaf(xh[c][i], c2, c1));
+        if (p.dresidual_out != nullptr)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ds[i] += r[i];
+            for (int c = 0; c < kV; ++c) {
+                float v[8];
+                in.r[c].get(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[c][i] += v[i];
             }
-            norm_store<IoT, kVec>(static_cast<IoT*>(p.dx) + row * p.dx_stride, p.dim, c, tid, n, ds);
+        if (kAhead && row + step < p.rows) in.load_res(p, row + step, tid, n);
+#pragma unroll
+        for (int c = 0; c < kV; ++c) {
+            norm_store<IoT, kVec>(static_cast<IoT*>(p.dx) + row * p.dx_stride, p.dim, c, tid, n, q[c]);
             if (p.dresidual != nullptr)
-                norm_store_res<IoT, kVec>(p.dresidual, row * p.dresidual_stride, p.res_f32, p.dim, c,
-                                          tid, n, ds);
+                norm_store<ResT, kVec>(static_cast<ResT*>(p.dresidual) + row * p.dresidual_stride, p.dim, c,
+                                       tid, n, q[c]);
         }
     }
     if (p.partial == nullptr) return;
-    float* part = p.partial + (int64_t)blockIdx.x * (p.has_dw + p.has_db) * p.dim;
-    float* part_db = part + (p.has_dw ? p.dim : 0);
-    if (blockDim.y == 1) {
+    // [teams' running sums: dw | db], one team after another
+    const int width = kV * 8 * n;
+    float* sums = reinterpret_cast<float*>(room);
+    for (int y = 0; y < (int)blockDim.y; ++y) {
+        if (y > 0 || !NormWeights<kV, kVec>::kRegs) __syncthreads();
+        if ((int)threadIdx.y != y) continue;
+        const bool last = y == (int)blockDim.y - 1;
+        float* part = p.partial + (int64_t)blockIdx.x * (p.has_dw + p.has_db) * p.dim;
+        float* part_db = part + (p.has_dw ? p.dim : 0);
 #pragma unroll
         for (int c = 0; c < kV; ++c) {
-            if (p.has_dw) norm_store<float, kVec>(part, p.dim, c, tid, n, dw[c]);
-            if (p.has_db) norm_store<float, kVec>(part_db, p.dim, c, tid, n, db[c]);
-        }
-        return;
-    }
-    float* mine = cols + threadIdx.y * 2 * p.dim;
 #pragma unroll
-    for (int c = 0; c < kV; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int col = norm_col<kVec>(c, i, tid, n);
-            if (col < p.dim) {
-                mine[col] = dw[c][i];
-                mine[p.dim + col] = db[c][i];
+            for (int i = 0; i < 8; ++i) {
+                const int col = norm_col<kVec>(c, i, tid, n);
+                if (y > 0) {
+                    dw[c][i] = sums[col] + dw[c][i];
+                    db[c][i] = sums[width + col] + db[c][i];
+                }
+                if (!last) {
+                    sums[col] = dw[c][i];
+                    sums[width + col] = db[c][i];
+                }
             }
-        }
-    __syncthreads();
-    for (int j = threadIdx.y * 32 + tid; j < 2 * p.dim; j += 32 * blockDim.y) {
-        float sum = 0.0f;
-        for (int y = 0; y < (int)blockDim.y; ++y) sum += cols[y * 2 * p.dim + j];
-        if (j < p.dim) {
-            if (p.has_dw) part[j] = sum;
-        } else if (p.has_db) {
-            part_db[j - p.dim] = sum;
+            if (last) {
+                if (p.has_dw) norm_store<float, kVec>(part, p.dim, c, tid, n, dw[c]);
+                if (p.has_db) norm_store<float, kVec>(part_db, p.dim, c, tid, n, db[c]);
+            }
         }
     }
 }
@@ -422,9 +576,9 @@ __global__ void __launch_bounds__(kNormWideThreads)
         auto load = [&](int c, float (&xh)[8], float (&q)[8]) {
             norm_load_res<IoT, kVec>(p.x, row * p.x_stride, p.res_f32, p.dim, c, tid, n, xh);
             norm_load<IoT, kVec>(static_cast<const IoT*>(p.dout) + row * p.out_stride, p.dim, c, tid,
-                                 n, 0.0f, q);
+                                 n, q);
             float w[8];
-            if (p.weight != nullptr) norm_load<float, kVec>(p.weight, p.dim, c, tid, n, 0.0f, w);
+            if (p.weight != nullptr) norm_load<float, kVec>(p.weight, p.dim, c, tid, n, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 xh[i] = (xh[i] - mean) * rstd;
