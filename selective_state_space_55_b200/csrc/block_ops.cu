@@ -10,6 +10,7 @@
 #include "gated_scan.cuh"
 #include "gated_chain.cuh"
 
+
 namespace mamba {
 
 bool block_ops_take_status(int* code) { return take_device_status(code); }
@@ -32,9 +33,18 @@ int resident_ctas(Kernel kernel, int threads, size_t smem, int* cache, int dev) 
 
 cudaError_t launch_column_sum(const float* partial, int64_t rows, int64_t cols, int64_t split,
                               float* first, float* second, cudaStream_t stream) {
-    const unsigned grid = (unsigned)((cols + 31) / 32);
-    column_sum_kernel<<<grid, kColSumThreads, 0, stream>>>(partial, rows, cols, split, first, second);
-    return cudaGetLastError();
+    // A dependent launch: the CTAs may take their places while the kernel before
+    // finishes, and wait for it on the device.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((cols + 31) / 32));
+    cfg.blockDim = dim3(kColSumThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, column_sum_kernel, partial, rows, cols, split, first, second);
 }
 
 // ------------------------------------------------------------------ layer norm
@@ -62,7 +72,8 @@ NormPlan plan_norm(int64_t rows, int64_t dim, int sms, bool backward) {
         const int64_t warps = (units + v - 1) / v;
         if (warps > (v <= kNormFewChunks ? kNormFewWarps : kNormCtaWarps)) continue;
         const bool few = rows < 2 * (int64_t)sms;
-        if (n.chunks == 0 || few || warps * v < best) {     // few rows: the smallest number that fits
+        // few rows: the smallest number that fits; backward: two, whatever lanes that wastes
+        if (n.chunks == 0 || few || (!backward && warps * v < best)) {
             n.chunks = v;
             best = warps * v;
         }
@@ -79,9 +90,9 @@ NormPlan plan_norm(int64_t rows, int64_t dim, int sms, bool backward) {
         n.teams = std::max(1, kNormCtaWarps / n.warps);
         if (rows < (int64_t)sms * n.teams) n.teams = 1;
     }
-    // As many CTAs as stay resident (64 registers a thread with one chunk and in
-    // the wide kernels, 128 otherwise), each walking rows with its weights at hand.
-    const int per_sm = std::max(1, (n.wide || n.chunks == 1 ? 1024 : 512) / (n.warps * 32 * n.teams));
+    // CTAs that walk rows, at most: 1024 threads per SM.  The launch takes as many
+    // of them as are resident at once.
+    const int per_sm = std::max(1, 1024 / (n.warps * 32 * n.teams));
     n.ctas = std::max<int64_t>(1, std::min<int64_t>((rows + n.teams - 1) / n.teams, (int64_t)sms * per_sm));
     const int64_t col_blocks = (dim + kNormColThreads - 1) / kNormColThreads;
     n.slices = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(rows, 1024), (int64_t)sms * 8 / col_blocks));
@@ -108,49 +119,86 @@ bool norm_vec(const void* p, int64_t stride, int es) {
     return p == nullptr || (aligned(p, 16) && (stride * es) % 16 == 0);
 }
 
-template <typename IoT, typename ResT, int kV, bool kVec, bool kBackward>
-cudaError_t launch_norm_chunks(const NormParams& prm, const NormPlan& n, int dev, cudaStream_t stream) {
-    static bool attr_done[kMaxDevices] = {false};
-    auto kernel = layer_norm_fwd_kernel<IoT, ResT, kV, kVec>;
-    if constexpr (kBackward) kernel = layer_norm_bwd_kernel<IoT, ResT, kV, kVec>;
-    // weights (and bias) beyond a lane's registers, and the backward's sums of several teams
-    const size_t width = (size_t)kV * 8 * 32 * n.warps * sizeof(float);
-    const size_t smem = kV > 1 || (kBackward && n.teams > 1) ? 2 * width : 0;
-    constexpr int most = 2 * kV * 8 * 32 * (kV <= kNormFewChunks ? kNormFewWarps : kNormCtaWarps) * (int)sizeof(float);
-    if (smem > 48 * 1024) {
+// Launches one instance.  Shared memory: first `fixed` bytes (the weights beyond
+// a lane's registers, where the backward's sums of several teams come later),
+// then every team's ring of rows of `stage` bytes.
+template <typename Kernel>
+cudaError_t launch_norm_kernel(Kernel kernel, const NormParams& prm, NormPlan& n, size_t fixed, size_t stage,
+                               int* resident, bool* attr_done, int dev, int sms, cudaStream_t stream) {
+    // as many stages, two to four, as leave room for the CTAs that the registers
+    // allow (512 threads of 128)
+    constexpr int most = 226 * 1024;             // beside the kernels' static part
+    const size_t share = most / std::max(1, 512 / (n.warps * n.teams * 32));
+    int stages = stage == 0 ? 0 : kNormStages;
+    while (stages > 2 && fixed + stages * stage * n.teams + 3 * 1024 > share) --stages;
+    const size_t smem = fixed + stages * stage * n.teams;
+    if (smem > most) return cudaErrorInvalidConfiguration;
+    if (smem > 40 * 1024) {
         const cudaError_t e = ensure_smem_attr(kernel, most, attr_done, dev);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<(unsigned)n.ctas, dim3(n.warps * 32, n.teams), smem, stream>>>(prm);
+    // resident CTAs per SM, by team size and teams (the rows' width varies little within one)
+    int& per_sm = resident[n.warps * (kNormCtaWarps + 1) + n.teams];
+    if (per_sm <= 0) {
+        int found = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&found, kernel, n.warps * n.teams * 32, smem);
+        if (e != cudaSuccess) return e;
+        if (found <= 0) return cudaErrorInvalidConfiguration;
+        per_sm = found;
+    }
+    n.ctas = std::min<int64_t>(n.ctas, (int64_t)per_sm * sms);
+    kernel<<<(unsigned)n.ctas, dim3(n.warps * 32, n.teams), smem, stream>>>(prm, (int)(fixed / 16), (int)stage, stages);
     return cudaGetLastError();
 }
 
+constexpr int kNormPlans = (kNormFewWarps + 1) * (kNormCtaWarps + 1);
+
+template <typename IoT, typename ResT, int kV, bool kVec, bool kBackward>
+cudaError_t launch_norm_chunks(const NormParams& prm, NormPlan& n, int dev, int sms, cudaStream_t stream) {
+    static bool attr_done[kMaxDevices] = {false};
+    static int resident[kNormPlans] = {0};
+    const size_t width = (size_t)kV * 8 * 32 * n.warps * sizeof(float);
+    // a stage: a row of x (dout) and of the residual stream's tensors
+    size_t stage = 0;
+    if (kVec && kV <= kNormFewChunks)
+        stage = (size_t)prm.dim * (sizeof(IoT) + (kBackward ? 1 + (prm.dresidual_out != nullptr)
+                                                            : prm.residual != nullptr) * sizeof(ResT));
+    if constexpr (kBackward)
+        return launch_norm_kernel(layer_norm_bwd_kernel<IoT, ResT, kV, kVec>, prm, n,
+                                  n.teams > 1 ? 2 * width : (kV > 1 ? width : 0),
+                                  stage, resident, attr_done, dev, sms, stream);
+    else
+        return launch_norm_kernel(layer_norm_fwd_kernel<IoT, ResT, kV, kVec>, prm, n, kV > 1 ? 2 * width : 0,
+                                  stage, resident, attr_done, dev, sms, stream);
+}
+
 template <typename IoT, typename ResT, bool kVec>
-cudaError_t dispatch_norm_fwd(const NormParams& prm, const NormPlan& n, int dev, cudaStream_t stream) {
+cudaError_t dispatch_norm_fwd(const NormParams& prm, NormPlan& n, int dev, int sms, cudaStream_t stream) {
     switch (n.chunks) {
-        case 1: return launch_norm_chunks<IoT, ResT, 1, kVec, false>(prm, n, dev, stream);
-        case 2: return launch_norm_chunks<IoT, ResT, 2, kVec, false>(prm, n, dev, stream);
-        case 3: return launch_norm_chunks<IoT, ResT, 3, kVec, false>(prm, n, dev, stream);
-        case 4: return launch_norm_chunks<IoT, ResT, 4, kVec, false>(prm, n, dev, stream);
-        case 5: return launch_norm_chunks<IoT, ResT, 5, kVec, false>(prm, n, dev, stream);
-        case 6: return launch_norm_chunks<IoT, ResT, 6, kVec, false>(prm, n, dev, stream);
-        default: return launch_norm_chunks<IoT, ResT, 8, kVec, false>(prm, n, dev, stream);
+        case 1: return launch_norm_chunks<IoT, ResT, 1, kVec, false>(prm, n, dev, sms, stream);
+        case 2: return launch_norm_chunks<IoT, ResT, 2, kVec, false>(prm, n, dev, sms, stream);
+        case 3: return launch_norm_chunks<IoT, ResT, 3, kVec, false>(prm, n, dev, sms, stream);
+        case 4: return launch_norm_chunks<IoT, ResT, 4, kVec, false>(prm, n, dev, sms, stream);
+        case 5: return launch_norm_chunks<IoT, ResT, 5, kVec, false>(prm, n, dev, sms, stream);
+        case 6: return launch_norm_chunks<IoT, ResT, 6, kVec, false>(prm, n, dev, sms, stream);
+        default: return launch_norm_chunks<IoT, ResT, 8, kVec, false>(prm, n, dev, sms, stream);
     }
 }
 
 template <typename IoT, bool kVec>
-cudaError_t launch_norm_fwd(const NormParams& prm, const NormPlan& n, int dev, cudaStream_t stream) {
+cudaError_t launch_norm_fwd(const NormParams& prm, NormPlan& n, int dev, int sms, cudaStream_t stream) {
     if (n.wide) {
         layer_norm_fwd_wide_kernel<IoT, kVec><<<(unsigned)n.ctas, kNormWideThreads, 0, stream>>>(prm);
         return cudaGetLastError();
     }
     if (sizeof(IoT) == 2 && prm.res_f32 && (prm.residual != nullptr || prm.residual_out != nullptr))
-        return dispatch_norm_fwd<IoT, float, kVec>(prm, n, dev, stream);
-    return dispatch_norm_fwd<IoT, IoT, kVec>(prm, n, dev, stream);
+        return dispatch_norm_fwd<IoT, float, kVec>(prm, n, dev, sms, stream);
+    return dispatch_norm_fwd<IoT, IoT, kVec>(prm, n, dev, sms, stream);
 }
 
+// n.ctas becomes the number of partial rows.
 template <typename IoT, bool kVec>
-cudaError_t launch_norm_bwd(const NormParams& prm, const NormPlan& n, int dev, cudaStream_t stream) {
+cudaError_t launch_norm_bwd(const NormParams& prm, NormPlan& n, int dev, int sms, cudaStream_t stream) {
     if (n.wide) {                       // sums first: dx may replace dout
         if (prm.partial != nullptr) {
             const dim3 cols((unsigned)((prm.dim + kNormColThreads - 1) / kNormColThreads), (unsigned)n.slices);
@@ -160,10 +208,10 @@ cudaError_t launch_norm_bwd(const NormParams& prm, const NormPlan& n, int dev, c
         return cudaGetLastError();
     }
     if (sizeof(IoT) == 2 && prm.res_f32)
-        return n.chunks == 1 ? launch_norm_chunks<IoT, float, 1, kVec, true>(prm, n, dev, stream)
-                             : launch_norm_chunks<IoT, float, 2, kVec, true>(prm, n, dev, stream);
-    return n.chunks == 1 ? launch_norm_chunks<IoT, IoT, 1, kVec, true>(prm, n, dev, stream)
-                         : launch_norm_chunks<IoT, IoT, 2, kVec, true>(prm, n, dev, stream);
+        return n.chunks == 1 ? launch_norm_chunks<IoT, float, 1, kVec, true>(prm, n, dev, sms, stream)
+                             : launch_norm_chunks<IoT, float, 2, kVec, true>(prm, n, dev, sms, stream);
+    return n.chunks == 1 ? launch_norm_chunks<IoT, IoT, 1, kVec, true>(prm, n, dev, sms, stream)
+                         : launch_norm_chunks<IoT, IoT, 2, kVec, true>(prm, n, dev, sms, stream);
 }
 
 // ------------------------------------------------------------------ gated recurrence
@@ -614,16 +662,16 @@ MAMBA_API mamba_status_t mamba_layer_norm_fwd(const void* x, const void* residua
     int dev = 0;
     const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
-    const NormPlan n = plan_norm(dims->rows, dims->dim, sms, false);
+    NormPlan n = plan_norm(dims->rows, dims->dim, sms, false);
     const bool vec = dims->dim % kNormElems == 0 && norm_vec(x, prm.x_stride, es) &&
                      norm_vec(out, prm.out_stride, es) && norm_vec(residual, prm.residual_stride, rs) &&
                      norm_vec(residual_out, prm.residual_out_stride, rs) && norm_vec(weight, 0, 4) &&
                      norm_vec(bias, 0, 4);
     if (dims->io_dtype == MAMBA_BF16)
-        return status_of(vec ? launch_norm_fwd<__nv_bfloat16, true>(prm, n, dev, stream)
-                             : launch_norm_fwd<__nv_bfloat16, false>(prm, n, dev, stream));
-    return status_of(vec ? launch_norm_fwd<float, true>(prm, n, dev, stream)
-                         : launch_norm_fwd<float, false>(prm, n, dev, stream));
+        return status_of(vec ? launch_norm_fwd<__nv_bfloat16, true>(prm, n, dev, sms, stream)
+                             : launch_norm_fwd<__nv_bfloat16, false>(prm, n, dev, sms, stream));
+    return status_of(vec ? launch_norm_fwd<float, true>(prm, n, dev, sms, stream)
+                         : launch_norm_fwd<float, false>(prm, n, dev, sms, stream));
 }
 
 MAMBA_API size_t mamba_layer_norm_bwd_workspace_bytes(const mamba_norm_dims_t* dims) {
@@ -680,7 +728,7 @@ MAMBA_API mamba_status_t mamba_layer_norm_bwd(const void* s, const float* weight
     int dev = 0;
     const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
-    const NormPlan n = plan_norm(dims->rows, dims->dim, sms, true);
+    NormPlan n = plan_norm(dims->rows, dims->dim, sms, true);
     // buffers may coincide only element for element
     if (dx == s || (dresidual != nullptr && (dresidual == s || dresidual == dx || dresidual == dout)) ||
         (dx == dout && prm.dx_stride != prm.out_stride) ||
@@ -700,10 +748,10 @@ MAMBA_API mamba_status_t mamba_layer_norm_bwd(const void* s, const float* weight
                      norm_vec(weight, 0, 4);
     cudaError_t e;
     if (dims->io_dtype == MAMBA_BF16)
-        e = vec ? launch_norm_bwd<__nv_bfloat16, true>(prm, n, dev, stream)
-                : launch_norm_bwd<__nv_bfloat16, false>(prm, n, dev, stream);
+        e = vec ? launch_norm_bwd<__nv_bfloat16, true>(prm, n, dev, sms, stream)
+                : launch_norm_bwd<__nv_bfloat16, false>(prm, n, dev, sms, stream);
     else
-        e = vec ? launch_norm_bwd<float, true>(prm, n, dev, stream) : launch_norm_bwd<float, false>(prm, n, dev, stream);
+        e = vec ? launch_norm_bwd<float, true>(prm, n, dev, sms, stream) : launch_norm_bwd<float, false>(prm, n, dev, sms, stream);
     if (e == cudaSuccess && sums > 0)
         e = launch_column_sum(prm.partial, n.wide ? n.slices : n.ctas, (int64_t)sums * dims->dim,
                               prm.has_dw ? dims->dim : 0, dweight, dbias, stream);

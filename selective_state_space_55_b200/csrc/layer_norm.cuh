@@ -27,15 +27,8 @@
 
 namespace mamba {
 
-#ifndef NBAHEAD
-#define NBAHEAD 12
-#endif
-#ifndef NFAHEAD
-#define NFAHEAD 2
-#endif
 constexpr int kNormElems = 8;            // consecutive elements per lane and chunk
 constexpr int kNormFwdChunks = 8;        // most chunks per lane, forward and backward
-constexpr int kNormBwdChunks = 2;
 constexpr int kNormFewChunks = 2;        // up to here a team may have kNormFewWarps warps
 constexpr int kNormCtaWarps = 8;         // warps of a CTA: whole teams side by side
 constexpr int kNormFewWarps = 16;        // of a team with few chunks per lane
@@ -159,6 +152,20 @@ __device__ __forceinline__ void norm_store_res(void* base, int64_t offset, int f
     else norm_store<IoT, kVec>(static_cast<IoT*>(base) + offset, dim, c, tid, n, v);
 }
 
+// A chunk as four pairs, for packed fp32x2 arithmetic, and back.
+__device__ __forceinline__ void to_pairs(const float (&v)[8], float2 (&q)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = make_float2(v[2 * i], v[2 * i + 1]);
+}
+
+__device__ __forceinline__ void from_pairs(const float2 (&q)[4], float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = q[i].x;
+        v[2 * i + 1] = q[i].y;
+    }
+}
+
 // Sums of kN values over the team: blockDim.x threads (threadIdx.y numbers the
 // CTA's teams); every thread gets them.  `buf` is [2][32 kN] shared floats used
 // in turn, so one barrier per call is enough.
@@ -177,10 +184,15 @@ __device__ __forceinline__ void team_sum(float (&v)[kN], float* buf, int& turn) 
         asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
 #pragma unroll
         for (int k = 0; k < kN; ++k) v[k] = lane < warps ? b[lane * kN + k] : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        // the lanes past the warps hold 0: the steps over them can be left out, lane 0's
+        // power-of-two neighbourhood holds them all, and the others read its sum
+        int reach = 1;
+        while (reach < warps) reach <<= 1;
+        for (int o = reach >> 1; o > 0; o >>= 1)
 #pragma unroll
             for (int k = 0; k < kN; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
         turn ^= 1;
     }
 }
@@ -225,77 +237,161 @@ struct NormWeights {
     }
 };
 
-// A team's row as it lies in memory.  ResT: the residual stream's type.
-template <typename IoT, typename ResT, int kV, bool kVec>
-struct NormFwdRow {
-    NormRaw<IoT, kVec> x[kV];
-    NormRaw<ResT, kVec> r[kV];
-    __device__ __forceinline__ void load(const NormParams& p, int64_t row, int tid, int n) {
-#pragma unroll
-        for (int c = 0; c < kV; ++c)
-            x[c].load(static_cast<const IoT*>(p.x) + row * p.x_stride, p.dim, c, tid, n);
-        if (p.residual != nullptr)
-#pragma unroll
-            for (int c = 0; c < kV; ++c)
-                r[c].load(static_cast<const ResT*>(p.residual) + row * p.residual_stride, p.dim, c, tid, n);
+// Coming rows of a team in shared memory, brought by bulk copies that one thread
+// asks for: a stage holds one row of up to kTensors tensors, each as it lies in
+// memory.  `bars` are the team's barriers, one per stage.
+constexpr int kNormStages = 4;               // at most
+
+template <int kTensors>
+struct NormRing {
+    const unsigned char* from[kTensors];     // of the next row to ask for
+    int64_t stride[kTensors];                // between a team's rows, bytes
+    uint32_t bytes[kTensors], offset[kTensors];
+    uint32_t data, stage_bytes, bars, at;    // at: the stage being worked on
+    int64_t coming, rows, step;
+    int stages, stage;
+    uint32_t parity;
+    bool failed;
+
+    // Tensor k (null: there is none) with rows of `dim` elements.
+    template <typename T>
+    __device__ __forceinline__ void tensor(int k, const void* base, int64_t row, int64_t row_stride, int dim) {
+        from[k] = static_cast<const unsigned char*>(base) + row * row_stride * (int64_t)sizeof(T);
+        stride[k] = step * row_stride * (int64_t)sizeof(T);
+        bytes[k] = base != nullptr ? dim * (uint32_t)sizeof(T) : 0u;
+        offset[k] = k == 0 ? 0u : offset[k - 1] + bytes[k - 1];
     }
-    // Loads and sum at once: fewer registers than load, then get.
-    static __device__ __forceinline__ void fetch(const NormParams& p, int64_t row, int tid, int n, float (&s)[kV][8]) {
-        NormRaw<IoT, kVec> x[kV];
-#pragma unroll
-        for (int c = 0; c < kV; ++c)
-            x[c].load(static_cast<const IoT*>(p.x) + row * p.x_stride, p.dim, c, tid, n);
-        if (p.residual == nullptr) {
-#pragma unroll
-            for (int c = 0; c < kV; ++c) x[c].get(s[c]);
-            return;
-        }
-        const ResT* res = static_cast<const ResT*>(p.residual) + row * p.residual_stride;
-        NormRaw<ResT, kVec> r[kV];
-#pragma unroll
-        for (int c = 0; c < kV; ++c) r[c].load(res, p.dim, c, tid, n);
-#pragma unroll
-        for (int c = 0; c < kV; ++c) {
-            float v[8];
-            r[c].get(s[c]);
-            x[c].get(v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[c][i] += v[i];
+    // After the tensors; every thread calls it, a barrier of the CTA has to follow.
+    __device__ __forceinline__ void init(const float4* room, uint32_t bytes_per_stage, uint32_t team_bars, int n_stages,
+                                         int64_t first, int64_t n_rows) {
+        stage_bytes = bytes_per_stage;
+        data = smem_u32(room) + threadIdx.y * n_stages * bytes_per_stage;
+        bars = team_bars;
+        at = data;
+        stages = n_stages;
+        stage = 0;
+        parity = 0;
+        failed = false;
+        coming = first;
+        rows = n_rows;
+        if (threadIdx.x == 0) {
+            for (int k = 0; k < n_stages; ++k) mbar_init(bars + 8 * k, 1);
+            fence_mbar_init();
         }
     }
-    __device__ __forceinline__ void get(const NormParams& p, float (&s)[kV][8]) const {
-        if (p.residual == nullptr) {
+    // The next row into stage `to`; one thread of the team.
+    __device__ __forceinline__ void request(int to) {
+        if (coming < rows) {
+            const uint32_t bar = bars + 8 * to, dst = data + to * stage_bytes;
+            uint32_t total = 0;
 #pragma unroll
-            for (int c = 0; c < kV; ++c) x[c].get(s[c]);
-        } else {
+            for (int k = 0; k < kTensors; ++k) total += bytes[k];
+            mbar_arrive_expect_tx(bar, total);
 #pragma unroll
-            for (int c = 0; c < kV; ++c) {
-                float v[8];
-                x[c].get(v);
-                r[c].get(s[c]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[c][i] += v[i];
-            }
+            for (int k = 0; k < kTensors; ++k)
+                if (bytes[k] != 0u) bulk_load(dst + offset[k], from[k], bytes[k], bar);
         }
+        coming += step;
+#pragma unroll
+        for (int k = 0; k < kTensors; ++k) from[k] += stride[k];
+    }
+    __device__ __forceinline__ void wait() {
+        if (!failed && !mbar_wait_bounded(bars + 8 * stage, parity)) {
+            failed = true;
+            record_device_error(MAMBA_ERR_TIMEOUT);
+        }
+    }
+    // Eight elements of tensor k from column col on; 0 where there are none.
+    template <typename T>
+    __device__ __forceinline__ void get(int k, int col, int dim, float (&v)[8]) const {
+        uint4 q[sizeof(T) / 2];
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            q[i] = make_uint4(0, 0, 0, 0);
+            if (col < dim)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
+                             : "r"(at + offset[k] + col * (uint32_t)sizeof(T) + 16 * i)
+                             : "memory");
+        }
+        unpack_steps<T>(q, v);
+    }
+    // Every thread of the team has read stage `st` (it comes from a barrier, or is
+    // a single warp): it takes the row `stages` further on.
+    __device__ __forceinline__ void refill(int st) {
+        if (blockDim.x == 32) __syncwarp();
+        if (threadIdx.x == 0) request(st);
+    }
+    __device__ __forceinline__ int before() const { return stage == 0 ? stages - 1 : stage - 1; }
+    __device__ __forceinline__ void advance() {
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        if (stage == 0) parity ^= 1;
+        at = data + stage * stage_bytes;
     }
 };
 
+// A thread's place in consecutive rows of one tensor, `step` rows apart.
+template <typename T>
+struct NormWalk {
+    T* at;
+    int64_t stride;
+    __device__ __forceinline__ NormWalk(void* base, int64_t row, int64_t row_stride, int64_t step, int col)
+        : at(static_cast<T*>(base) + row * row_stride + col), stride(step * row_stride) {}
+    __device__ __forceinline__ void next() { at += stride; }
+};
+
+// Loads and sums a row's x and residual at once, all loads first.
+template <typename IoT, typename ResT, int kV, bool kVec>
+__device__ __forceinline__ void norm_fetch(const NormParams& p, int64_t row, int tid, int n, float (&s)[kV][8]) {
+    NormRaw<IoT, kVec> x[kV];
+#pragma unroll
+    for (int c = 0; c < kV; ++c)
+        x[c].load(static_cast<const IoT*>(p.x) + row * p.x_stride, p.dim, c, tid, n);
+    if (p.residual == nullptr) {
+#pragma unroll
+        for (int c = 0; c < kV; ++c) x[c].get(s[c]);
+        return;
+    }
+    const ResT* res = static_cast<const ResT*>(p.residual) + row * p.residual_stride;
+    NormRaw<ResT, kVec> r[kV];
+#pragma unroll
+    for (int c = 0; c < kV; ++c) r[c].load(res, p.dim, c, tid, n);
+#pragma unroll
+    for (int c = 0; c < kV; ++c) {
+        float v[8];
+        r[c].get(s[c]);
+        x[c].get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[c][i] += v[i];
+    }
+}
+
 // Forward, the row in registers: a team of blockDim.x threads per row,
-// blockDim.y teams side by side.  With few chunks per lane the next row is
-// requested before this one is reduced.
+// blockDim.y teams side by side.  With few chunks per lane and vectors, rows
+// come through a ring of `stages`; otherwise a lane's many loads are enough.
 template <typename IoT, typename ResT, int kV, bool kVec>
 __global__ void __launch_bounds__(32 * (kV <= kNormFewChunks ? kNormFewWarps : kNormCtaWarps),
                                   kV <= kNormFewChunks ? 1 : 2)
-    layer_norm_fwd_kernel(const __grid_constant__ NormParams p) {
+    layer_norm_fwd_kernel(const __grid_constant__ NormParams p, int ring_at, int stage_bytes, int stages) {
     __shared__ float buf[2 * 32];
-    extern __shared__ float4 room[];                 // weights and bias, when not in registers
-    constexpr bool kAhead = kV <= NFAHEAD;
+    __shared__ uint64_t bars[kNormCtaWarps][kNormStages];
+    extern __shared__ float4 room[];                 // weights and bias, when not in registers; the ring
+    constexpr bool kRing = kV <= kNormFewChunks && kVec;
     const int tid = threadIdx.x;
     int n = blockDim.x, turn = 0;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    NormFwdRow<IoT, ResT, kV, kVec> ahead;
-    if (kAhead && row < p.rows) ahead.load(p, row, tid, n);
+    const int col = norm_col<kVec>(0, 0, tid, n);
+    NormRing<2> ring;                                // x, residual
+    if constexpr (kRing) {
+        ring.step = step;
+        ring.template tensor<IoT>(0, p.x, row, p.x_stride, p.dim);
+        ring.template tensor<ResT>(1, p.residual, row, p.residual_stride, p.dim);
+        ring.init(room + ring_at, stage_bytes, smem_u32(&bars[threadIdx.y][0]), stages, row, p.rows);
+        __syncthreads();
+        if (tid == 0)
+            for (int k = 0; k < stages; ++k) ring.request(k);
+    }
     NormWeights<kV, kVec> w, b;
     w.init(p.weight, 1.0f, reinterpret_cast<float*>(room), p.dim, tid, n);
     b.init(p.bias, 0.0f, reinterpret_cast<float*>(room) + kV * 8 * n, p.dim, tid, n);
@@ -304,55 +400,84 @@ __global__ void __launch_bounds__(32 * (kV <= kNormFewChunks ? kNormFewWarps : k
     for (; row < p.rows; row += step) {
         n = norm_opaque<kVec>(n);
         float s[kV][8];
-        if constexpr (kAhead) {
-            ahead.get(p, s);
-            if (row + step < p.rows) ahead.load(p, row + step, tid, n);
+        if constexpr (kRing) {
+            ring.wait();
+#pragma unroll
+            for (int c = 0; c < kV; ++c) {
+                ring.template get<IoT>(0, col + c * n * kNormElems, p.dim, s[c]);
+                if (p.residual != nullptr) {
+                    float v[8];
+                    ring.template get<ResT>(1, col + c * n * kNormElems, p.dim, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[c][i] += v[i];
+                }
+            }
         } else {
-            NormFwdRow<IoT, ResT, kV, kVec>::fetch(p, row, tid, n, s);
+            norm_fetch<IoT, ResT, kV, kVec>(p, row, tid, n, s);
         }
         if (p.residual_out != nullptr)
 #pragma unroll
             for (int c = 0; c < kV; ++c)
                 norm_store<ResT, kVec>(static_cast<ResT*>(p.residual_out) + row * p.residual_out_stride,
                                        p.dim, c, tid, n, s[c]);
+        float2 t[kV][4];
+#pragma unroll
+        for (int c = 0; c < kV; ++c) to_pairs(s[c], t[c]);
         float mean = 0.0f;
         if (!p.rms) {
-            float sum[1] = {0.0f};
+            float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int c = 0; c < kV; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum[0] += s[c][i];
+                for (int i = 0; i < 4; ++i) acc = __fadd2_rn(acc, t[c][i]);
+            float sum[1] = {acc.x + acc.y};
             team_sum(sum, buf, turn);
             mean = sum[0] * inv_dim;
         }
-        float sq[1] = {0.0f};
+        const float2 shift = make_float2(-mean, -mean);
+        float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int c = 0; c < kV; ++c) {
-            // columns from dim on hold 0, not the mean: they stay out
-            if constexpr (kVec) {
-                if (norm_col<true>(c, 0, tid, n) >= p.dim) continue;
-            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                s[c][i] -= mean;
-                if (kVec || norm_col<false>(c, i, tid, n) < p.dim) sq[0] = fmaf(s[c][i], s[c][i], sq[0]);
+            for (int i = 0; i < 4; ++i) t[c][i] = __fadd2_rn(t[c][i], shift);
+            // columns from dim on held 0 and now hold -mean: they stay out
+            if constexpr (kVec) {
+                if (norm_col<true>(c, 0, tid, n) < p.dim)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc = __ffma2_rn(t[c][i], t[c][i], acc);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (norm_col<false>(c, 2 * i, tid, n) < p.dim) acc.x = fmaf(t[c][i].x, t[c][i].x, acc.x);
+                    if (norm_col<false>(c, 2 * i + 1, tid, n) < p.dim) acc.y = fmaf(t[c][i].y, t[c][i].y, acc.y);
+                }
             }
         }
+        float sq[1] = {acc.x + acc.y};
         team_sum(sq, buf, turn);
+        if constexpr (kRing) {
+            ring.refill(ring.stage);
+            ring.advance();
+        }
         const float rstd = 1.0f / sqrtf(fmaf(sq[0], inv_dim, p.eps));
         if (tid == 0) {
             if (p.mean != nullptr) p.mean[row] = mean;
             if (p.rstd != nullptr) p.rstd[row] = rstd;
         }
+        const float2 scale = make_float2(rstd, rstd);
         IoT* out = static_cast<IoT*>(p.out) + row * p.out_stride;
 #pragma unroll
         for (int c = 0; c < kV; ++c) {
-            float wv[8], bv[8];
-            w.get(c, tid, n, wv);
-            b.get(c, tid, n, bv);
+            float v[8];
+            float2 wv[4], bv[4];
+            w.get(c, tid, n, v);
+            to_pairs(v, wv);
+            b.get(c, tid, n, v);
+            to_pairs(v, bv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[c][i] = fmaf(s[c][i] * rstd, wv[i], bv[i]);
-            norm_store<IoT, kVec>(out, p.dim, c, tid, n, s[c]);
+            for (int i = 0; i < 4; ++i) t[c][i] = __ffma2_rn(__fmul2_rn(t[c][i], scale), wv[i], bv[i]);
+            from_pairs(t[c], v);
+            norm_store<IoT, kVec>(out, p.dim, c, tid, n, v);
         }
     }
 }
@@ -425,111 +550,140 @@ __global__ void __launch_bounds__(kNormWideThreads)
     }
 }
 
-template <typename IoT, typename ResT, int kV, bool kVec>
-struct NormBwdRow {
-    NormRaw<IoT, kVec> d[kV];
-    NormRaw<ResT, kVec> s[kV], r[kV];
-    float mean, rstd;
-    __device__ __forceinline__ void load(const NormParams& p, int64_t row, int tid, int n) {
-        mean = p.rms ? 0.0f : p.mean_in[row];
-        rstd = p.rstd_in[row];
-#pragma unroll
-        for (int c = 0; c < kV; ++c) {
-            d[c].load(static_cast<const IoT*>(p.dout) + row * p.out_stride, p.dim, c, tid, n);
-            s[c].load(static_cast<const ResT*>(p.x) + row * p.x_stride, p.dim, c, tid, n);
-        }
-    }
-    __device__ __forceinline__ void load_res(const NormParams& p, int64_t row, int tid, int n) {
-        if (p.dresidual_out == nullptr) return;
-#pragma unroll
-        for (int c = 0; c < kV; ++c)
-            r[c].load(static_cast<const ResT*>(p.dresidual_out) + row * p.residual_out_stride, p.dim, c, tid, n);
-    }
-};
-
-// Backward, the row in registers; teams as in the forward, the next row
-// requested while this one is reduced.  Every CTA writes its column sums to
-// partial[blockIdx.x] (dw then db, those asked for), the teams' sums added in
-// order.
+// Backward, the row in registers; teams as in the forward, rows through a ring
+// of `stages` (element path: loaded where they are used).  Every CTA writes its
+// column sums to partial[blockIdx.x] (dw then db, those asked for), the teams'
+// sums added in order.
 template <typename IoT, typename ResT, int kV, bool kVec>
 __global__ void __launch_bounds__(32 * kNormFewWarps, 1)
-    layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+    layer_norm_bwd_kernel(const __grid_constant__ NormParams p, int ring_at, int stage_bytes, int stages) {
     __shared__ float buf[2 * 64];
-    extern __shared__ float4 room[];         // weights while rows go by, then the teams' column sums
-    // registers for the next row: up to 24 of them
-    constexpr bool kAhead = kV * (sizeof(IoT) + 2 * sizeof(ResT)) <= NBAHEAD;
+    __shared__ uint64_t bars[kNormCtaWarps][kNormStages];
+    extern __shared__ float4 room[];         // weights while rows go by, then the teams' column sums; the ring
     const int tid = threadIdx.x;
     int n = blockDim.x, turn = 0;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    NormBwdRow<IoT, ResT, kV, kVec> ahead;
-    if (kAhead && row < p.rows) {
-        ahead.load(p, row, tid, n);
-        ahead.load_res(p, row, tid, n);
+    const int col = norm_col<kVec>(0, 0, tid, n);
+    NormRing<3> ring;                        // dout, s, dresidual_out
+    if constexpr (kVec) {
+        ring.step = step;
+        ring.template tensor<IoT>(0, p.dout, row, p.out_stride, p.dim);
+        ring.template tensor<ResT>(1, p.x, row, p.x_stride, p.dim);
+        ring.template tensor<ResT>(2, p.dresidual_out, row, p.residual_out_stride, p.dim);
+        ring.init(room + ring_at, stage_bytes, smem_u32(&bars[threadIdx.y][0]), stages, row, p.rows);
+        __syncthreads();
+        if (tid == 0)
+            for (int k = 0; k < stages; ++k) ring.request(k);
+    }
+    NormWalk<IoT> dx(p.dx, row, p.dx_stride, step, col);
+    NormWalk<ResT> dr(p.dresidual, row, p.dresidual_stride, step, col);
+    bool started = false;
+    float mean = 0.0f, rstd = 0.0f;
+    if (row < p.rows) {
+        mean = p.rms ? 0.0f : p.mean_in[row];
+        rstd = p.rstd_in[row];
     }
     NormWeights<kV, kVec> w;
     w.init(p.weight, 1.0f, reinterpret_cast<float*>(room), p.dim, tid, n);
     if constexpr (!NormWeights<kV, kVec>::kRegs) __syncthreads();
-    float dw[kV][8], db[kV][8];
+    float2 dw2[kV][4], db2[kV][4];
 #pragma unroll
     for (int c = 0; c < kV; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) dw2[c][i] = db2[c][i] = make_float2(0.0f, 0.0f);
     const float inv_dim = 1.0f / (float)p.dim;
     for (; row < p.rows; row += step) {
         n = norm_opaque<kVec>(n);
-        NormBwdRow<IoT, ResT, kV, kVec> here;
-        if (!kAhead) {
-            here.load(p, row, tid, n);
-            here.load_res(p, row, tid, n);
-        }
-        NormBwdRow<IoT, ResT, kV, kVec>& in = kAhead ? ahead : here;
-        const float rstd = in.rstd, mean = in.mean;
-        float xh[kV][8], q[kV][8];
-        float sum[2] = {0.0f, 0.0f};
+        float2 xh[kV][4], q[kV][4];
+        if constexpr (kVec) ring.wait();
 #pragma unroll
         for (int c = 0; c < kV; ++c) {
-            float wv[8];
-            in.d[c].get(q[c]);               // 0 from dim on: nothing is added there
-            in.s[c].get(xh[c]);
-            w.get(c, tid, n, wv);
+            float d[8], x[8];
+            if constexpr (kVec) {
+                ring.template get<IoT>(0, col + c * n * kNormElems, p.dim, d);
+                ring.template get<ResT>(1, col + c * n * kNormElems, p.dim, x);
+            } else {
+                norm_load<IoT, kVec>(static_cast<const IoT*>(p.dout) + row * p.out_stride, p.dim, c, tid, n, d);
+                norm_load<ResT, kVec>(static_cast<const ResT*>(p.x) + row * p.x_stride, p.dim, c, tid, n, x);
+            }
+            to_pairs(d, q[c]);
+            to_pairs(x, xh[c]);
+        }
+        const float2 scale = make_float2(rstd, rstd), shift = make_float2(-mean, -mean);
+        if (row + step < p.rows) {
+            mean = p.rms ? 0.0f : p.mean_in[row + step];
+            rstd = p.rstd_in[row + step];
+        }
+        float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float h = (xh[c][i] - mean) * rstd;
+        for (int c = 0; c < kV; ++c) {       // dout is 0 from dim on: nothing is added there
+            float v[8];
+            float2 wv[4];
+            w.get(c, tid, n, v);
+            to_pairs(v, wv);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 h = __fmul2_rn(__fadd2_rn(xh[c][i], shift), scale);
                 xh[c][i] = h;
-                dw[c][i] = fmaf(q[c][i], h, dw[c][i]);
-                db[c][i] += q[c][i];
-                q[c][i] *= wv[i];
-                sum[0] += q[c][i];
-                sum[1] = fmaf(q[c][i], h, sum[1]);
+                dw2[c][i] = __ffma2_rn(q[c][i], h, dw2[c][i]);
+                db2[c][i] = __fadd2_rn(db2[c][i], q[c][i]);
+                q[c][i] = __fmul2_rn(q[c][i], wv[i]);
+                s0 = __fadd2_rn(s0, q[c][i]);
+                s1 = __ffma2_rn(q[c][i], h, s1);
             }
         }
-        if (kAhead && row + step < p.rows) in.load(p, row + step, tid, n);
+        float sum[2] = {s0.x + s0.y, s1.x + s1.y};
         team_sum(sum, buf, turn);
-        const float c1 = p.rms ? 0.0f : sum[0] * inv_dim;
-        const float c2 = sum[1] * inv_dim;
-#pragma unroll
-        for (int c = 0; c < kV; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[c][i] = rstd * (q[c][i] - fmaf(xh[c][i], c2, c1));
-        if (p.dresidual_out != nullptr)
-#pragma unroll
-            for (int c = 0; c < kV; ++c) {
-                float v[8];
-                in.r[c].get(v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) q[c][i] += v[i];
-            }
-        if (kAhead && row + step < p.rows) in.load_res(p, row + step, tid, n);
+        // past this barrier the row before is done with
+        if constexpr (kVec) {
+            if (started) ring.refill(ring.before());
+            started = true;
+        }
+        const float c1 = p.rms ? 0.0f : -sum[0] * inv_dim;
+        const float c2 = -sum[1] * inv_dim;
 #pragma unroll
         for (int c = 0; c < kV; ++c) {
-            norm_store<IoT, kVec>(static_cast<IoT*>(p.dx) + row * p.dx_stride, p.dim, c, tid, n, q[c]);
-            if (p.dresidual != nullptr)
-                norm_store<ResT, kVec>(static_cast<ResT*>(p.dresidual) + row * p.dresidual_stride, p.dim, c,
-                                       tid, n, q[c]);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                q[c][i] = __fmul2_rn(scale, __fadd2_rn(q[c][i], __ffma2_rn(xh[c][i], make_float2(c2, c2), make_float2(c1, c1))));
+            if (p.dresidual_out != nullptr) {
+                float2 r[4];
+                if constexpr (kVec)
+                    ring.template get<ResT>(2, col + c * n * kNormElems, p.dim, v);
+                else
+                    norm_load<ResT, kVec>(static_cast<const ResT*>(p.dresidual_out) + row * p.residual_out_stride,
+                                          p.dim, c, tid, n, v);
+                to_pairs(v, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[c][i] = __fadd2_rn(q[c][i], r[i]);
+            }
+            from_pairs(q[c], v);
+            if constexpr (kVec) {
+                if (col + c * n * kNormElems < p.dim) {
+                    store8_vec(dx.at + c * n * kNormElems, v);
+                    if (p.dresidual != nullptr) store8_vec(dr.at + c * n * kNormElems, v);
+                }
+            } else {
+                norm_store<IoT, kVec>(static_cast<IoT*>(p.dx) + row * p.dx_stride, p.dim, c, tid, n, v);
+                if (p.dresidual != nullptr)
+                    norm_store<ResT, kVec>(static_cast<ResT*>(p.dresidual) + row * p.dresidual_stride, p.dim, c, tid, n, v);
+            }
+        }
+        if constexpr (kVec) {
+            ring.advance();
+            dx.next();
+            dr.next();
         }
     }
     if (p.partial == nullptr) return;
+    float dw[kV][8], db[kV][8];
+#pragma unroll
+    for (int c = 0; c < kV; ++c) {
+        from_pairs(dw2[c], dw[c]);
+        from_pairs(db2[c], db[c]);
+    }
     // [teams' running sums: dw | db], one team after another
     const int width = kV * 8 * n;
     float* sums = reinterpret_cast<float*>(room);
@@ -655,6 +809,7 @@ static __global__ void __launch_bounds__(kColSumThreads)
     column_sum_kernel(const float* __restrict__ partial, int64_t rows, int64_t cols, int64_t split,
                       float* first, float* second) {
     __shared__ float acc[32][33];
+    grid_dependency_wait();          // launched to overlap the kernel that writes the partial rows
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t col = (int64_t)blockIdx.x * 32 + lane;
     float sum = 0.0f;

@@ -68,6 +68,13 @@ def test_row_counts(res, dim, rows):
     check(make(rows, dim, BF, res, seed=rows))
 
 
+@pytest.mark.parametrize("dim", [4100, 6144, 8192])
+@pytest.mark.parametrize("dtype,res", [(F32, "same"), (BF, "fp32"), (BF, "same")])
+def test_widest_rows_in_registers(dtype, res, dim):
+    """Many rows at the widths where the shared memory of a CTA is fullest."""
+    check(make(700, dim, dtype, res, seed=dim))
+
+
 @pytest.mark.parametrize("weight,bias", [(True, False), (False, True), (False, False)])
 @pytest.mark.parametrize("dim", [130, 640, 9000])
 def test_without_weight_or_bias(dim, weight, bias):
