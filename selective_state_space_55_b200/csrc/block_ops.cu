@@ -574,7 +574,7 @@ mamba_status_t plan_conv_bwd(const mamba_dims_t* d, int width, int sms, ConvBwdP
     const int es = dtype_bytes(d->io_dtype);
     const int64_t tiles = std::max<int64_t>(1, (d->seqlen + 16 / es - 1 + kWarpSteps - 1) / kWarpSteps);
     const int64_t pairs = (chains + 1) / 2;
-    const int64_t want = pairs > 0 ? ((int64_t)sms * CONVW + pairs - 1) / pairs : 1;
+    const int64_t want = pairs > 0 ? ((int64_t)sms * 48 + pairs - 1) / pairs : 1;
     n->stretches = std::max<int64_t>(1, std::min<int64_t>(tiles, want));
     n->stretch_tiles = (tiles + n->stretches - 1) / n->stretches;
     n->stretches = (tiles + n->stretch_tiles - 1) / n->stretch_tiles;

@@ -25,13 +25,7 @@
 
 namespace mamba {
 
-#ifndef CONVMIN
-#define CONVMIN 2
-#endif
-#ifndef CONVW
-#define CONVW 48
-#endif
-constexpr int kConvBwdWarps = 8;
+constexpr int kConvBwdWarps = 4;
 
 struct ConvBwdParams {
     const void* x;
@@ -132,7 +126,7 @@ struct ConvRing {
 };
 
 template <typename IoT, int kW>
-__global__ void __launch_bounds__(kConvBwdWarps * 32, CONVMIN)
+__global__ void __launch_bounds__(kConvBwdWarps * 32, 4)
     causal_conv1d_bwd_kernel(const __grid_constant__ ConvBwdParams p) {
     constexpr int H = kW > 1 ? kW - 1 : 1;               // neighbours on each side
     using Ring = ConvRing<IoT>;
@@ -174,45 +168,49 @@ __global__ void __launch_bounds__(kConvBwdWarps * 32, CONVMIN)
     const int64_t total = p.chains * p.seqlen * (int64_t)sizeof(IoT);
     const Span xspan{static_cast<const unsigned char*>(p.x), static_cast<const unsigned char*>(p.x) + total};
     const Span dspan{static_cast<const unsigned char*>(p.dout), static_cast<const unsigned char*>(p.dout) + total};
-    // A vector travels through the ring when it is aligned and inside the tensor.
-    auto in_ring = [&](const IoT* q, const Span& span) {
-        return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && span.holds(q, 8 * (int)sizeof(IoT));
+    // A tile travels through the ring when dout's rows lie like x's and the tensors
+    // hold all of it (what belongs to other rows is thrown away).
+    const bool alike = row_phase(r0.dout) == row_phase(r0.x) && row_phase(r1.dout) == row_phase(r1.x);
+    constexpr int kTileBytes = kWarpSteps * (int)sizeof(IoT);
+    auto fits = [&](int tile) {
+        const int o0 = r0.begin + tile * kWarpSteps, o1 = r1.begin + tile * kWarpSteps;
+        return alike && tile >= 0 && xspan.holds(r0.x + o0, kTileBytes) && xspan.holds(r1.x + o1, kTileBytes) &&
+               dspan.holds(r0.dout + o0, kTileBytes) && dspan.holds(r1.dout + o1, kTileBytes);
     };
-    auto request = [&](int tile) {                   // one group per call, empty before the stretch
-        if (tile >= 0) {
-            uint4* slot = ring + (tile % Ring::kStages) * (4 * Ring::kVecs * 32) + lane;
+    int ring_lo = 0, ring_hi = tiles;                    // only the tensors' two ends can fall outside
+    while (ring_hi > 0 && !fits(ring_hi - 1)) --ring_hi;
+    while (ring_lo < ring_hi && !fits(ring_lo)) ++ring_lo;
+    auto in_ring = [&](int tile) { return tile >= ring_lo && tile < ring_hi; };
+    // Shared address of this lane's words in a stage.
+    constexpr int kStageBytes = 4 * Ring::kVecs * 32 * 16;
+    const uint32_t mine = smem_u32(ring) + lane * 16;
+    auto stage_of = [&](int tile) { return (uint32_t)(tile % Ring::kStages) * kStageBytes; };
+    auto request = [&](int tile) {                   // one group per call, empty where nothing is asked for
+        if (in_ring(tile)) {
+            const uint32_t to = mine + stage_of(tile);
             const int o0 = r0.begin + tile * kWarpSteps + lane * kLaneSteps;
             const int o1 = r1.begin + tile * kWarpSteps + lane * kLaneSteps;
             const IoT* src[4] = {r0.x + o0, r1.x + o1, r0.dout + o0, r1.dout + o1};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (in_ring(src[j], j < 2 ? xspan : dspan))
 #pragma unroll
-                    for (int v = 0; v < Ring::kVecs; ++v)
-                        copy_async16(smem_u32(slot + (j * Ring::kVecs + v) * 32), reinterpret_cast<const uint4*>(src[j]) + v);
+                for (int v = 0; v < Ring::kVecs; ++v)
+                    copy_async16(to + (j * Ring::kVecs + v) * 512, reinterpret_cast<const uint4*>(src[j]) + v);
         }
         copy_async_commit();
     };
-    // A lane's eight steps of one tensor; masked to [lo, hi) by the caller.
-    auto take = [&](int tile, int j, const IoT* row, const Span& span, int t, int lo, int hi, float (&v)[8]) {
-        if (in_ring(row + t, span)) {
-            const uint4* slot = ring + (tile % Ring::kStages) * (4 * Ring::kVecs * 32) + lane;
-            uint4 raw[Ring::kVecs];
+    auto take = [&](uint32_t from, int j, float (&v)[8]) {
+        uint4 raw[Ring::kVecs];
 #pragma unroll
-            for (int k = 0; k < Ring::kVecs; ++k) raw[k] = slot[(j * Ring::kVecs + k) * 32];
-            unpack_steps<IoT>(raw, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = (t + i >= lo && t + i < hi) ? DType<IoT>::load(row + t + i) : 0.0f;
-        }
+        for (int k = 0; k < Ring::kVecs; ++k)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(raw[k].x), "=r"(raw[k].y), "=r"(raw[k].z), "=r"(raw[k].w)
+                         : "r"(from + (j * Ring::kVecs + k) * 512)
+                         : "memory");
+        unpack_steps<IoT>(raw, v);
     };
-    // Input x_s of the tile before: its lane 31's vector holds steps base - 8 .. base - 1.
-    auto from_before = [&](int tile, int j, int i) {
-        const uint4* slot = ring + ((tile - 1) % Ring::kStages) * (4 * Ring::kVecs * 32) + 31;
-        const int e = 8 - (kW - 1) + i;
-        const IoT* q = reinterpret_cast<const IoT*>(slot + (j * Ring::kVecs + e * (int)sizeof(IoT) / 16) * 32);
-        return DType<IoT>::load(q + (e * (int)sizeof(IoT) % 16) / (int)sizeof(IoT));
-    };
+    const bool dx_alike = row_phase(r0.dx) == row_phase(r0.x) && row_phase(r1.dx) == row_phase(r1.x);
+
 #pragma unroll
     for (int k = 0; k < Ring::kStages - 1; ++k) request(tiles - 1 - k);
     for (int tile = tiles - 1; tile >= 0; --tile) {
@@ -220,44 +218,64 @@ __global__ void __launch_bounds__(kConvBwdWarps * 32, CONVMIN)
         __syncwarp();
         const int b0 = r0.begin + tile * kWarpSteps, b1 = r1.begin + tile * kWarpSteps;
         const int t0 = b0 + lane * kLaneSteps, t1 = b1 + lane * kLaneSteps;
-        // inside both rows, with neighbours before and no final state to add
-        const bool inner = b0 >= r0.lo && b1 >= r1.lo && b0 >= H && b1 >= H && b0 + kWarpSteps <= r0.hi &&
-                           b1 + kWarpSteps <= r1.hi && (p.dfinal == nullptr || (b0 + kWarpSteps <= L - kW && b1 + kWarpSteps <= L - kW));
+        const bool here = in_ring(tile);
+        // all steps inside both rows, none with a final state to add
+        const bool inner = here && b0 >= 0 && b1 >= 0 && b0 + kWarpSteps <= r0.hi && b1 + kWarpSteps <= r1.hi &&
+                           (p.dfinal == nullptr || (b0 + kWarpSteps <= L - kW && b1 + kWarpSteps <= L - kW));
+        const uint32_t from = mine + stage_of(tile);
         float2 xv[8], dp[8], before[H], after[H];
         {
             float v0[8], v1[8], g0[8], g1[8];
-            take(tile, 0, r0.x, xspan, t0, r0.lo, r0.hi, v0);
-            take(tile, 1, r1.x, xspan, t1, r1.lo, r1.hi, v1);
-            take(tile, 2, r0.dout, dspan, t0, r0.lo, r0.hi, g0);
-            take(tile, 3, r1.dout, dspan, t1, r1.lo, r1.hi, g1);
+            if (here) {
+                take(from, 0, v0);
+                take(from, 1, v1);
+                take(from, 2, g0);
+                take(from, 3, g1);
+            } else {
+                load_steps(r0.x, t0, r0.lo, r0.hi, xspan, v0);
+                load_steps(r1.x, t1, r1.lo, r1.hi, xspan, v1);
+                load_steps(r0.dout, t0, r0.lo, r0.hi, dspan, g0);
+                load_steps(r1.dout, t1, r1.lo, r1.hi, dspan, g1);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 xv[i] = make_float2(v0[i], v1[i]);
                 dp[i] = make_float2(g0[i], g1[i]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < H; ++i) before[i] = after[i] = zero;
         if (!inner) {
             // before the row's start: the initial state; behind its end: nothing
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (t0 + i < r0.lo || t0 + i >= r0.hi) xv[i].x = t0 + i < r0.lo ? r0.input(t0 + i, L) : 0.0f;
-                if (t1 + i < r1.lo || t1 + i >= r1.hi) xv[i].y = t1 + i < r1.lo ? r1.input(t1 + i, L) : 0.0f;
+                if (t0 + i < 0 || t0 + i >= r0.hi) xv[i].x = t0 + i < 0 ? r0.input(t0 + i, L) : 0.0f;
+                if (t1 + i < 0 || t1 + i >= r1.hi) xv[i].y = t1 + i < 0 ? r1.input(t1 + i, L) : 0.0f;
             }
         }
-        if (kW > 1) {
 #pragma unroll
-            for (int i = 0; i < kW - 1; ++i) before[i] = shfl_up2(xv[8 - (kW - 1) + i], 1);
-            if (lane == 0)
+        for (int i = 0; i < H; ++i) before[i] = after[i] = zero;
+        if constexpr (kW > 1) {
+            // the last steps of the tile before, for lane 0: lane 31's words of its stage
+            float2 edge[H];
+            if (inner && in_ring(tile - 1)) {
+                const uint32_t last = smem_u32(ring) + 31 * 16 + stage_of(tile - 1);
+                float e0[8], e1[8];
+                take(last, 0, e0);
+                take(last, 1, e1);
+#pragma unroll
+                for (int i = 0; i < kW - 1; ++i) edge[i] = make_float2(e0[8 - (kW - 1) + i], e1[8 - (kW - 1) + i]);
+            } else {
 #pragma unroll
                 for (int i = 0; i < kW - 1; ++i) {
-                    const int s0 = t0 - (kW - 1) + i, s1 = t1 - (kW - 1) + i;
-                    if (inner && tile > 0)
-                        before[i] = make_float2(from_before(tile, 0, i), from_before(tile, 1, i));
-                    else
-                        before[i] = make_float2(s0 < r0.hi ? r0.input(s0, L) : 0.0f, s1 < r1.hi ? r1.input(s1, L) : 0.0f);
+                    const int s0 = b0 - (kW - 1) + i, s1 = b1 - (kW - 1) + i;
+                    edge[i] = make_float2(lane == 0 && s0 < r0.hi ? r0.input(s0, L) : 0.0f,
+                                          lane == 0 && s1 < r1.hi ? r1.input(s1, L) : 0.0f);
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < kW - 1; ++i) {
+                const float2 up = shfl_up2(xv[8 - (kW - 1) + i], 1);
+                before[i] = make_float2(lane == 0 ? edge[i].x : up.x, lane == 0 ? edge[i].y : up.y);
+            }
         }
         __syncwarp();                                    // the slots read above are free again
         request(tile - (Ring::kStages - 1));
@@ -270,7 +288,10 @@ __global__ void __launch_bounds__(kConvBwdWarps * 32, CONVMIN)
                 pre = __ffma2_rn(w[k], j >= 0 ? xv[j] : before[kW - 1 + j], pre);
             }
             dp[i] = conv_dpre2(pre, dp[i], p.silu);
-            if (!inner) {                                // outside: dout was not read, x may be anything
+        }
+        if (!inner) {                                    // outside: what was read there counts for nothing
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
                 if (t0 + i < r0.lo || t0 + i >= r0.hi) dp[i].x = 0.0f;
                 if (t1 + i < r1.lo || t1 + i >= r1.hi) dp[i].y = 0.0f;
             }
@@ -284,34 +305,44 @@ __global__ void __launch_bounds__(kConvBwdWarps * 32, CONVMIN)
                 dw[k] = __ffma2_rn(dp[i], j >= 0 ? xv[j] : before[kW - 1 + j], dw[k]);
             }
         }
-        // dpre after this lane's steps: the lane above, or the tile done before
-        if (kW > 1) {
+        // dpre after this lane's steps: the lane above; for lane 31, what lane 0 had one tile later
+        if constexpr (kW > 1) {
 #pragma unroll
             for (int i = 0; i < kW - 1; ++i) {
-                const float2 down = shfl_down2(dp[i], 1);
-                after[i] = lane == 31 ? later[i] : down;
-                later[i] = shfl2(dp[i], 0);
+                const float2 next = shfl2(dp[i], (lane + 1) & 31);
+                after[i] = make_float2(lane == 31 ? later[i].x : next.x, lane == 31 ? later[i].y : next.y);
+                later[i] = next;
             }
         }
         float2 o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            o[i] = zero;
+            o[i] = __fmul2_rn(w[kW - 1], dp[i]);
 #pragma unroll
-            for (int k = 0; k < kW; ++k) {
+            for (int k = 0; k < kW - 1; ++k) {
                 const int j = i + kW - 1 - k;
                 o[i] = __ffma2_rn(w[k], j < 8 ? dp[j] : after[j - 8 < H ? j - 8 : 0], o[i]);
             }
         }
-        if (!inner && p.dfinal != nullptr) {
+        if (inner && dx_alike) {
+            float v0[8], v1[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int f0 = t0 + i + kW - L, f1 = t1 + i + kW - L;
-                if (f0 >= 0 && f0 < kW && t0 + i >= 0) o[i].x += DType<IoT>::load(r0.dfinal + f0);
-                if (f1 >= 0 && f1 < kW && t1 + i >= 0) o[i].y += DType<IoT>::load(r1.dfinal + f1);
+                v0[i] = o[i].x;
+                v1[i] = o[i].y;
             }
+            store_eight(r0.dx + t0, v0);
+            store_eight(r1.dx + t1, v1);
+        } else {
+            if (p.dfinal != nullptr)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int f0 = t0 + i + kW - L, f1 = t1 + i + kW - L;
+                    if (f0 >= 0 && f0 < kW && t0 + i >= 0) o[i].x += DType<IoT>::load(r0.dfinal + f0);
+                    if (f1 >= 0 && f1 < kW && t1 + i >= 0) o[i].y += DType<IoT>::load(r1.dfinal + f1);
+                }
+            store_steps2(r0.dx, t0, r0.lo, r0.hi, r1.dx, t1, r1.lo, r1.hi, o);
         }
-        store_steps2(r0.dx, t0, r0.lo, r0.hi, r1.dx, t1, r1.lo, r1.hi, o);
     }
     float s0[kW], s1[kW];
 #pragma unroll

@@ -397,25 +397,27 @@ __global__ void __launch_bounds__(kChainThreads, 2)
 #pragma unroll
         for (int i = 0; i < kChainSteps; ++i)
             gated_gains2<kLog>(ring_get<IoT>(grow + i * kRow, lane), bias2, g[i], a[i]);
-        float2 x[kChainSteps], dd[kChainSteps];
+        float2 x[kChainSteps];
 #pragma unroll
-        for (int i = 0; i < kChainSteps; ++i) {
-            x[i] = ring_get<IoT>(xrow + i * kRow, lane);
-            dd[i] = ring_get<IoT>(drow + i * kRow, lane);
-        }
+        for (int i = 0; i < kChainSteps; ++i) x[i] = ring_get<IoT>(xrow + i * kRow, lane);
         if (left < kChainSteps)
 #pragma unroll
             for (int i = 0; i < kChainSteps; ++i)
                 if (i >= left) {
                     a[i] = one;
-                    x[i] = dd[i] = zero;
+                    x[i] = zero;
                 }
+        // dout, read twice from the ring: registers are short
+        auto dout_at = [&](int i) {
+            const float2 v = ring_get<IoT>(drow + i * kRow, lane);
+            return left < kChainSteps && i >= left ? zero : v;
+        };
         float2 A = one, H = zero, R = zero;
 #pragma unroll
         for (int i = 0; i < kChainSteps; ++i) {
             H = __ffma2_rn(a[i], H, kLog ? x[i] : __fmul2_rn(g[i], x[i]));
             A = __fmul2_rn(A, a[i]);
-            R = __ffma2_rn(A, dd[i], R);
+            R = __ffma2_rn(A, dout_at(i), R);
         }
         float4 (&maps)[kChainWarps][32] = sh.maps[n];
         float2 (&rights)[kChainWarps][32] = sh.rights[n];
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kChainThreads, 2)
         }
 #pragma unroll
         for (int i = kChainSteps - 1; i >= 0; --i) {
-            const float2 l = __fadd2_rn(dd[i], r);
+            const float2 l = __fadd2_rn(dout_at(i), r);
             r = __fmul2_rn(a[i], l);
             float2 df = __fmul2_rn(r, x[i]), dv = l;
             if constexpr (!kLog) {

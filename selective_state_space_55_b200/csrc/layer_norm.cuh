@@ -112,22 +112,12 @@ __device__ __forceinline__ void norm_load(const T* row, int dim, int c, int tid,
     r.get(v);
 }
 
-template <typename T>
-__device__ __forceinline__ void store8_vec(T* p, const float (&v)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(p) = pack16(v);
-    } else {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-}
-
 template <typename T, bool kVec>
 __device__ __forceinline__ void norm_store(T* row, int dim, int c, int tid, int n,
                                            const float (&v)[8]) {
     if constexpr (kVec) {
         const int col = norm_col<true>(c, 0, tid, n);
-        if (col < dim) store8_vec(row + col, v);
+        if (col < dim) store_eight(row + col, v);
     } else {
         int col = norm_col<false>(c, 0, tid, n);
         T* at = row + col;
@@ -662,8 +652,8 @@ __global__ void __launch_bounds__(32 * kNormFewWarps, 1)
             from_pairs(q[c], v);
             if constexpr (kVec) {
                 if (col + c * n * kNormElems < p.dim) {
-                    store8_vec(dx.at + c * n * kNormElems, v);
-                    if (p.dresidual != nullptr) store8_vec(dr.at + c * n * kNormElems, v);
+                    store_eight(dx.at + c * n * kNormElems, v);
+                    if (p.dresidual != nullptr) store_eight(dr.at + c * n * kNormElems, v);
                 }
             } else {
                 norm_store<IoT, kVec>(static_cast<IoT*>(p.dx) + row * p.dx_stride, p.dim, c, tid, n, v);

@@ -104,16 +104,21 @@ __device__ __forceinline__ float2 shfl2(float2 v, int lane, int width = 32) {
 }
 
 template <typename T>
+__device__ __forceinline__ void store_eight(T* p, const float (&v)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) = pack16(v);
+    } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+template <typename T>
 __device__ __forceinline__ void store_steps(T* row, int t0, int lo, int hi,
                                             const float (&v)[8]) {
     T* p = row + t0;
     if (t0 >= lo && t0 + 8 <= hi && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4*>(p) = pack16(v);
-        } else {
-            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+        store_eight(p, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
