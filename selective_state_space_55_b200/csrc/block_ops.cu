@@ -2,6 +2,7 @@
 // gated linear recurrence and the convolution's backward.  Argument checks,
 // planning and kernel dispatch.
 #include <algorithm>
+#include <mutex>
 
 #include "mamba_ssm.h"
 #include "host_util.cuh"
@@ -119,12 +120,14 @@ bool norm_vec(const void* p, int64_t stride, int es) {
     return p == nullptr || (aligned(p, 16) && (stride * es) % 16 == 0);
 }
 
+struct NormResident { size_t smem; int ctas; };
+
 // Launches one instance.  Shared memory: first `fixed` bytes (the weights beyond
 // a lane's registers, where the backward's sums of several teams come later),
 // then every team's ring of rows of `stage` bytes.
 template <typename Kernel>
 cudaError_t launch_norm_kernel(Kernel kernel, const NormParams& prm, NormPlan& n, size_t fixed, size_t stage,
-                               int* resident, bool* attr_done, int dev, int sms, cudaStream_t stream) {
+                               NormResident* resident, bool* attr_done, int dev, int sms, cudaStream_t stream) {
     // as many stages, two to four, as leave room for the CTAs that the registers
     // allow (512 threads of 128)
     constexpr int most = 226 * 1024;             // beside the kernels' static part
@@ -137,14 +140,22 @@ cudaError_t launch_norm_kernel(Kernel kernel, const NormParams& prm, NormPlan& n
         const cudaError_t e = ensure_smem_attr(kernel, most, attr_done, dev);
         if (e != cudaSuccess) return e;
     }
-    // resident CTAs per SM, by team size and teams (the rows' width varies little within one)
-    int& per_sm = resident[n.warps * (kNormCtaWarps + 1) + n.teams];
-    if (per_sm <= 0) {
-        int found = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&found, kernel, n.warps * n.teams * 32, smem);
-        if (e != cudaSuccess) return e;
-        if (found <= 0) return cudaErrorInvalidConfiguration;
-        per_sm = found;
+    // resident CTAs per SM; kept for the last shared memory size of each team size
+    // (the number fixes the order of the backward's sums: it has to be this call's own)
+    static std::mutex lock;
+    int per_sm = 0;
+    {
+        std::lock_guard<std::mutex> guard(lock);
+        NormResident& slot = resident[n.warps * (kNormCtaWarps + 1) + n.teams];
+        if (slot.ctas <= 0 || slot.smem != smem) {
+            int found = 0;
+            const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&found, kernel, n.warps * n.teams * 32, smem);
+            if (e != cudaSuccess) return e;
+            if (found <= 0) return cudaErrorInvalidConfiguration;
+            slot.smem = smem;
+            slot.ctas = found;
+        }
+        per_sm = slot.ctas;
     }
     n.ctas = std::min<int64_t>(n.ctas, (int64_t)per_sm * sms);
     kernel<<<(unsigned)n.ctas, dim3(n.warps * 32, n.teams), smem, stream>>>(prm, (int)(fixed / 16), (int)stage, stages);
@@ -156,7 +167,7 @@ constexpr int kNormPlans = (kNormFewWarps + 1) * (kNormCtaWarps + 1);
 template <typename IoT, typename ResT, int kV, bool kVec, bool kBackward>
 cudaError_t launch_norm_chunks(const NormParams& prm, NormPlan& n, int dev, int sms, cudaStream_t stream) {
     static bool attr_done[kMaxDevices] = {false};
-    static int resident[kNormPlans] = {0};
+    static NormResident resident[kNormPlans] = {};
     const size_t width = (size_t)kV * 8 * 32 * n.warps * sizeof(float);
     // a stage: a row of x (dout) and of the residual stream's tensors
     size_t stage = 0;
@@ -262,15 +273,12 @@ struct GatedLayout {           // offsets in the workspace, bytes
     // chained stretches
     size_t chain_zeroed, chain_zeroed_bytes, chain_handoff, chain_bias;
     int64_t chain_groups, chain_stretches, chain_stretch_tiles;
+    // segments of few chains, forward
+    size_t seg_zeroed, seg_zeroed_bytes, seg_maps, seg_states;
+    int64_t seg_segments;
 };
 
-#ifndef CHAINMIN
-#define CHAINMIN 128
-#endif
-#ifndef CHAINK
-#define CHAINK 4
-#endif
-constexpr int64_t kChainMinGroups = CHAINMIN;
+constexpr int64_t kChainMinGroups = 128;
 constexpr int64_t kChainResident = 2 * 148;      // CTAs that a B200 holds
 
 // One segment per chain needs no look-back: no tickets, flags or maps.
@@ -298,13 +306,24 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
         }
         if (backward && recompute) w->enter = take((size_t)d->batch * w->blocks * d->dim * sizeof(float));
         if (backward) w->bias = take((size_t)d->batch * w->segments * d->dim * sizeof(float));
-        // Chained stretches: some CHAINK items per resident CTA, 8 tiles or more each.
+        // Chained stretches: some 4 items per resident CTA, 8 tiles or more each.
         w->chain_groups = d->batch * ((d->dim + kChainChannels - 1) / kChainChannels);
-        const int64_t want = (CHAINK * kChainResident + w->chain_groups - 1) / w->chain_groups;
+        const int64_t want = (4 * kChainResident + w->chain_groups - 1) / w->chain_groups;
         w->chain_stretches = std::max<int64_t>(1, std::min<int64_t>(want, w->blocks / 8));
         w->chain_stretch_tiles = (w->blocks + w->chain_stretches - 1) / w->chain_stretches;
         w->chain_stretches = (w->blocks + w->chain_stretch_tiles - 1) / w->chain_stretch_tiles;
         const size_t items = (size_t)w->chain_groups * w->chain_stretches;
+        if (!backward && w->chain_groups < kChainMinGroups) {
+            const int64_t steps = d->io_dtype == MAMBA_BF16 ? SegmentSizes<__nv_bfloat16>::kSegment : SegmentSizes<float>::kSegment;
+            w->seg_segments = (L + steps - 1) / steps;
+            if (w->seg_segments > 1) {
+                const size_t n = (size_t)w->chain_groups * w->seg_segments;
+                w->seg_zeroed_bytes = 256 + n * sizeof(unsigned int);
+                w->seg_zeroed = take(w->seg_zeroed_bytes);
+                w->seg_maps = take(n * 32 * sizeof(float4));
+                w->seg_states = take((size_t)w->chain_groups * ((w->seg_segments + kGatedJoin - 1) / kGatedJoin) * 32 * sizeof(float2));
+            }
+        }
         if (w->chain_groups >= kChainMinGroups && items < (size_t)kLimit31 / 2) {
             if (w->chain_stretches > 1) {
                 w->chain_zeroed = take(256 + items * sizeof(unsigned int));
@@ -458,7 +477,7 @@ mamba_status_t run_gated_chain(const GatedParams& g, const GatedLayout& w, const
     prm.stretch_tiles = w.chain_stretch_tiles;
     prm.stretches = w.chain_stretches;
     prm.items = prm.groups * prm.stretches;
-    prm.withhold = g.withhold;
+    prm.withhold = g.links.withhold;
     if (prm.stretches > 1) {
         prm.ticket = reinterpret_cast<unsigned int*>(ws + w.chain_zeroed);
         prm.flags = reinterpret_cast<unsigned int*>(ws + w.chain_zeroed + 256);
@@ -471,6 +490,61 @@ mamba_status_t run_gated_chain(const GatedParams& g, const GatedLayout& w, const
                                    : launch_gated_chain<__nv_bfloat16, false, kBackward>(prm, dev, sms, stream));
     return status_of(log_decay ? launch_gated_chain<float, true, kBackward>(prm, dev, sms, stream)
                                : launch_gated_chain<float, false, kBackward>(prm, dev, sms, stream));
+}
+
+template <typename IoT, bool kLog>
+cudaError_t launch_gated_segments(const SegmentParams& prm, int dev, int sms, cudaStream_t stream) {
+    static int resident[kMaxDevices] = {0};
+    static bool attr_done[kMaxDevices] = {false};
+    auto kernel = gated_segment_fwd_kernel<IoT, kLog>;
+    constexpr int smem = (int)sizeof(SegmentShared<IoT>);
+    const cudaError_t e = ensure_smem_attr(kernel, smem, attr_done, dev);
+    if (e != cudaSuccess) return e;
+    int64_t grid = prm.items;
+    if (prm.ticket != nullptr) {
+        const int per_sm = resident_ctas(kernel, kChainWarps * 32, smem, resident, dev);
+        if (per_sm <= 0) return cudaErrorInvalidConfiguration;
+        grid = std::min<int64_t>(grid, (int64_t)per_sm * sms);
+    }
+    kernel<<<(unsigned)grid, kChainWarps * 32, smem, stream>>>(prm);
+    return cudaGetLastError();
+}
+
+// Few chains, forward.
+mamba_status_t run_gated_segments(const GatedParams& g, const GatedLayout& w, const mamba_gated_dims_t* d, uint8_t* ws,
+                                  int dev, int sms, cudaStream_t stream) {
+    const int es = dtype_bytes(d->io_dtype);
+    const bool bf16 = d->io_dtype == MAMBA_BF16, log_decay = d->log_decay != 0;
+    const uint32_t steps = bf16 ? SegmentSizes<__nv_bfloat16>::kSteps : SegmentSizes<float>::kSteps;
+    SegmentParams prm{};
+    if (!encode_chain_map(&prm.gate, g.gate, g.gate_s, d, es, steps) || !encode_chain_map(&prm.x, g.x, g.x_s, d, es, steps) ||
+        !encode_chain_map(&prm.out, g.out, g.out_s, d, es, steps))
+        return MAMBA_ERR_CUDA;
+    prm.bias = g.bias;
+    prm.h0 = g.h0;
+    prm.seqlens = g.seqlens;
+    prm.last = g.last;
+    prm.enter = g.enter;
+    prm.dim = d->dim;
+    prm.seqlen = d->seqlen;
+    prm.blocks = w.blocks;
+    prm.groups_per_row = (d->dim + kChainChannels - 1) / kChainChannels;
+    prm.groups = w.chain_groups;
+    prm.items = prm.groups * w.seg_segments;
+    prm.links.segments = w.seg_segments;
+    prm.links.withhold = g.links.withhold;
+    if (w.seg_segments > 1) {
+        prm.ticket = reinterpret_cast<unsigned int*>(ws + w.seg_zeroed);
+        prm.links.flags = reinterpret_cast<unsigned int*>(ws + w.seg_zeroed + 256);
+        prm.links.maps = reinterpret_cast<float4*>(ws + w.seg_maps);
+        prm.links.states = reinterpret_cast<float2*>(ws + w.seg_states);
+        if (cudaMemsetAsync(ws + w.seg_zeroed, 0, w.seg_zeroed_bytes, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
+    }
+    if (bf16)
+        return status_of(log_decay ? launch_gated_segments<__nv_bfloat16, true>(prm, dev, sms, stream)
+                                   : launch_gated_segments<__nv_bfloat16, false>(prm, dev, sms, stream));
+    return status_of(log_decay ? launch_gated_segments<float, true>(prm, dev, sms, stream)
+                               : launch_gated_segments<float, false>(prm, dev, sms, stream));
 }
 
 template <typename IoT, bool kLog, bool kBackward>
@@ -534,7 +608,7 @@ mamba_status_t gated_common(const void* gate, const void* x, const float* bias, 
     prm->dim = d->dim;
     prm->seqlen = d->seqlen;
     prm->chains = d->batch * d->dim;
-    prm->withhold = (d->flags & MAMBA_FLAG_TEST_WITHHOLD_HANDOFF) != 0;
+    prm->links.withhold = (d->flags & MAMBA_FLAG_TEST_WITHHOLD_HANDOFF) != 0;
     return MAMBA_OK;
 }
 
@@ -546,9 +620,10 @@ void gated_apply_layout(const GatedLayout& w, uint8_t* ws, GatedParams* prm) {
     prm->groups = w.groups;
     prm->items = w.items;
     prm->ticket = w.zeroed ? reinterpret_cast<unsigned int*>(ws + w.tickets) : nullptr;
-    prm->flags = reinterpret_cast<unsigned int*>(ws + w.flags);
-    prm->maps = reinterpret_cast<float4*>(ws + w.maps);
-    prm->states = reinterpret_cast<float4*>(ws + w.joins);
+    prm->links.segments = w.segments;
+    prm->links.flags = reinterpret_cast<unsigned int*>(ws + w.flags);
+    prm->links.maps = reinterpret_cast<float4*>(ws + w.maps);
+    prm->links.states = reinterpret_cast<float2*>(ws + w.joins);
 }
 
 mamba_status_t check_workspace(const void* ws, size_t have, size_t need) {
@@ -851,6 +926,7 @@ MAMBA_API mamba_status_t mamba_gated_scan_fwd(const void* gate, const void* x, c
         return MAMBA_ERR_ALIGN;
     if (!resolve_strides(dims->out, dims->batch, rows, inner, true, &prm.out_s)) return MAMBA_ERR_INVALID_ARG;
     if (out != nullptr && (out == gate || out == x)) return MAMBA_ERR_INVALID_ARG;
+    if (partly_overlap(initial_state, last_state, (size_t)prm.chains * sizeof(float))) return MAMBA_ERR_INVALID_ARG;
     if (dims->seqlen == 0)
         return status_of(copy_or_zero(last_state, initial_state, (size_t)prm.chains * sizeof(float), stream));
     GatedLayout w;
@@ -872,9 +948,10 @@ MAMBA_API mamba_status_t mamba_gated_scan_fwd(const void* gate, const void* x, c
     const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
     prm.enter = checkpoints;
-    if (w.chain_groups >= kChainMinGroups && chain_tensor_ok(gate, prm.gate_s, es, dims->batch) &&
-        chain_tensor_ok(x, prm.x_s, es, dims->batch) && chain_tensor_ok(out, prm.out_s, es, dims->batch))
-        return run_gated_chain<false>(prm, w, dims, ws, dev, sms, stream);
+    if (chain_tensor_ok(gate, prm.gate_s, es, dims->batch) && chain_tensor_ok(x, prm.x_s, es, dims->batch) &&
+        chain_tensor_ok(out, prm.out_s, es, dims->batch))
+        return w.chain_groups >= kChainMinGroups ? run_gated_chain<false>(prm, w, dims, ws, dev, sms, stream)
+                                                 : run_gated_segments(prm, w, dims, ws, dev, sms, stream);
     if (w.zeroed && cudaMemsetAsync(ws, 0, w.zeroed, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
     const bool vec = dims->dim % 4 == 0 && rows_aligned(gate, prm.gate_s, es, 4 * es) &&
                      rows_aligned(x, prm.x_s, es, 4 * es) && rows_aligned(out, prm.out_s, es, 4 * es) &&
@@ -964,7 +1041,7 @@ MAMBA_API mamba_status_t mamba_gated_scan_bwd(
         fwd.enter = reinterpret_cast<float*>(ws + w.enter);
         if (w.zeroed) {
             fwd.ticket = prm.ticket + 1;
-            fwd.flags = reinterpret_cast<unsigned int*>(ws + w.flags2);
+            fwd.links.flags = reinterpret_cast<unsigned int*>(ws + w.flags2);
         }
         e = dispatch_gated_tiles<false>(fwd, w.warps, bf16, log_decay, vec_in, dev, sms, stream);
         if (e != cudaSuccess) return MAMBA_ERR_CUDA;

@@ -21,15 +21,6 @@
 
 namespace mamba {
 
-#ifndef CFMIN
-#define CFMIN 3
-#endif
-#ifndef CFS
-#define CFS 3
-#endif
-#ifndef CBS
-#define CBS 3
-#endif
 constexpr int kChainSteps = 8;                              // per warp and tile
 constexpr int kChainWarps = 8;                              // besides the producer
 constexpr int kChainTile = kChainSteps * kChainWarps;
@@ -63,8 +54,8 @@ template <typename IoT, bool kBackward>
 struct ChainSizes {
     static constexpr int kTensor = kChainTile * kChainChannels * (int)sizeof(IoT);     // bytes of a tile
     static constexpr int kStage = kBackward ? 3 * kTensor + kChainChannels * 4 : 2 * kTensor;   // + entering states
-    // stages of the ring: two CTAs share an SM's shared memory
-    static constexpr int kStages = sizeof(IoT) == 2 ? (kBackward ? CBS : CFS) : (kBackward ? 2 : 3);
+    // stages of the ring: two or three CTAs share an SM's shared memory
+    static constexpr int kStages = sizeof(IoT) == 2 ? 3 : (kBackward ? 2 : 3);
 };
 
 // What the producer says about the tile in a stage.
@@ -271,7 +262,7 @@ __device__ __forceinline__ void chain_send_rows(const CUtensorMap* map0, const C
 }
 
 template <typename IoT, bool kLog>
-__global__ void __launch_bounds__(kChainThreads, sizeof(IoT) == 2 ? CFMIN : 2)
+__global__ void __launch_bounds__(kChainThreads, sizeof(IoT) == 2 ? 3 : 2)
     gated_chain_fwd_kernel(const __grid_constant__ ChainParams p) {
     extern __shared__ __align__(128) unsigned char raw[];
     auto& sh = *reinterpret_cast<ChainShared<IoT, false>*>(raw);
@@ -478,6 +469,183 @@ __global__ void __launch_bounds__(kChainThreads, 2)
                 chain_store2(p.bias_partial + row * p.dim, d, p.dim, sum);
             }
         }
+    }
+    if (lane == 0) bulk_wait_read<0>();
+}
+
+// --------------------------------------------------------------- few chains
+//
+// With fewer groups of channels than fill the GPU, time has to be split as well.
+// A segment is 8 blocks of kSteps steps x 64 channels, one per warp, brought by
+// TMA and kept in shared memory while the segments of a chain are joined
+// (gated_join): phase one reads a block for its map, phase two again for its
+// outputs, which replace x there and leave by TMA.  HBM sees each input once; the
+// steps' arithmetic is done twice.  Three CTAs per SM cover one another's loads
+// and joins.
+template <typename IoT>
+struct SegmentSizes {
+    static constexpr int kSteps = sizeof(IoT) == 2 ? 32 : 16;                      // per warp
+    static constexpr int kBlock = kSteps * kChainChannels * (int)sizeof(IoT);      // bytes of one tensor's block
+    static constexpr int kSegment = kSteps * kChainWarps;
+};
+
+template <typename IoT>
+struct SegmentShared {
+    alignas(128) unsigned char blocks[kChainWarps][2][SegmentSizes<IoT>::kBlock];  // gate, x (then out)
+    float4 maps[kChainWarps][32];
+    float2 entering[kChainWarps][32];
+    uint64_t full[kChainWarps];
+    int64_t first_slot, next_slot;
+};
+
+struct SegmentParams {
+    CUtensorMap gate, x, out;      // boxes of 64 channels x kSteps steps
+    const float* bias;             // (dim) or null
+    const float* h0;               // (batch, dim) or null
+    const int32_t* seqlens;        // (batch) or null
+    float* last;                   // or null
+    float* enter;                  // [batch][blocks of 64 steps][dim] or null
+    GatedLinks links;
+    unsigned int* ticket;          // null: one segment per chain
+    int64_t dim, seqlen, blocks;
+    int64_t groups_per_row, groups, items;
+};
+
+template <typename IoT, bool kLog>
+__global__ void __launch_bounds__(kChainWarps * 32, 3)
+    gated_segment_fwd_kernel(const __grid_constant__ SegmentParams p) {
+    extern __shared__ __align__(128) unsigned char raw[];
+    auto& sh = *reinterpret_cast<SegmentShared<IoT>*>(raw);
+    using Sizes = SegmentSizes<IoT>;
+    constexpr int kSteps = Sizes::kSteps, kAt = 8;       // steps worked on at a time
+    constexpr int kRow = kChainChannels * (int)sizeof(IoT);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float2 one = make_float2(1.0f, 1.0f), zero = make_float2(0.0f, 0.0f);
+    if (lane == 0) {
+        mbar_init(smem_u32(&sh.full[warp]), 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) sh.first_slot = p.ticket != nullptr ? (int64_t)atomicAdd(p.ticket, 1u) : (int64_t)blockIdx.x;
+    __syncthreads();
+    unsigned char* grow = sh.blocks[warp][0];
+    unsigned char* xrow = sh.blocks[warp][1];
+    const uint32_t bar = smem_u32(&sh.full[warp]);
+    // This warp's block of an item: its first step may lie behind the tensor's end
+    // (then nothing is asked for).
+    auto place = [&](int64_t item, int* b, int* d0, int64_t* t, int64_t* pos, int64_t* group) {
+        *pos = item / p.groups;
+        *group = item - *pos * p.groups;
+        *b = (int)(*group / p.groups_per_row);
+        *d0 = (int)(*group - *b * p.groups_per_row) * kChainChannels;
+        *t = *pos * Sizes::kSegment + warp * kSteps;
+    };
+    auto request = [&](int64_t item) {
+        if (item >= p.items || lane != 0) return;
+        int b, d0;
+        int64_t t, pos, group;
+        place(item, &b, &d0, &t, &pos, &group);
+        if (t >= p.seqlen) return;
+        mbar_arrive_expect_tx(bar, 2 * Sizes::kBlock);
+        tma_load_3d(smem_u32(grow), &p.gate, d0, (int)t, b, bar);
+        tma_load_3d(smem_u32(xrow), &p.x, d0, (int)t, b, bar);
+    };
+    int64_t item = sh.first_slot;
+    request(item);
+    uint32_t parity = 0;
+    while (item < p.items) {
+        int b, d0;
+        int64_t t, pos, group;
+        place(item, &b, &d0, &t, &pos, &group);
+        int64_t coming = p.items;                // asked for now, needed at the barrier
+        if (threadIdx.x == 0 && p.ticket != nullptr) coming = atomicAdd(p.ticket, 1u);
+        const int64_t d = d0 + 2 * lane;
+        const int64_t len = p.seqlens != nullptr ? min(max((int64_t)p.seqlens[b], (int64_t)0), p.seqlen) : p.seqlen;
+        const int left = (int)min(max(len - t, (int64_t)0), (int64_t)kSteps);
+        float2 start[1] = {p.h0 != nullptr ? chain_load2(p.h0 + (int64_t)b * p.dim, d, p.dim) : zero};
+        const float2 bias2 = p.bias != nullptr ? __fmul2_rn(chain_load2(p.bias, d, p.dim), make_float2(kLog2e, kLog2e)) : zero;
+        bool failed = false;
+        if (t < p.seqlen) {
+            failed = !mbar_wait_bounded(bar, parity);
+            parity ^= 1;
+            if (failed) record_device_error(MAMBA_ERR_TIMEOUT);
+        }
+        auto terms = [&](int s, float2 (&a)[kAt], float2 (&u)[kAt]) {
+#pragma unroll
+            for (int i = 0; i < kAt; ++i)
+                gated_terms2<kLog>(ring_get<IoT>(grow + (s + i) * kRow, lane), bias2,
+                                   ring_get<IoT>(xrow + (s + i) * kRow, lane), a[i], u[i]);
+            if (left - s < kAt)
+#pragma unroll
+                for (int i = 0; i < kAt; ++i)
+                    if (s + i >= left) {
+                        a[i] = one;
+                        u[i] = zero;
+                    }
+        };
+        float2 A = one, H = zero;
+        for (int s = 0; s < left; s += kAt) {
+            float2 a[kAt], u[kAt];
+            terms(s, a, u);
+#pragma unroll
+            for (int i = 0; i < kAt; ++i) {
+                H = __ffma2_rn(a[i], H, u[i]);
+                A = __fmul2_rn(A, a[i]);
+            }
+        }
+        sh.maps[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
+        if (threadIdx.x == 0) sh.next_slot = coming;
+        // a CTA whose copy never came leaves as a whole
+        if (__syncthreads_or(failed)) break;
+        const int64_t following = sh.next_slot;
+        if (warp == 0) {
+            if (p.ticket != nullptr) {
+                float2 At[1] = {one}, Ht[1] = {zero};
+#pragma unroll
+                for (int v = 0; v < kChainWarps; ++v) {
+                    const float4 m = sh.maps[v][lane];
+                    Ht[0] = __ffma2_rn(make_float2(m.x, m.y), Ht[0], make_float2(m.z, m.w));
+                    At[0] = __fmul2_rn(At[0], make_float2(m.x, m.y));
+                }
+                gated_join<1>(p.links, group, pos, lane, At, Ht, start);
+            }
+            float2 h = start[0];
+#pragma unroll
+            for (int v = 0; v < kChainWarps; ++v) {
+                const float4 m = sh.maps[v][lane];
+                sh.entering[v][lane] = h;
+                h = __ffma2_rn(make_float2(m.x, m.y), h, make_float2(m.z, m.w));
+            }
+        }
+        __syncthreads();
+        float2 h = sh.entering[warp][lane];
+        if (t < p.seqlen) {
+            if (p.enter != nullptr && t % kChainTile == 0)
+                chain_store2(p.enter + ((int64_t)b * p.blocks + t / kChainTile) * p.dim, d, p.dim, h);
+            for (int s = 0; s < kSteps; s += kAt) {
+                if (s < left) {
+                    float2 a[kAt], u[kAt];
+                    terms(s, a, u);
+#pragma unroll
+                    for (int i = 0; i < kAt; ++i) {
+                        h = __ffma2_rn(a[i], h, u[i]);
+                        ring_put<IoT>(xrow + (s + i) * kRow, lane, s + i < left ? h : zero);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kAt; ++i) ring_put<IoT>(xrow + (s + i) * kRow, lane, zero);
+                }
+            }
+            if (p.last != nullptr && t + kSteps >= p.seqlen) chain_store2(p.last + (int64_t)b * p.dim, d, p.dim, h);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(&p.out, d0, (int)t, b, smem_u32(xrow));
+                bulk_commit();
+                bulk_wait_read<0>();
+            }
+        }
+        request(following);                      // the block's own shared memory is free again
+        item = following;
     }
     if (lane == 0) bulk_wait_read<0>();
 }

@@ -22,24 +22,24 @@
 // long as the step's arithmetic (two special-function operations for the
 // sigmoid, one for the log decay) and the joins stay below the issue rate.
 //
-// Layout (batch, seqlen, dim): a warp takes a block of 64 steps of 128 channels
-// (a lane four neighbours: rows of 256 or 512 bytes per access), up to 8 warps
-// side by side in time make a segment of 512 steps.  Phase one walks the block
-// and keeps only its map; the segment's maps are composed through shared
-// memory; segments of a chain are joined by a look-back in fixed groups of 8,
-// so that every state is composed in the same order whatever the timing.  Phase
-// two walks the block again from its true start: its inputs come from L2 (a
-// segment is 256 KB in bf16), so HBM
-// sees each input once.  The steps' arithmetic is done twice in exchange, in
-// packed fp32x2.  Segments are handed out by a counter, the earliest steps of
-// all chains first, so that every segment's predecessors belong to CTAs that
-// are running or done; the wait is bounded all the same.
+// Layout (batch, seqlen, dim), what TMA cannot move (odd strides or bases) and the
+// backward of few chains: a warp takes a block of 64 steps of 128 channels (a lane
+// four neighbours: rows of 256 or 512 bytes per access), up to 8 warps side by side
+// in time make a segment of 512 steps.  Phase one walks the block and keeps only its
+// map; the segment's maps are composed through shared memory; segments of a chain
+// are joined by a look-back in fixed groups of 24, so that every state is composed
+// in the same order whatever the timing.  Phase two walks the block again from its
+// true start: its inputs come from L2 (a segment is 256 KB in bf16), so HBM sees
+// each input once.  The steps' arithmetic is done twice in exchange, in packed
+// fp32x2.  Segments are handed out by a counter, the earliest steps of all chains
+// first, so that every segment's predecessors belong to CTAs that are running or
+// done; the wait is bounded all the same.  What TMA can move has kernels of its own
+// (gated_chain.cuh).
 //
-// Layout (batch, dim, seqlen): a lane takes 8 consecutive steps of two
-// neighbouring chains, the warp composes its lanes' maps by shuffles, and 1 to 8
-// warps share a tile of a pair through shared memory.  Chains are plentiful here (one per
-// channel instead of one per 64), so a chain stays with its warps and nothing
-// waits.
+// Layout (batch, dim, seqlen): a lane takes 8 consecutive steps of two neighbouring
+// chains, the warp composes its lanes' maps by shuffles, and 1 to 8 warps share a
+// tile of a pair through shared memory.  Chains are plentiful here (one per channel
+// instead of one per 64), so a chain stays with its warps and nothing waits.
 #pragma once
 
 #include "row_vectors.cuh"
@@ -50,10 +50,20 @@ constexpr int kGatedBlock = 64;                             // steps per warp
 constexpr int kGatedWarps = 8;                              // blocks per segment, at most
 constexpr int kGatedChannels = 128;                         // per CTA, four per lane
 constexpr int kGatedThreads = kGatedWarps * 32;
-constexpr int kGatedJoin = 8;                               // segments folded from one known state
+constexpr int kGatedJoin = 24;                              // segments folded from one known state
+static_assert(kGatedJoin < 32, "one lane per map and one for the state");
 static_assert(kGatedBlock == MAMBA_GATED_CHECKPOINT_STEPS, "checkpoints are the states entering blocks");
 
 struct GatedStrides { int64_t batch, row; };
+
+// What the segments of the chains hand on: `segments` per group of channels.
+struct GatedLinks {
+    float4* maps;                 // [groups][segments][pairs][32]: a lane's maps
+    float2* states;               // [groups][segments / kGatedJoin][pairs][32]: states entering a join group
+    unsigned int* flags;          // [groups][segments]: 0, 1 = map published, 2 = state published
+    int64_t segments;
+    int withhold;                 // test only: publish nothing
+};
 
 struct GatedParams {
     const void* gate;
@@ -71,9 +81,7 @@ struct GatedParams {
     float* bias_partial;          // bwd: [batch * segments][dim] (seqlen fastest: [batch][dim]) or null
     // (batch, seqlen, dim)
     float* enter;                 // [batch][blocks][dim], states entering blocks; fwd: written or null
-    float4* maps;                 // [groups][segments][A | H][32]: of a lane's four channels
-    float4* states;               // [groups][segments / kGatedJoin][32]: states entering a join group
-    unsigned int* flags;          // [groups][segments]: 0, 1 = map published, 2 = state published
+    GatedLinks links;
     unsigned int* ticket;         // null: one segment per chain, one CTA per segment
     // (batch, dim, seqlen), bwd: states entering tiles, [chains][tiles]
     float* chain_states;
@@ -85,7 +93,6 @@ struct GatedParams {
     int64_t groups;
     int64_t items;                // groups * segments
     int64_t tiles;                // (batch, dim, seqlen): per chain
-    int withhold;                 // test only: publish nothing
 };
 
 constexpr unsigned int kGatedPollLimit = 1u << 19;
@@ -312,35 +319,37 @@ __device__ __forceinline__ GatedBlockAt gated_block(const GatedParams& p, int64_
 }
 
 // Publishing: every lane has written its part; lane 0 raises the flag.
-__device__ __forceinline__ void gated_publish(const GatedParams& p, unsigned int* flag, int lane,
+__device__ __forceinline__ void gated_publish(const GatedLinks& links, unsigned int* flag, int lane,
                                               unsigned int value) {
     __syncwarp();
-    if (lane == 0 && !p.withhold) {
+    if (lane == 0 && !links.withhold) {
         __threadfence();
         store_release(flag, value);
     }
 }
 
 // The state entering segment `pos` of a chain (positions in scan order) for
-// this lane's channels; called by one warp with the segment's own map.
-// Positions form groups of kGatedJoin.  The last of a group publishes the state
-// that leaves it, the others their maps; a segment waits for the state entering
-// its group and the maps of the group's earlier segments, and folds them in
-// order.  h is the state entering position 0 and becomes the one entering pos.
-__device__ __forceinline__ void gated_join(const GatedParams& p, int64_t group, int64_t pos, int lane,
-                                           const Maps& map, float2 (&h)[kGatedPairs]) {
+// this lane's kP pairs of channels; called by one warp with the segment's own
+// map (A, H).  Positions form groups of kGatedJoin.  The last of a group
+// publishes the state that leaves it, the others their maps; a segment waits for
+// the state entering its group and the maps of the group's earlier segments, and
+// folds them in order.  h is the state entering position 0 and becomes the one
+// entering pos.  False when the wait ran out.
+template <int kP>
+__device__ __forceinline__ bool gated_join(const GatedLinks& links, int64_t group, int64_t pos, int lane,
+                                           const float2 (&A)[kP], const float2 (&H)[kP], float2 (&h)[kP]) {
     const int64_t join = pos / kGatedJoin, first = join * kGatedJoin;
     const int before = (int)(pos - first);
-    unsigned int* flags = p.flags + group * p.segments;
-    float4* maps = p.maps + (group * p.segments) * 64 + lane;       // [segment][A | H][lane]
-    const int64_t joins = (p.segments + kGatedJoin - 1) / kGatedJoin;
-    float4* states = p.states + (group * joins) * 32 + lane;
+    unsigned int* flags = links.flags + group * links.segments;
+    float4* maps = links.maps + (group * links.segments) * (32 * kP) + lane;
+    const int64_t joins = (links.segments + kGatedJoin - 1) / kGatedJoin;
+    float2* states = links.states + (group * joins) * (32 * kP) + lane;
     const bool closes = before == kGatedJoin - 1;
-    if (!closes && pos + 1 < p.segments) {
-        const MapStore m = pack_maps(map);
-        __stcg(maps + pos * 64, m.A);
-        __stcg(maps + pos * 64 + 32, m.H);
-        gated_publish(p, flags + pos, lane, 1u);
+    if (!closes && pos + 1 < links.segments) {
+#pragma unroll
+        for (int k = 0; k < kP; ++k)
+            __stcg(maps + (pos * kP + k) * 32, make_float4(A[k].x, A[k].y, H[k].x, H[k].y));
+        gated_publish(links, flags + pos, lane, 1u);
     }
     // lane l < before waits for the map of segment first + l, lane kGatedJoin for the state
     const bool wait_map = lane < before, wait_state = lane == kGatedJoin && join > 0;
@@ -353,27 +362,32 @@ __device__ __forceinline__ void gated_join(const GatedParams& p, int64_t group, 
     }
     if (poll == kGatedPollLimit) {
         if (lane == 0) record_device_error(MAMBA_ERR_TIMEOUT);
-    } else {
-        if (join > 0) {
-            const float4 v = __ldcg(states + join * 32);
-            h[0] = make_float2(v.x, v.y);
-            h[1] = make_float2(v.z, v.w);
-        }
-#pragma unroll
-        for (int i = 0; i < kGatedJoin - 1; ++i)
-            if (i < before) {
-                const Maps m = unpack_maps(__ldcg(maps + (first + i) * 64), __ldcg(maps + (first + i) * 64 + 32));
-#pragma unroll
-                for (int k = 0; k < kGatedPairs; ++k) h[k] = __ffma2_rn(m.A[k], h[k], m.H[k]);
-            }
+        return false;
     }
-    if (closes && pos + 1 < p.segments) {
-        float2 e[kGatedPairs];
+    if (join > 0)
 #pragma unroll
-        for (int k = 0; k < kGatedPairs; ++k) e[k] = __ffma2_rn(map.A[k], h[k], map.H[k]);
-        __stcg(states + (join + 1) * 32, make_float4(e[0].x, e[0].y, e[1].x, e[1].y));
-        gated_publish(p, flags + pos, lane, 2u);
+        for (int k = 0; k < kP; ++k) h[k] = __ldcg(states + (join * kP + k) * 32);
+    constexpr int kBatch = 8;                    // maps asked for together
+    for (int c = 0; c < before; c += kBatch) {
+        float4 m[kBatch][kP];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int k = 0; k < kP; ++k)
+                m[i][k] = c + i < before ? __ldcg(maps + ((first + c + i) * kP + k) * 32)
+                                         : make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int k = 0; k < kP; ++k)
+                h[k] = __ffma2_rn(make_float2(m[i][k].x, m[i][k].y), h[k], make_float2(m[i][k].z, m[i][k].w));
     }
+    if (closes && pos + 1 < links.segments) {
+#pragma unroll
+        for (int k = 0; k < kP; ++k) __stcg(states + ((join + 1) * kP + k) * 32, __ffma2_rn(A[k], h[k], H[k]));
+        gated_publish(links, flags + pos, lane, 2u);
+    }
+    return true;
 }
 
 // The first item of a CTA.
@@ -399,7 +413,8 @@ __device__ __forceinline__ void gated_enter(const GatedParams& p, const GatedBlo
             all = compose(all, unpack_maps(sA[w][lane], sH[w][lane]));
         }
         float2 e[kGatedPairs] = {h[0], h[1]};
-        gated_join(p, at.group, at.pos, lane, all, e);
+        // a wait that ran out is recorded; the call's outputs are undefined then
+        gated_join<kGatedPairs>(p.links, at.group, at.pos, lane, all.A, all.H, e);
         entering[lane] = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
     }
     Maps mine = identity_maps();
@@ -429,19 +444,20 @@ __device__ __forceinline__ void load_state(const float* base, int64_t row, int64
     h[1] = q.get(1);
 }
 
-#ifndef GSUB
-#define GSUB 4
-#endif
-#ifndef GFMIN
-#define GFMIN 4
-#endif
-#ifndef GBMIN
-#define GBMIN 2
-#endif
-constexpr int kGatedSub = GSUB;                 // steps requested at a time
+constexpr int kGatedSub = 4;                 // steps requested at a time
+
+// Walks `left` steps, kGatedSub at a time.
+template <typename IoT, typename Load, typename Work>
+__device__ __forceinline__ void walk_block(int left, Load load, Work work) {
+    for (int s = 0; s < left; s += kGatedSub) {
+        Quad<IoT> f[kGatedSub], x[kGatedSub];
+        load(f, x, s);
+        work(f, x, s);
+    }
+}
 
 template <typename IoT, bool kLog, bool kVec>
-__global__ void __launch_bounds__(kGatedThreads, sizeof(IoT) == 2 ? GFMIN : GFMIN > 2 ? 2 : GFMIN)
+__global__ void __launch_bounds__(kGatedThreads, sizeof(IoT) == 2 ? 4 : 2)
     gated_scan_fwd_kernel(const __grid_constant__ GatedParams p) {
     __shared__ float4 sA[kGatedWarps][32], sH[kGatedWarps][32];
     __shared__ float4 entering[32];
@@ -461,37 +477,42 @@ __global__ void __launch_bounds__(kGatedThreads, sizeof(IoT) == 2 ? GFMIN : GFMI
         const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.t * p.x_s.row + at.c.d;
         int64_t following = p.items;
         if (p.blocks > 1) {
-            if (threadIdx.x == 0 && p.ticket != nullptr) next_slot = atomicAdd(p.ticket, 1u);
+            int64_t coming = 0;                  // asked for now, needed at the barrier
+            if (threadIdx.x == 0 && p.ticket != nullptr) coming = atomicAdd(p.ticket, 1u);
             Maps m = identity_maps();
             const IoT* gs = gate;
             const IoT* xs = x;
-            for (int s = 0; s < at.left; s += kGatedSub) {
-                Quad<IoT> rf[kGatedSub], rx[kGatedSub];
-                load_quads<IoT, kVec>(rf, gs, p.gate_s.row, at.left - s, live);
-                load_quads<IoT, kVec>(rx, xs, p.x_s.row, at.left - s, live);
-                gs += kGatedSub * p.gate_s.row;
-                xs += kGatedSub * p.x_s.row;
-                float2 a[kGatedSub][kGatedPairs], u[kGatedSub][kGatedPairs];
-#pragma unroll
-                for (int i = 0; i < kGatedSub; ++i)
-#pragma unroll
-                    for (int k = 0; k < kGatedPairs; ++k)
-                        gated_terms2<kLog>(rf[i].get(k), bias2[k], rx[i].get(k), a[i][k], u[i][k]);
-                if (at.left - s < kGatedSub)
+            walk_block<IoT>(
+                at.left,
+                [&](Quad<IoT> (&rf)[kGatedSub], Quad<IoT> (&rx)[kGatedSub], int s) {
+                    load_quads<IoT, kVec>(rf, gs, p.gate_s.row, at.left - s, live);
+                    load_quads<IoT, kVec>(rx, xs, p.x_s.row, at.left - s, live);
+                    gs += kGatedSub * p.gate_s.row;
+                    xs += kGatedSub * p.x_s.row;
+                },
+                [&](const Quad<IoT> (&rf)[kGatedSub], const Quad<IoT> (&rx)[kGatedSub], int s) {
+                    float2 a[kGatedSub][kGatedPairs], u[kGatedSub][kGatedPairs];
 #pragma unroll
                     for (int i = 0; i < kGatedSub; ++i)
-                        if (s + i >= at.left) a[i][0] = a[i][1] = one;       // u is 0: x was not read
 #pragma unroll
-                for (int i = 0; i < kGatedSub; ++i)
+                        for (int k = 0; k < kGatedPairs; ++k)
+                            gated_terms2<kLog>(rf[i].get(k), bias2[k], rx[i].get(k), a[i][k], u[i][k]);
+                    if (at.left - s < kGatedSub)
 #pragma unroll
-                    for (int k = 0; k < kGatedPairs; ++k) {
-                        m.H[k] = __ffma2_rn(a[i][k], m.H[k], u[i][k]);
-                        m.A[k] = __fmul2_rn(m.A[k], a[i][k]);
-                    }
-            }
+                        for (int i = 0; i < kGatedSub; ++i)
+                            if (s + i >= at.left) a[i][0] = a[i][1] = one;       // u is 0: x was not read
+#pragma unroll
+                    for (int i = 0; i < kGatedSub; ++i)
+#pragma unroll
+                        for (int k = 0; k < kGatedPairs; ++k) {
+                            m.H[k] = __ffma2_rn(a[i][k], m.H[k], u[i][k]);
+                            m.A[k] = __fmul2_rn(m.A[k], a[i][k]);
+                        }
+                });
             const MapStore ms = pack_maps(m);
             sA[warp][lane] = ms.A;
             sH[warp][lane] = ms.H;
+            if (threadIdx.x == 0) next_slot = coming;
             __syncthreads();
             if (p.ticket != nullptr) following = next_slot;
             gated_enter<false>(p, at, warp, lane, sA, sH, entering, h);
@@ -500,31 +521,34 @@ __global__ void __launch_bounds__(kGatedThreads, sizeof(IoT) == 2 ? GFMIN : GFMI
             store_quad<float, kVec>(p.enter + (at.b * p.blocks + at.block) * p.dim + at.c.d, live, h[0], h[1]);
         if (p.out != nullptr) {
             IoT* out = static_cast<IoT*>(p.out) + at.b * p.out_s.batch + at.t * p.out_s.row + at.c.d;
-            int s = 0;
-            for (; s < at.left; s += kGatedSub) {
-                Quad<IoT> rf[kGatedSub], rx[kGatedSub];
-                load_quads<IoT, kVec>(rf, gate, p.gate_s.row, at.left - s, live);
-                load_quads<IoT, kVec>(rx, x, p.x_s.row, at.left - s, live);
-                gate += kGatedSub * p.gate_s.row;
-                x += kGatedSub * p.x_s.row;
-                float2 a[kGatedSub][kGatedPairs], u[kGatedSub][kGatedPairs];
+            walk_block<IoT>(
+                at.left,
+                [&](Quad<IoT> (&rf)[kGatedSub], Quad<IoT> (&rx)[kGatedSub], int s) {
+                    load_quads<IoT, kVec>(rf, gate, p.gate_s.row, at.left - s, live);
+                    load_quads<IoT, kVec>(rx, x, p.x_s.row, at.left - s, live);
+                    gate += kGatedSub * p.gate_s.row;
+                    x += kGatedSub * p.x_s.row;
+                },
+                [&](const Quad<IoT> (&rf)[kGatedSub], const Quad<IoT> (&rx)[kGatedSub], int s) {
+                    float2 a[kGatedSub][kGatedPairs], u[kGatedSub][kGatedPairs];
 #pragma unroll
-                for (int i = 0; i < kGatedSub; ++i)
+                    for (int i = 0; i < kGatedSub; ++i)
 #pragma unroll
-                    for (int k = 0; k < kGatedPairs; ++k)
-                        gated_terms2<kLog>(rf[i].get(k), bias2[k], rx[i].get(k), a[i][k], u[i][k]);
+                        for (int k = 0; k < kGatedPairs; ++k)
+                            gated_terms2<kLog>(rf[i].get(k), bias2[k], rx[i].get(k), a[i][k], u[i][k]);
 #pragma unroll
-                for (int i = 0; i < kGatedSub; ++i) {
-                    const bool in = s + i < at.left;
-                    if (in) {
-                        h[0] = __ffma2_rn(a[i][0], h[0], u[i][0]);
-                        h[1] = __ffma2_rn(a[i][1], h[1], u[i][1]);
+                    for (int i = 0; i < kGatedSub; ++i) {
+                        const bool in = s + i < at.left;
+                        if (in) {
+                            h[0] = __ffma2_rn(a[i][0], h[0], u[i][0]);
+                            h[1] = __ffma2_rn(a[i][1], h[1], u[i][1]);
+                        }
+                        if (s + i < at.rows)
+                            store_quad<IoT, kVec>(out + i * p.out_s.row, live, in ? h[0] : zero, in ? h[1] : zero);
                     }
-                    if (s + i < at.rows)
-                        store_quad<IoT, kVec>(out + i * p.out_s.row, live, in ? h[0] : zero, in ? h[1] : zero);
-                }
-                out += kGatedSub * p.out_s.row;
-            }
+                    out += kGatedSub * p.out_s.row;
+                });
+            int s = (at.left + kGatedSub - 1) / kGatedSub * kGatedSub;
             for (; s < at.rows; ++s, out += p.out_s.row) store_quad<IoT, kVec>(out, live, zero, zero);
             if (p.last != nullptr && at.block == p.blocks - 1)
                 store_quad<float, kVec>(p.last + at.b * p.dim + at.c.d, live, h[0], h[1]);
@@ -540,7 +564,7 @@ constexpr int kGatedKept = kGatedBlock / kGatedSub;
 constexpr int kGatedBwdSmem = kGatedWarps * kGatedKept * 32 * (int)sizeof(float4);
 
 template <typename IoT, bool kLog, bool kVec>
-__global__ void __launch_bounds__(kGatedThreads, GBMIN)
+__global__ void __launch_bounds__(kGatedThreads, 2)
     gated_scan_bwd_kernel(const __grid_constant__ GatedParams p) {
     __shared__ float4 sA[kGatedWarps][32], sH[kGatedWarps][32];
     __shared__ float4 entering[32];
@@ -560,35 +584,69 @@ __global__ void __launch_bounds__(kGatedThreads, GBMIN)
         const IoT* gate = static_cast<const IoT*>(p.gate) + at.b * p.gate_s.batch + at.t * p.gate_s.row + at.c.d;
         const IoT* x = static_cast<const IoT*>(p.x) + at.b * p.x_s.batch + at.t * p.x_s.row + at.c.d;
         const IoT* dout = static_cast<const IoT*>(p.dout) + at.b * p.out_s.batch + at.t * p.out_s.row + at.c.d;
-        if (threadIdx.x == 0 && p.ticket != nullptr) next_slot = atomicAdd(p.ticket, 1u);
+        int64_t coming = 0;                      // asked for now, needed at the barrier
+        if (threadIdx.x == 0 && p.ticket != nullptr) coming = atomicAdd(p.ticket, 1u);
         load_state<kVec>(at.rows > 0 ? p.enter : nullptr, at.b * p.blocks + at.block, p.dim, at.c, h);
         Maps m = identity_maps();
-        for (int s = 0; s < at.left; s += kGatedSub) {
-            Quad<IoT> rf[kGatedSub], rx[kGatedSub], rd[kGatedSub];
-            load_quads<IoT, kVec>(rf, gate, p.gate_s.row, at.left - s, live);
-            load_quads<IoT, kVec>(rx, x, p.x_s.row, at.left - s, live);
-            load_quads<IoT, kVec>(rd, dout, p.out_s.row, at.left - s, live);
-            gate += kGatedSub * p.gate_s.row;
-            x += kGatedSub * p.x_s.row;
-            dout += kGatedSub * p.out_s.row;
+        struct Raw { Quad<IoT> f[kGatedSub], x[kGatedSub], d[kGatedSub]; };
+        auto load = [&](Raw& r, int s) {
+            load_quads<IoT, kVec>(r.f, gate, p.gate_s.row, at.left - s, live);
+            load_quads<IoT, kVec>(r.x, x, p.x_s.row, at.left - s, live);
+            load_quads<IoT, kVec>(r.d, dout, p.out_s.row, at.left - s, live);
+        };
+        auto forward = [&](const Raw& r, int s) {
             kept[s / kGatedSub * 32] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
 #pragma unroll
             for (int i = 0; i < kGatedSub; ++i)
 #pragma unroll
                 for (int k = 0; k < kGatedPairs; ++k) {
                     float2 a, u;
-                    gated_terms2<kLog>(rf[i].get(k), bias2[k], rx[i].get(k), a, u);
+                    gated_terms2<kLog>(r.f[i].get(k), bias2[k], r.x[i].get(k), a, u);
                     if (s + i >= at.left) a = one;              // u and dout are 0: not read
                     h[k] = __ffma2_rn(a, h[k], u);
                     m.A[k] = __fmul2_rn(m.A[k], a);
-                    m.H[k] = __ffma2_rn(m.A[k], rd[i].get(k), m.H[k]);
+                    m.H[k] = __ffma2_rn(m.A[k], r.d[i].get(k), m.H[k]);
                 }
+        };
+        auto move = [&](int steps) {
+            gate += steps * p.gate_s.row;
+            x += steps * p.x_s.row;
+            dout += steps * p.out_s.row;
+        };
+        // 16-bit inputs: registers for the next steps' loads under way
+        constexpr bool kAhead = sizeof(IoT) == 2;
+        Raw ra, rb;
+        if constexpr (kAhead) {
+            if (at.left > 0) load(ra, 0);
+            for (int s = 0; s < at.left; s += 2 * kGatedSub) {
+                move(kGatedSub);
+                if (s + kGatedSub < at.left) load(rb, s + kGatedSub);
+                forward(ra, s);
+                if (s + kGatedSub >= at.left) break;
+                move(kGatedSub);
+                if (s + 2 * kGatedSub < at.left) load(ra, s + 2 * kGatedSub);
+                forward(rb, s + kGatedSub);
+            }
+        } else {
+            for (int s = 0; s < at.left; s += kGatedSub) {
+                Raw raw;
+                load(raw, s);
+                move(kGatedSub);
+                forward(raw, s);
+            }
         }
+        // the pointers now stand at the block's end, in whole groups of kGatedSub steps
         const MapStore ms = pack_maps(m);
         sA[warp][lane] = ms.A;
         sH[warp][lane] = ms.H;
+        if (threadIdx.x == 0) next_slot = coming;
         __syncthreads();
         const int64_t following = p.ticket != nullptr ? next_slot : p.items;
+        // phase two's first loads, under way during the join
+        if (kAhead && at.left > 0) {
+            move(-kGatedSub);
+            load(ra, (at.left - 1) / kGatedSub * kGatedSub);
+        }
         float2 r[kGatedPairs];
         load_state<kVec>(p.dlast, at.b, p.dim, at.c, r);
         gated_enter<true>(p, at, warp, lane, sA, sH, entering, r);
@@ -603,17 +661,10 @@ __global__ void __launch_bounds__(kGatedThreads, GBMIN)
         const int top = (at.left + kGatedSub - 1) / kGatedSub * kGatedSub;
         dgate += top * p.dgate_s.row;
         dx += top * p.dx_s.row;
-        for (int s = top - kGatedSub; s >= 0; s -= kGatedSub) {
+        auto backward = [&](const Raw& raw, int s) {
             const int left = at.left - s;
-            Quad<IoT> rf[kGatedSub], rx[kGatedSub], rd[kGatedSub];
-            gate -= kGatedSub * p.gate_s.row;
-            x -= kGatedSub * p.x_s.row;
-            dout -= kGatedSub * p.out_s.row;
             dgate -= kGatedSub * p.dgate_s.row;
             dx -= kGatedSub * p.dx_s.row;
-            load_quads<IoT, kVec>(rf, gate, p.gate_s.row, left, live);
-            load_quads<IoT, kVec>(rx, x, p.x_s.row, left, live);
-            load_quads<IoT, kVec>(rd, dout, p.out_s.row, left, live);
             float2 a[kGatedSub][kGatedPairs], g[kGatedSub][kGatedPairs], before[kGatedSub][kGatedPairs];
             const float4 hk = kept[s / kGatedSub * 32];
             h[0] = make_float2(hk.x, hk.y);
@@ -622,9 +673,9 @@ __global__ void __launch_bounds__(kGatedThreads, GBMIN)
             for (int i = 0; i < kGatedSub; ++i)
 #pragma unroll
                 for (int k = 0; k < kGatedPairs; ++k) {
-                    gated_gains2<kLog>(rf[i].get(k), bias2[k], g[i][k], a[i][k]);
+                    gated_gains2<kLog>(raw.f[i].get(k), bias2[k], g[i][k], a[i][k]);
                     before[i][k] = h[k];
-                    h[k] = __ffma2_rn(a[i][k], h[k], kLog ? rx[i].get(k) : __fmul2_rn(g[i][k], rx[i].get(k)));
+                    h[k] = __ffma2_rn(a[i][k], h[k], kLog ? raw.x[i].get(k) : __fmul2_rn(g[i][k], raw.x[i].get(k)));
                 }
 #pragma unroll
             for (int i = kGatedSub - 1; i >= 0; --i)
@@ -632,13 +683,13 @@ __global__ void __launch_bounds__(kGatedThreads, GBMIN)
                     float2 df[kGatedPairs], dv[kGatedPairs];
 #pragma unroll
                     for (int k = 0; k < kGatedPairs; ++k) {
-                        const float2 l = __fadd2_rn(rd[i].get(k), r[k]);
+                        const float2 l = __fadd2_rn(raw.d[i].get(k), r[k]);
                         r[k] = __fmul2_rn(a[i][k], l);
                         if constexpr (kLog) {
                             dv[k] = l;
                             df[k] = __fmul2_rn(r[k], before[i][k]);
                         } else {
-                            const float2 diff = __ffma2_rn(before[i][k], make_float2(-1.0f, -1.0f), rx[i].get(k));
+                            const float2 diff = __ffma2_rn(before[i][k], make_float2(-1.0f, -1.0f), raw.x[i].get(k));
                             dv[k] = __fmul2_rn(g[i][k], l);
                             df[k] = __fmul2_rn(__fmul2_rn(g[i][k], r[k]), diff);
                         }
@@ -647,6 +698,28 @@ __global__ void __launch_bounds__(kGatedThreads, GBMIN)
                     store_quad<IoT, kVec>(dgate + i * p.dgate_s.row, live, df[0], df[1]);
                     store_quad<IoT, kVec>(dx + i * p.dx_s.row, live, dv[0], dv[1]);
                 }
+        };
+        if constexpr (kAhead) {
+            for (int s = top - kGatedSub; s >= 0; s -= 2 * kGatedSub) {
+                if (s > 0) {
+                    move(-kGatedSub);
+                    load(rb, s - kGatedSub);
+                }
+                backward(ra, s);
+                if (s == 0) break;
+                if (s > kGatedSub) {
+                    move(-kGatedSub);
+                    load(ra, s - 2 * kGatedSub);
+                }
+                backward(rb, s - kGatedSub);
+            }
+        } else {
+            for (int s = top - kGatedSub; s >= 0; s -= kGatedSub) {
+                Raw raw;
+                move(-kGatedSub);
+                load(raw, s);
+                backward(raw, s);
+            }
         }
         if (p.dh0 != nullptr && at.block == 0)
             store_quad<float, kVec>(p.dh0 + at.b * p.dim + at.c.d, live, r[0], r[1]);
@@ -809,6 +882,61 @@ __device__ __forceinline__ void row_gains(float2 (&a)[8], float2 (&g)[8], float2
         }
 }
 
+// Two rows' eight steps of one tensor, asked for before any is unpacked: vectors
+// where they are aligned and inside the tensor, else (ok false) element by
+// element in fill().
+template <typename IoT>
+struct RowPair {
+    uint4 r0[sizeof(IoT) / 2], r1[sizeof(IoT) / 2];
+    bool ok0, ok1;
+    __device__ __forceinline__ void load(const IoT* p0, const IoT* p1, const Span& span) {
+        ok0 = (reinterpret_cast<uintptr_t>(p0) & 15) == 0 && span.holds(p0, 8 * (int)sizeof(IoT));
+        ok1 = (reinterpret_cast<uintptr_t>(p1) & 15) == 0 && span.holds(p1, 8 * (int)sizeof(IoT));
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(IoT) / 2; ++i) {
+            r0[i] = ok0 ? reinterpret_cast<const uint4*>(p0)[i] : make_uint4(0, 0, 0, 0);
+            r1[i] = ok1 ? reinterpret_cast<const uint4*>(p1)[i] : make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void get(float2 (&v)[8]) const {
+        float a[8], b[8];
+        unpack_steps<IoT>(r0, a);
+        unpack_steps<IoT>(r1, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = make_float2(a[i], b[i]);
+    }
+    // Steps outside [0, n) become 0; those that no vector brought are read.
+    __device__ __forceinline__ void fill(float2 (&v)[8], const IoT* p0, int t0, int n0, const IoT* p1, int t1, int n1) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (t0 + i < 0 || t0 + i >= n0) v[i].x = 0.0f;
+            if (t1 + i < 0 || t1 + i >= n1) v[i].y = 0.0f;
+        }
+        if (!ok0)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (t0 + i >= 0 && t0 + i < n0) v[i].x = DType<IoT>::load(p0 + i);
+        if (!ok1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (t1 + i >= 0 && t1 + i < n1) v[i].y = DType<IoT>::load(p1 + i);
+    }
+};
+
+__device__ __forceinline__ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename IoT>
+__device__ __forceinline__ void store_pair_rows(IoT* p0, IoT* p1, const float2 (&v)[8]) {
+    float a[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        a[i] = v[i].x;
+        b[i] = v[i].y;
+    }
+    store_eight(p0, a);
+    store_eight(p1, b);
+}
+
 template <typename IoT, bool kLog, int kWarps>
 __global__ void __launch_bounds__(kGatedThreads)
     gated_scan_rows_fwd_kernel(const __grid_constant__ GatedParams p, int width) {
@@ -826,8 +954,19 @@ __global__ void __launch_bounds__(kGatedThreads)
     for (int tile = 0; tile < tiles; ++tile) {
         const int t0 = tile * at.step + at.r0.shift, t1 = tile * at.step + at.r1.shift;
         float2 a[8], u[8], g[8];
-        load_steps2(gate0, t0, 0, at.r0.n, gate1, t1, 0, at.r1.n, gspan, a);
-        load_steps2(x0, t0, 0, at.r0.n, x1, t1, 0, at.r1.n, xspan, u);
+        RowPair<IoT> gr, xr;
+        gr.load(gate0 + t0, gate1 + t1, gspan);
+        xr.load(x0 + t0, x1 + t1, xspan);
+        // the whole warp inside both sequences, on vectors
+        const bool whole = __all_sync(0xffffffffu, t0 >= 0 && t1 >= 0 && t0 + 8 <= at.r0.n && t1 + 8 <= at.r1.n &&
+                                                       gr.ok0 && gr.ok1 && xr.ok0 && xr.ok1 && on16(out0 + t0) &&
+                                                       on16(out1 + t1));
+        gr.get(a);
+        xr.get(u);
+        if (!whole) {
+            gr.fill(a, gate0 + t0, t0, at.r0.n, gate1 + t1, t1, at.r1.n);
+            xr.fill(u, x0 + t0, t0, at.r0.n, x1 + t1, t1, at.r1.n);
+        }
         row_gains<kLog>(a, g, bias2, t0, at.r0.n, t1, at.r1.n);
         float2 A = make_float2(1.0f, 1.0f), H = make_float2(0.0f, 0.0f), At, Ht;
 #pragma unroll
@@ -845,12 +984,15 @@ __global__ void __launch_bounds__(kGatedThreads)
             h = __ffma2_rn(a[i], h, u[i]);
             u[i] = h;
         }
-        if (t0 + 8 > at.r0.n || t1 + 8 > at.r1.n)
+        if (whole) {
+            store_pair_rows(out0 + t0, out1 + t1, u);
+            continue;
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (t0 + i >= at.r0.n) u[i].x = 0.0f;
-                if (t1 + i >= at.r1.n) u[i].y = 0.0f;
-            }
+        for (int i = 0; i < 8; ++i) {
+            if (t0 + i >= at.r0.n) u[i].x = 0.0f;
+            if (t1 + i >= at.r1.n) u[i].y = 0.0f;
+        }
         store_steps2(out0, t0, 0, at.r0.hi, out1, t1, 0, at.r1.hi, u);
     }
     at.put(p.last, carry);
@@ -878,8 +1020,17 @@ __global__ void __launch_bounds__(kGatedThreads, 2)
     for (int tile = 0; tile + 1 < tiles; ++tile) {
         const int t0 = tile * at.step + at.r0.shift, t1 = tile * at.step + at.r1.shift;
         float2 a[8], x[8], g[8];
-        load_steps2(gate0, t0, 0, at.r0.n, gate1, t1, 0, at.r1.n, gspan, a);
-        load_steps2(x0, t0, 0, at.r0.n, x1, t1, 0, at.r1.n, xspan, x);
+        RowPair<IoT> gr, xr;
+        gr.load(gate0 + t0, gate1 + t1, gspan);
+        xr.load(x0 + t0, x1 + t1, xspan);
+        const bool whole = __all_sync(0xffffffffu, t0 >= 0 && t1 >= 0 && t0 + 8 <= at.r0.n && t1 + 8 <= at.r1.n &&
+                                                       gr.ok0 && gr.ok1 && xr.ok0 && xr.ok1);
+        gr.get(a);
+        xr.get(x);
+        if (!whole) {
+            gr.fill(a, gate0 + t0, t0, at.r0.n, gate1 + t1, t1, at.r1.n);
+            xr.fill(x, x0 + t0, t0, at.r0.n, x1 + t1, t1, at.r1.n);
+        }
         row_gains<kLog>(a, g, bias2, t0, at.r0.n, t1, at.r1.n);
         float2 A = one, H = zero, At, Ht;
 #pragma unroll
@@ -908,9 +1059,22 @@ __global__ void __launch_bounds__(kGatedThreads, 2)
     for (int tile = tiles - 1; tile >= 0; --tile) {
         const int t0 = tile * at.step + at.r0.shift, t1 = tile * at.step + at.r1.shift;
         float2 a[8], g[8], x[8], dd[8];
-        load_steps2(gate0, t0, 0, at.r0.n, gate1, t1, 0, at.r1.n, gspan, a);
-        load_steps2(x0, t0, 0, at.r0.n, x1, t1, 0, at.r1.n, xspan, x);
-        load_steps2(dout0, t0, 0, at.r0.n, dout1, t1, 0, at.r1.n, dspan, dd);
+        RowPair<IoT> gr, xr, dr;
+        gr.load(gate0 + t0, gate1 + t1, gspan);
+        xr.load(x0 + t0, x1 + t1, xspan);
+        dr.load(dout0 + t0, dout1 + t1, dspan);
+        const bool whole = __all_sync(0xffffffffu, t0 >= 0 && t1 >= 0 && t0 + 8 <= at.r0.n && t1 + 8 <= at.r1.n &&
+                                                       gr.ok0 && gr.ok1 && xr.ok0 && xr.ok1 && dr.ok0 && dr.ok1 &&
+                                                       on16(dgate0 + t0) && on16(dgate1 + t1) && on16(dx0 + t0) &&
+                                                       on16(dx1 + t1));
+        gr.get(a);
+        xr.get(x);
+        dr.get(dd);
+        if (!whole) {
+            gr.fill(a, gate0 + t0, t0, at.r0.n, gate1 + t1, t1, at.r1.n);
+            xr.fill(x, x0 + t0, t0, at.r0.n, x1 + t1, t1, at.r1.n);
+            dr.fill(dd, dout0 + t0, t0, at.r0.n, dout1 + t1, t1, at.r1.n);
+        }
         if (tile + 1 < tiles) carry = make_float2(states0[tile], states1[tile]);
         row_gains<kLog>(a, g, bias2, t0, at.r0.n, t1, at.r1.n);
         float2 A = one, H = zero, At, Ht;
@@ -955,8 +1119,13 @@ __global__ void __launch_bounds__(kGatedThreads, 2)
             }
 #pragma unroll
         for (int i = 0; i < 8; ++i) db = __fadd2_rn(db, dd[i]);
-        store_steps2(dgate0, t0, 0, at.r0.hi, dgate1, t1, 0, at.r1.hi, dd);
-        store_steps2(dx0, t0, 0, at.r0.hi, dx1, t1, 0, at.r1.hi, x);
+        if (whole) {
+            store_pair_rows(dgate0 + t0, dgate1 + t1, dd);
+            store_pair_rows(dx0 + t0, dx1 + t1, x);
+        } else {
+            store_steps2(dgate0, t0, 0, at.r0.hi, dgate1, t1, 0, at.r1.hi, dd);
+            store_steps2(dx0, t0, 0, at.r0.hi, dx1, t1, 0, at.r1.hi, x);
+        }
     }
     at.put(p.dh0, r_carry);
     if (p.bias_partial != nullptr) {

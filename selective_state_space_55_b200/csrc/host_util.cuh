@@ -25,6 +25,13 @@ inline bool dtype_ok(int32_t dt) { return dt == MAMBA_F32 || dt == MAMBA_BF16; }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// Do two buffers of `bytes` overlap without being the same?
+inline bool partly_overlap(const void* a, const void* b, size_t bytes) {
+    if (a == nullptr || b == nullptr || a == b) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bytes && y < x + bytes;
+}
+
 // SM count of the current device, cached per device.
 inline int current_sm_count(int* device_out) {
     static int cached[kMaxDevices] = {0};

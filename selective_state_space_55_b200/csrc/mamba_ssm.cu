@@ -1037,12 +1037,6 @@ mamba_status_t check_conv(const mamba_dims_t* dims, int width, bool seq) {
     return MAMBA_OK;
 }
 
-bool partly_overlap(const void* a, const void* b, size_t bytes) {
-    if (a == nullptr || b == nullptr || a == b) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + bytes && y < x + bytes;
-}
-
 unsigned int blocks_for(int64_t threads) {
     return (unsigned int)((threads + kConvThreads - 1) / kConvThreads);
 }

@@ -79,18 +79,7 @@ __device__ __forceinline__ void load_steps(const T* row, int t0, int lo, int hi,
     }
 }
 
-// Two rows side by side (x: first row, y: second), so that the arithmetic runs
-// in packed fp32x2.  The rows' steps may differ (their phases do).
-template <typename T>
-__device__ __forceinline__ void load_steps2(const T* row0, int t0, int lo0, int hi0, const T* row1,
-                                            int t1, int lo1, int hi1, const Span& span, float2 (&v)[8]) {
-    float a[8], b[8];
-    load_steps(row0, t0, lo0, hi0, span, a);
-    load_steps(row1, t1, lo1, hi1, span, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = make_float2(a[i], b[i]);
-}
-
+// Pairs of values, one per row of two that a warp works on side by side.
 __device__ __forceinline__ float2 shfl_up2(float2 v, int o, int width = 32) {
     return make_float2(__shfl_up_sync(0xffffffffu, v.x, o, width), __shfl_up_sync(0xffffffffu, v.y, o, width));
 }

@@ -69,6 +69,7 @@ def test_gated_refuses_aliased_and_overlapping_outputs(lib):
     assert gated_bwd(lib, gated_dims(), dx=FAKE) == INVALID
     assert gated_bwd(lib, gated_dims(), dout=None) == INVALID
     assert gated_bwd(lib, gated_dims(dx=S(64, 64))) == INVALID
+    assert gated_fwd(lib, gated_dims(), h0=0x40000, last=0x40100) == INVALID     # partial overlap of the states
     # time-major rows do not overlap: the next check (the workspace) answers
     assert gated_fwd(lib, gated_dims(out=S(64, 2 * 64))) == WORKSPACE
 
@@ -84,9 +85,9 @@ def test_gated_empty_problems_need_nothing(lib):
 def test_gated_workspace_sizes(lib):
     size = lambda **kw: lib.mamba_gated_scan_workspace_bytes(ctypes.byref(gated_dims(**kw)))  # noqa: E731
     bwd = lambda have, **kw: lib.mamba_gated_scan_bwd_workspace_bytes(ctypes.byref(gated_dims(**kw)), have)  # noqa: E731
-    assert size(seqlen=512) == 0                   # one segment per chain: nothing to hand on
+    assert size(seqlen=256) == 0                   # one segment per chain: nothing to hand on
     assert size(flags=0, seqlen=100000) == 0       # a chain stays with its warps
-    assert size(seqlen=513) > 0
+    assert size(seqlen=257) > 0
     assert bwd(0) > bwd(1) > 0
     none = ctypes.c_size_t(-1).value
     assert size(batch=-1) == none and bwd(0, io_dtype=9) == none

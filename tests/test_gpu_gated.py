@@ -80,7 +80,7 @@ def test_rows_layout_tile_borders(dtype, L):
 @pytest.mark.parametrize("log_decay", [False, True])
 @pytest.mark.parametrize("layout", ["bld", "bdl"])
 def test_many_tiles(layout, log_decay):
-    """20,000 steps: 40 segments joined in groups of 8 (10 tiles in the rows layout)."""
+    """20,000 steps: 40 segments in two join groups (10 tiles in the rows layout)."""
     v, back = make(1, 66, 20000, layout, BF, log_decay, seed=5)
     check(v, back, layout, log_decay)
 
@@ -340,6 +340,16 @@ def test_withheld_handoff_is_reported():
     assert ops.device_status() == 0
     want = ref.gated(**v, layout="bld")
     assert_close("out", ops.gated_scan_fwd(**v, layout="bld"), *want["out"])
+
+
+@pytest.mark.parametrize("log_decay", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("batch,dim,L", [(1, 64, 7000), (2, 200, 513), (3, 72, 257), (1, 1536, 300), (5, 16, 31)])
+def test_few_chains(batch, dim, L, dtype, log_decay):
+    """Fewer than 128 groups, rows on 16-byte boundaries: segments of a chain kept on chip
+    while they are joined; 7000 steps are more segments than one join group holds."""
+    v, back = make(batch, dim, L, "bld", dtype, log_decay, seed=L + dim)
+    check(v, back, "bld", log_decay)
 
 
 CHAINED = [(4, 2048, 1100), (2, 4160, 700), (130, 64, 70), (3, 2728, 130), (9, 1000, 600)]
