@@ -246,6 +246,8 @@ bool resolve_strides(const mamba_strides_t& s, int64_t batch, int64_t rows, int6
         const int64_t near = row_first ? s.row : s.batch, far = row_first ? s.batch : s.row;
         if (far < near * ((row_first ? rows : batch) - 1) + inner) return false;
     }
+    if (rows <= 1) out->row = inner;            // distances of extent one are never stepped
+    if (batch <= 1) out->batch = out->row * std::max<int64_t>(rows, 1);
     return true;
 }
 
@@ -272,13 +274,19 @@ struct GatedLayout {           // offsets in the workspace, bytes
     int warps, width;          // (batch, seqlen, dim): blocks per segment; else warps and lanes per chain
     // chained stretches
     size_t chain_zeroed, chain_zeroed_bytes, chain_handoff, chain_bias;
+    bool chained;
     int64_t chain_groups, chain_stretches, chain_stretch_tiles;
     // segments of few chains, forward
     size_t seg_zeroed, seg_zeroed_bytes, seg_maps, seg_states;
     int64_t seg_segments;
 };
 
-constexpr int64_t kChainMinGroups = 128;
+// Chains of 64 channels from which a CTA per chain beats splitting time, both timed
+// with dim 4096 (us, chained / split).  bf16 forward, L 4096: 128 groups 117 / 68, 192
+// 123 / 92, 256 129 / 115, 512 183 / 226; L 1024, 256: 45 / 41.  bf16 backward, L 4096:
+// 128 164 / 131, 192 178 / 186, 256 180 / 238.  fp32, L 4096: forward 128 115 / 96, 192
+// 125 / 135; backward 192 264 / 266.
+constexpr int64_t kChainMinGroups = 192, kChainMinGroupsBf16Forward = 320;
 constexpr int64_t kChainResident = 2 * 148;      // CTAs that a B200 holds
 
 // One segment per chain needs no look-back: no tickets, flags or maps.
@@ -313,8 +321,11 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
         w->chain_stretch_tiles = (w->blocks + w->chain_stretches - 1) / w->chain_stretches;
         w->chain_stretches = (w->blocks + w->chain_stretch_tiles - 1) / w->chain_stretch_tiles;
         const size_t items = (size_t)w->chain_groups * w->chain_stretches;
-        if (!backward && w->chain_groups < kChainMinGroups) {
-            const int64_t steps = d->io_dtype == MAMBA_BF16 ? SegmentSizes<__nv_bfloat16>::kSegment : SegmentSizes<float>::kSegment;
+        const bool bf16 = d->io_dtype == MAMBA_BF16;
+        w->chained = w->chain_groups >= (bf16 && !backward ? kChainMinGroupsBf16Forward : kChainMinGroups) &&
+                     items < (size_t)kLimit31 / 2;
+        if (!backward && !w->chained) {
+            const int64_t steps = bf16 ? SegmentSizes<__nv_bfloat16>::kSegment : SegmentSizes<float>::kSegment;
             w->seg_segments = (L + steps - 1) / steps;
             if (w->seg_segments > 1) {
                 const size_t n = (size_t)w->chain_groups * w->seg_segments;
@@ -324,7 +335,7 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
                 w->seg_states = take((size_t)w->chain_groups * ((w->seg_segments + kGatedJoin - 1) / kGatedJoin) * 32 * sizeof(float2));
             }
         }
-        if (w->chain_groups >= kChainMinGroups && items < (size_t)kLimit31 / 2) {
+        if (w->chained) {
             if (w->chain_stretches > 1) {
                 w->chain_zeroed = take(256 + items * sizeof(unsigned int));
                 w->chain_zeroed_bytes = 256 + items * sizeof(unsigned int);
@@ -334,16 +345,13 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
         }
     } else {
         // Lanes take 8 steps each; the row's start may lie up to phase_max steps into its tile.
-        const int64_t span = L + phase_max;
-        w->warps = 1;
+        const int64_t span = L + phase_max, units = (span + kWarpSteps - 1) / kWarpSteps;
+        if (chains >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
+        w->tiles = (units + kRowWarps - 1) / kRowWarps;
+        w->warps = (int)((units + w->tiles - 1) / w->tiles);
         w->width = 32;
-        if (span <= kWarpSteps) {
+        if (units == 1)
             while (w->width > 1 && (w->width / 2) * (int64_t)kLaneSteps >= span) w->width /= 2;
-        } else {
-            while (w->warps < kGatedWarps && w->warps * (int64_t)kWarpSteps < span) w->warps *= 2;
-        }
-        const int64_t step = (int64_t)w->warps * w->width * kLaneSteps;
-        w->tiles = (span + step - 1) / step;
         if (backward) {
             w->bias = take((size_t)chains * sizeof(float));
             if (w->tiles > 1) w->states = take((size_t)chains * w->tiles * sizeof(float));
@@ -547,34 +555,40 @@ mamba_status_t run_gated_segments(const GatedParams& g, const GatedLayout& w, co
                                : launch_gated_segments<float, false>(prm, dev, sms, stream));
 }
 
-template <typename IoT, bool kLog, bool kBackward>
-cudaError_t launch_gated_rows(const GatedParams& prm, const GatedLayout& w, cudaStream_t stream) {
-    const int64_t per_cta = w.warps > 1 ? kGatedWarps / w.warps : (int64_t)kGatedWarps * (32 / w.width);
-    const unsigned grid = (unsigned)(((prm.chains + 1) / 2 + per_cta - 1) / per_cta);     // CTAs hold pairs of chains
-#define MAMBA_GATED_ROWS(W)                                                                          \
-    if constexpr (kBackward)                                                                         \
-        gated_scan_rows_bwd_kernel<IoT, kLog, W><<<grid, kGatedThreads, 0, stream>>>(prm, w.width); \
-    else                                                                                             \
-        gated_scan_rows_fwd_kernel<IoT, kLog, W><<<grid, kGatedThreads, 0, stream>>>(prm, w.width)
-    switch (w.warps) {
-        case 1: MAMBA_GATED_ROWS(1); break;
-        case 2: MAMBA_GATED_ROWS(2); break;
-        case 4: MAMBA_GATED_ROWS(4); break;
-        default: MAMBA_GATED_ROWS(8); break;
-    }
-#undef MAMBA_GATED_ROWS
+template <typename IoT, bool kLog, bool kMulti, bool kBackward>
+cudaError_t launch_gated_rows(const GatedParams& prm, const GatedLayout& w, int dev, int sms, cudaStream_t stream) {
+    static int resident[kRowWarps + 1][kMaxDevices] = {};
+    static bool attr_done[kMaxDevices] = {false};
+    auto kernel = gated_scan_rows_fwd_kernel<IoT, kLog, kMulti>;
+    if constexpr (kBackward) kernel = gated_scan_rows_bwd_kernel<IoT, kLog, kMulti>;
+    constexpr int per_thread = RowStages<IoT, kBackward ? 3 : 2>::kBytesPerThread;
+    const cudaError_t e = ensure_smem_attr(kernel, per_thread * kRowThreads, attr_done, dev);
+    if (e != cudaSuccess) return e;
+    const int teams = std::max(1, kGatedWarps / w.warps), threads = teams * w.warps * 32;
+    const int64_t per_cta = (int64_t)teams * (32 / w.width);                  // pairs of chains
+    const int64_t blocks = (prm.batch * ((prm.dim + 1) / 2) + per_cta - 1) / per_cta;
+    const int per_sm = resident_ctas(kernel, threads, (size_t)per_thread * threads, resident[w.warps], dev);
+    if (per_sm <= 0) return cudaErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)per_sm * sms);
+    kernel<<<grid, threads, per_thread * threads, stream>>>(prm, w.warps, w.width, blocks);
     return cudaGetLastError();
+}
+
+template <typename IoT, bool kLog, bool kBackward>
+cudaError_t dispatch_gated_teams(const GatedParams& prm, const GatedLayout& w, int dev, int sms, cudaStream_t stream) {
+    return w.warps > 1 ? launch_gated_rows<IoT, kLog, true, kBackward>(prm, w, dev, sms, stream)
+                       : launch_gated_rows<IoT, kLog, false, kBackward>(prm, w, dev, sms, stream);
 }
 
 template <bool kBackward>
 cudaError_t dispatch_gated_rows(const GatedParams& prm, const GatedLayout& w, bool bf16, bool log_decay,
-                                cudaStream_t stream) {
+                                int dev, int sms, cudaStream_t stream) {
     using B = __nv_bfloat16;
     if (bf16)
-        return log_decay ? launch_gated_rows<B, true, kBackward>(prm, w, stream)
-                         : launch_gated_rows<B, false, kBackward>(prm, w, stream);
-    return log_decay ? launch_gated_rows<float, true, kBackward>(prm, w, stream)
-                     : launch_gated_rows<float, false, kBackward>(prm, w, stream);
+        return log_decay ? dispatch_gated_teams<B, true, kBackward>(prm, w, dev, sms, stream)
+                         : dispatch_gated_teams<B, false, kBackward>(prm, w, dev, sms, stream);
+    return log_decay ? dispatch_gated_teams<float, true, kBackward>(prm, w, dev, sms, stream)
+                     : dispatch_gated_teams<float, false, kBackward>(prm, w, dev, sms, stream);
 }
 
 // Can every row of this tensor start a vector of `bytes`?
@@ -939,18 +953,14 @@ MAMBA_API mamba_status_t mamba_gated_scan_fwd(const void* gate, const void* x, c
     prm.out = out;
     prm.last = last_state;
     const bool bf16 = dims->io_dtype == MAMBA_BF16, log_decay = dims->log_decay != 0;
-    if (!bld) {
-        const int64_t per_cta = w.warps > 1 ? kGatedWarps / w.warps : kGatedWarps;
-        if (prm.chains / per_cta >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
-        return status_of(dispatch_gated_rows<false>(prm, w, bf16, log_decay, stream));
-    }
     int dev = 0;
     const int sms = current_sm_count(&dev);
     if (sms <= 0) return MAMBA_ERR_CUDA;
+    if (!bld) return status_of(dispatch_gated_rows<false>(prm, w, bf16, log_decay, dev, sms, stream));
     prm.enter = checkpoints;
     if (chain_tensor_ok(gate, prm.gate_s, es, dims->batch) && chain_tensor_ok(x, prm.x_s, es, dims->batch) &&
         chain_tensor_ok(out, prm.out_s, es, dims->batch))
-        return w.chain_groups >= kChainMinGroups ? run_gated_chain<false>(prm, w, dims, ws, dev, sms, stream)
+        return w.chained ? run_gated_chain<false>(prm, w, dims, ws, dev, sms, stream)
                                                  : run_gated_segments(prm, w, dims, ws, dev, sms, stream);
     if (w.zeroed && cudaMemsetAsync(ws, 0, w.zeroed, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
     const bool vec = dims->dim % 4 == 0 && rows_aligned(gate, prm.gate_s, es, 4 * es) &&
@@ -995,6 +1005,7 @@ MAMBA_API mamba_status_t mamba_gated_scan_bwd(
         !resolve_strides(dims->dgate, dims->batch, rows, inner, true, &prm.dgate_s) ||
         !resolve_strides(dims->dx, dims->batch, rows, inner, true, &prm.dx_s))
         return MAMBA_ERR_INVALID_ARG;
+    if (partly_overlap(dlast_state, dinitial_state, (size_t)prm.chains * sizeof(float))) return MAMBA_ERR_INVALID_ARG;
     if (dims->seqlen > 0 && (dgate == dx || dgate == gate || dgate == x || dgate == dout || dx == gate || dx == x || dx == dout))
         return MAMBA_ERR_INVALID_ARG;
     if (dims->seqlen == 0) {
@@ -1018,18 +1029,16 @@ MAMBA_API mamba_status_t mamba_gated_scan_bwd(
     prm.bias_partial = dgate_bias != nullptr ? reinterpret_cast<float*>(ws + w.bias) : nullptr;
     const bool bf16 = dims->io_dtype == MAMBA_BF16, log_decay = dims->log_decay != 0;
     cudaError_t e;
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
+    if (sms <= 0) return MAMBA_ERR_CUDA;
     if (!bld) {
-        const int64_t per_cta = w.warps > 1 ? kGatedWarps / w.warps : kGatedWarps;
-        if (prm.chains / per_cta >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
         prm.chain_states = w.tiles > 1 ? reinterpret_cast<float*>(ws + w.states) : nullptr;
-        e = dispatch_gated_rows<true>(prm, w, bf16, log_decay, stream);
+        e = dispatch_gated_rows<true>(prm, w, bf16, log_decay, dev, sms, stream);
         if (e == cudaSuccess && dgate_bias != nullptr)
             e = launch_column_sum(prm.bias_partial, dims->batch, dims->dim, dims->dim, dgate_bias, nullptr, stream);
         return status_of(e);
     }
-    int dev = 0;
-    const int sms = current_sm_count(&dev);
-    if (sms <= 0) return MAMBA_ERR_CUDA;
     if (w.zeroed && cudaMemsetAsync(ws, 0, w.zeroed, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
     const bool vec_in = dims->dim % 4 == 0 && rows_aligned(gate, prm.gate_s, es, 4 * es) &&
                         rows_aligned(x, prm.x_s, es, 4 * es) && (!gate_bias || aligned(gate_bias, 16)) &&
@@ -1049,7 +1058,7 @@ MAMBA_API mamba_status_t mamba_gated_scan_bwd(
     } else {
         prm.enter = const_cast<float*>(checkpoints);
     }
-    if (w.chain_groups >= kChainMinGroups && chain_tensor_ok(gate, prm.gate_s, es, dims->batch) &&
+    if (w.chained && chain_tensor_ok(gate, prm.gate_s, es, dims->batch) &&
         chain_tensor_ok(x, prm.x_s, es, dims->batch) && chain_tensor_ok(dout, prm.out_s, es, dims->batch) &&
         chain_tensor_ok(dgate, prm.dgate_s, es, dims->batch) && chain_tensor_ok(dx, prm.dx_s, es, dims->batch) &&
         dims->dim % 4 == 0 && aligned(prm.enter, 16)) {

@@ -567,7 +567,10 @@ __global__ void __launch_bounds__(kChainWarps * 32, 3)
         if (t < p.seqlen) {
             failed = !mbar_wait_bounded(bar, parity);
             parity ^= 1;
-            if (failed) record_device_error(MAMBA_ERR_TIMEOUT);
+            if (failed) {
+                record_device_error(MAMBA_ERR_TIMEOUT);
+                mbar_wait_bounded(bar, parity ^ 1);      // the copy may still be on its way
+            }
         }
         auto terms = [&](int s, float2 (&a)[kAt], float2 (&u)[kAt]) {
 #pragma unroll

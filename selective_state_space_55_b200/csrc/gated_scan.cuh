@@ -50,6 +50,8 @@ constexpr int kGatedBlock = 64;                             // steps per warp
 constexpr int kGatedWarps = 8;                              // blocks per segment, at most
 constexpr int kGatedChannels = 128;                         // per CTA, four per lane
 constexpr int kGatedThreads = kGatedWarps * 32;
+constexpr int kRowWarps = 8;                                // per pair of chains in (batch, dim, seqlen), at most
+constexpr int kRowThreads = kRowWarps * 32;
 constexpr int kGatedJoin = 24;                              // segments folded from one known state
 static_assert(kGatedJoin < 32, "one lane per map and one for the state");
 static_assert(kGatedBlock == MAMBA_GATED_CHECKPOINT_STEPS, "checkpoints are the states entering blocks");
@@ -747,12 +749,9 @@ __global__ void __launch_bounds__(kGatedThreads, 2)
 // Two neighbouring chains side by side, one per half of the packed arithmetic.
 
 // Compositions over a team of `width` lanes in scan order (kReverse: from the
-// team's last lane down): on return (A, H) is the map of every lane before this
-// one, (At, Ht) of the whole team.
+// team's last lane down): (A, H) becomes the map of the lanes up to this one.
 template <bool kReverse>
-__device__ __forceinline__ void team_scan(float2& A, float2& H, float2& At, float2& Ht, int lane, int width) {
-    const int rank = lane & (width - 1);
-    const int first = kReverse ? width - 1 : 0;
+__device__ __forceinline__ void team_scan(float2& A, float2& H, int rank, int width) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         if (o >= width) break;
@@ -763,68 +762,93 @@ __device__ __forceinline__ void team_scan(float2& A, float2& H, float2& At, floa
             A = __fmul2_rn(A, Ao);
         }
     }
-    At = shfl2(A, width - 1 - first, width);
-    Ht = shfl2(H, width - 1 - first, width);
-    const float2 Ae = kReverse ? shfl_down2(A, 1, width) : shfl_up2(A, 1, width);
-    const float2 He = kReverse ? shfl_down2(H, 1, width) : shfl_up2(H, 1, width);
-    A = rank == first ? make_float2(1.0f, 1.0f) : Ae;
-    H = rank == first ? make_float2(0.0f, 0.0f) : He;
 }
 
-// Composes the maps of the kWarps warps that share a pair of chains: (A, H)
-// gains the maps of the warps before this one in scan order, (At, Ht) becomes
-// the map of the whole tile.  `buf` holds one entry per warp of the CTA; two of
-// them are used in turn.
-template <int kWarps, bool kReverse>
-__device__ __forceinline__ void join_warps(float2& A, float2& H, float2& At, float2& Ht, float4* buf,
-                                           int warp, int lane) {
-    if constexpr (kWarps > 1) {
-        if (lane == 0) buf[warp] = make_float4(At.x, At.y, Ht.x, Ht.y);
-        __syncthreads();
-        const int base = warp / kWarps * kWarps, rank = warp - base;
-        float2 mA = make_float2(1.0f, 1.0f), mH = make_float2(0.0f, 0.0f), aA = mA, aH = mH;
+// The state entering this warp's part of a tile: folds the maps of the `warps`
+// warps that share a pair of chains, `maps` being the first one's.  carry, the
+// state entering the tile, becomes the one that leaves it.
+template <bool kReverse>
+__device__ __forceinline__ float2 fold_warps(float2& carry, const float4* maps, int rank, int warps) {
+    float2 h = carry;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            const int v = kReverse ? kWarps - 1 - k : k;
-            if (v == rank) {
-                mA = aA;
-                mH = aH;
-            }
-            const float4 m = buf[base + v];
-            aH = __ffma2_rn(make_float2(m.x, m.y), aH, make_float2(m.z, m.w));
-            aA = __fmul2_rn(aA, make_float2(m.x, m.y));
-        }
-        H = __ffma2_rn(A, mH, H);
-        A = __fmul2_rn(A, mA);
-        At = aA;
-        Ht = aH;
+    for (int k = 0; k < kRowWarps; ++k) {
+        if (k == warps) break;
+        const int v = kReverse ? warps - 1 - k : k;
+        if (v == rank) h = carry;
+        const float4 m = maps[v];
+        carry = __ffma2_rn(make_float2(m.x, m.y), carry, make_float2(m.z, m.w));
     }
+    return h;
 }
 
-// A lane's place: kWarps warps per pair of chains; with one, `width` lanes per pair.
-struct GatedRow {
-    int64_t chain, b, d;
-    int n, hi, shift;                       // steps of the sequence, of the tensor; first step of this
-    bool live;                              // lane in tile 0
+// The state entering a lane, from its inclusive map and the state h entering its
+// warp (team); `leaving`, if asked for, becomes the state behind the team.
+template <bool kReverse, bool kLeaving>
+__device__ __forceinline__ float2 enter_lane(float2 A, float2 H, float2 h, float2* leaving, int rank, int width) {
+    const float2 mine = __ffma2_rn(A, h, H);
+    if constexpr (kLeaving) *leaving = shfl2(mine, kReverse ? 0 : width - 1, width);
+    const float2 before = kReverse ? shfl_down2(mine, 1, width) : shfl_up2(mine, 1, width);
+    return rank == (kReverse ? width - 1 : 0) ? h : before;
+}
+
+// Pairs of neighbouring channels of a batch row (an odd one's last has one chain),
+// in the order in which a team takes them.  Fewer than 2^31 chains.
+struct PairWalk {
+    int64_t pair, pairs;
+    int b, half;                            // batch row, pair within it
+    int halves, step_b, step_half;
+    __device__ __forceinline__ PairWalk(const GatedParams& p, int64_t first, int64_t stride) {
+        halves = (int)((p.dim + 1) / 2);
+        pairs = p.batch * halves;
+        pair = first;
+        b = (int)(first / halves);
+        half = (int)(first - (int64_t)b * halves);
+        step_b = (int)(stride / halves);
+        step_half = (int)(stride - (int64_t)step_b * halves);
+        stride_ = stride;
+    }
+    __device__ __forceinline__ void advance() {
+        pair += stride_;
+        b += step_b;
+        half += step_half;
+        if (half >= halves) {
+            half -= halves;
+            ++b;
+        }
+    }
+    int64_t stride_;
 };
 
+// A lane's pair of chains.
 template <typename IoT>
-__device__ __forceinline__ GatedRow gated_row(const GatedParams& p, int64_t chain, int offset) {
-    GatedRow r;
-    r.live = chain < p.chains;
-    r.chain = r.live ? chain : p.chains - 1;
-    r.b = r.chain / p.dim;
-    r.d = r.chain - r.b * p.dim;
-    r.n = r.live ? (int)gated_length(p, r.b) : 0;
-    r.hi = r.live ? (int)p.seqlen : 0;
-    r.shift = offset - row_phase(static_cast<const IoT*>(p.gate) + r.b * p.gate_s.batch + r.d * p.gate_s.row);
-    return r;
-}
-
-template <typename IoT>
-__device__ __forceinline__ const IoT* row_of(const void* base, const GatedStrides& s, const GatedRow& r) {
-    return static_cast<const IoT*>(base) + r.b * s.batch + r.d * s.row;
-}
+struct GatedRows {
+    int b, d;                               // of the first; the second is channel d + 1
+    bool live0, live1;
+    int shift0, shift1;                     // first step of this lane in tile 0
+    __device__ __forceinline__ GatedRows(const GatedParams& p, const PairWalk& at, int offset) {
+        live0 = at.pair < at.pairs;
+        b = live0 ? at.b : 0;
+        d = live0 ? 2 * at.half : 0;
+        live1 = live0 && d + 1 < (int)p.dim;
+        shift0 = offset - row_phase(row0(p.gate, p.gate_s));
+        shift1 = offset - row_phase(row1(p.gate, p.gate_s));
+    }
+    __device__ __forceinline__ IoT* row0(const void* base, const GatedStrides& s) const {
+        return const_cast<IoT*>(static_cast<const IoT*>(base)) + b * s.batch + d * s.row;
+    }
+    __device__ __forceinline__ IoT* row1(const void* base, const GatedStrides& s) const {
+        return row0(base, s) + (live1 ? s.row : 0);
+    }
+    // one value per channel, per chain
+    __device__ __forceinline__ float2 pick(const float* v, int64_t i) const {
+        return v != nullptr ? make_float2(v[i], v[i + (live1 ? 1 : 0)]) : make_float2(0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void put(float* v, int64_t i, float2 x) const {
+        if (v == nullptr) return;
+        if (live0) v[i] = x.x;
+        if (live1) v[i + 1] = x.y;
+    }
+};
 
 // The bytes between a tensor's first and last element, (batch, dim) rows of seqlen.
 template <typename IoT>
@@ -833,42 +857,13 @@ __device__ __forceinline__ Span gated_span(const GatedParams& p, const void* bas
     return {b, b + ((p.batch - 1) * s.batch + (p.dim - 1) * s.row + p.seqlen) * (int64_t)sizeof(IoT)};
 }
 
-template <int kWarps, typename IoT>
-struct GatedRows {
-    int step, offset;                       // steps per tile; this lane's place in it
-    GatedRow r0, r1;
-    __device__ __forceinline__ GatedRows(const GatedParams& p, int warp, int lane, int width) {
-        int64_t pair;
-        if (kWarps > 1) {
-            pair = (int64_t)blockIdx.x * (kGatedWarps / kWarps) + warp / kWarps;
-            offset = (warp % kWarps) * kWarpSteps + lane * kLaneSteps;
-            step = kWarps * kWarpSteps;
-        } else {
-            pair = ((int64_t)blockIdx.x * kGatedWarps + warp) * (32 / width) + lane / width;
-            offset = (lane & (width - 1)) * kLaneSteps;
-            step = width * kLaneSteps;
-        }
-        r0 = gated_row<IoT>(p, 2 * pair, offset);
-        r1 = gated_row<IoT>(p, 2 * pair + 1, offset);
-    }
-    __device__ __forceinline__ float2 pick(const float* v, int64_t i0, int64_t i1) const {
-        return v != nullptr ? make_float2(v[i0], v[i1]) : make_float2(0.0f, 0.0f);
-    }
-    // one value per chain
-    __device__ __forceinline__ void put(float* v, float2 x) const {
-        if (v == nullptr || offset != 0) return;
-        if (r0.live) v[r0.chain] = x.x;
-        if (r1.live) v[r1.chain] = x.y;
-    }
-};
-
 // Gains of a lane's eight steps; steps outside a sequence pass the state on.
 template <bool kLog>
-__device__ __forceinline__ void row_gains(float2 (&a)[8], float2 (&g)[8], float2 bias2, int t0, int n0, int t1,
-                                          int n1) {
+__device__ __forceinline__ void row_gains(float2 (&a)[8], float2 (&g)[8], float2 bias2, bool inside, int t0, int n0,
+                                          int t1, int n1) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) gated_gains2<kLog>(a[i], bias2, g[i], a[i]);
-    if (t0 < 0 || t1 < 0 || t0 + 8 > n0 || t1 + 8 > n1)
+    if (!inside)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (t0 + i < 0 || t0 + i >= n0) {
@@ -882,41 +877,61 @@ __device__ __forceinline__ void row_gains(float2 (&a)[8], float2 (&g)[8], float2
         }
 }
 
-// Two rows' eight steps of one tensor, asked for before any is unpacked: vectors
-// where they are aligned and inside the tensor, else (ok false) element by
-// element in fill().
-template <typename IoT>
-struct RowPair {
-    uint4 r0[sizeof(IoT) / 2], r1[sizeof(IoT) / 2];
-    bool ok0, ok1;
-    __device__ __forceinline__ void load(const IoT* p0, const IoT* p1, const Span& span) {
-        ok0 = (reinterpret_cast<uintptr_t>(p0) & 15) == 0 && span.holds(p0, 8 * (int)sizeof(IoT));
-        ok1 = (reinterpret_cast<uintptr_t>(p1) & 15) == 0 && span.holds(p1, 8 * (int)sizeof(IoT));
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(IoT) / 2; ++i) {
-            r0[i] = ok0 ? reinterpret_cast<const uint4*>(p0)[i] : make_uint4(0, 0, 0, 0);
-            r1[i] = ok1 ? reinterpret_cast<const uint4*>(p1)[i] : make_uint4(0, 0, 0, 0);
-        }
+// A lane's eight steps of two rows, for kTensors tensors, come through its own slots
+// in shared memory (16 bytes per thread side by side): the next tile is on its way
+// while this one is worked on.  What cannot be copied as aligned vectors inside the
+// tensor is read element by element when its turn comes; a bit of `ok` per vector
+// says which was copied.
+template <typename IoT, int kTensors>
+struct RowStages {
+    static constexpr int kVecs = (int)sizeof(IoT) / 2;
+    static constexpr int kStages = 2;
+    static constexpr int kBytesPerThread = kStages * kTensors * 2 * kVecs * 16;
+    uint4* own;
+    __device__ __forceinline__ explicit RowStages(unsigned char* smem) : own(reinterpret_cast<uint4*>(smem) + threadIdx.x) {}
+    __device__ __forceinline__ uint4* slot(int stage, int tensor, int row) const {
+        return own + ((stage * kTensors + tensor) * 2 + row) * kVecs * blockDim.x;
     }
-    __device__ __forceinline__ void get(float2 (&v)[8]) const {
+    // Both rows' vectors of a tensor; in0, in1: is the vector inside its row?
+    __device__ __forceinline__ uint32_t copy(int stage, int tensor, const IoT* q0, bool in0, const IoT* q1, bool in1,
+                                             const Span& span) const {
+        return copy_row(stage, tensor, 0, q0, in0, span) | copy_row(stage, tensor, 1, q1, in1, span);
+    }
+    __device__ __forceinline__ uint32_t copy_row(int stage, int tensor, int row, const IoT* q, bool inside,
+                                                 const Span& span) const {
+        if (!inside) inside = span.holds(q, 8 * (int)sizeof(IoT));
+        if ((reinterpret_cast<uintptr_t>(q) & 15) != 0 || !inside) return 0u;
+        uint4* dst = slot(stage, tensor, row);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) copy_async16(smem_u32(dst + i * blockDim.x), reinterpret_cast<const uint4*>(q) + i);
+        return 1u << (2 * tensor + row);
+    }
+    __device__ __forceinline__ void get(int stage, int tensor, float2 (&v)[8]) const {
+        uint4 raw0[kVecs], raw1[kVecs];
         float a[8], b[8];
-        unpack_steps<IoT>(r0, a);
-        unpack_steps<IoT>(r1, b);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            raw0[i] = slot(stage, tensor, 0)[i * blockDim.x];
+            raw1[i] = slot(stage, tensor, 1)[i * blockDim.x];
+        }
+        unpack_steps<IoT>(raw0, a);
+        unpack_steps<IoT>(raw1, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = make_float2(a[i], b[i]);
     }
     // Steps outside [0, n) become 0; those that no vector brought are read.
-    __device__ __forceinline__ void fill(float2 (&v)[8], const IoT* p0, int t0, int n0, const IoT* p1, int t1, int n1) const {
+    __device__ __forceinline__ static void fill(float2 (&v)[8], uint32_t ok, int tensor, const IoT* p0, int t0, int n0,
+                                                const IoT* p1, int t1, int n1) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (t0 + i < 0 || t0 + i >= n0) v[i].x = 0.0f;
             if (t1 + i < 0 || t1 + i >= n1) v[i].y = 0.0f;
         }
-        if (!ok0)
+        if (!(ok >> (2 * tensor) & 1u))
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (t0 + i >= 0 && t0 + i < n0) v[i].x = DType<IoT>::load(p0 + i);
-        if (!ok1)
+        if (!(ok >> (2 * tensor + 1) & 1u))
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (t1 + i >= 0 && t1 + i < n1) v[i].y = DType<IoT>::load(p1 + i);
@@ -937,211 +952,264 @@ __device__ __forceinline__ void store_pair_rows(IoT* p0, IoT* p1, const float2 (
     store_eight(p1, b);
 }
 
-template <typename IoT, bool kLog, int kWarps>
-__global__ void __launch_bounds__(kGatedThreads)
-    gated_scan_rows_fwd_kernel(const __grid_constant__ GatedParams p, int width) {
-    __shared__ float4 buf[2][kGatedWarps];
+template <typename IoT, bool kLog, bool kMulti>
+__global__ void __launch_bounds__(kRowThreads, 3)
+    gated_scan_rows_fwd_kernel(const __grid_constant__ GatedParams p, int warps, int width_, int64_t blocks) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    __shared__ float4 buf[2][kRowWarps];
+    const RowStages<IoT, 2> ring(raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const GatedRows<kWarps, IoT> at(p, warp, lane, width);
-    const int tiles = (int)p.tiles;
-    const IoT *gate0 = row_of<IoT>(p.gate, p.gate_s, at.r0), *gate1 = row_of<IoT>(p.gate, p.gate_s, at.r1);
-    const IoT *x0 = row_of<IoT>(p.x, p.x_s, at.r0), *x1 = row_of<IoT>(p.x, p.x_s, at.r1);
+    const int width = kMulti ? 32 : width_;              // lanes of a pair in a warp
+    const int teams = (kMulti ? (int)(blockDim.x >> 5) / warps : (int)blockDim.x / width);
+    const int team = kMulti ? warp / warps : (int)threadIdx.x / width;
+    const int rank = kMulti ? warp - team * warps : 0, at_lane = lane & (width - 1);
+    const int offset = rank * kWarpSteps + at_lane * kLaneSteps;
+    const int tiles = (int)p.tiles, step = (kMulti ? warps : 1) * width * kLaneSteps, L = (int)p.seqlen;
     const Span gspan = gated_span<IoT>(p, p.gate, p.gate_s), xspan = gated_span<IoT>(p, p.x, p.x_s);
-    IoT* out0 = const_cast<IoT*>(row_of<IoT>(p.out, p.out_s, at.r0));
-    IoT* out1 = const_cast<IoT*>(row_of<IoT>(p.out, p.out_s, at.r1));
-    const float2 bias2 = __fmul2_rn(at.pick(p.bias, at.r0.d, at.r1.d), make_float2(kLog2e, kLog2e));
-    float2 carry = at.pick(p.h0, at.r0.chain, at.r1.chain);
-    for (int tile = 0; tile < tiles; ++tile) {
-        const int t0 = tile * at.step + at.r0.shift, t1 = tile * at.step + at.r1.shift;
-        float2 a[8], u[8], g[8];
-        RowPair<IoT> gr, xr;
-        gr.load(gate0 + t0, gate1 + t1, gspan);
-        xr.load(x0 + t0, x1 + t1, xspan);
-        // the whole warp inside both sequences, on vectors
-        const bool whole = __all_sync(0xffffffffu, t0 >= 0 && t1 >= 0 && t0 + 8 <= at.r0.n && t1 + 8 <= at.r1.n &&
-                                                       gr.ok0 && gr.ok1 && xr.ok0 && xr.ok1 && on16(out0 + t0) &&
-                                                       on16(out1 + t1));
-        gr.get(a);
-        xr.get(u);
-        if (!whole) {
-            gr.fill(a, gate0 + t0, t0, at.r0.n, gate1 + t1, t1, at.r1.n);
-            xr.fill(u, x0 + t0, t0, at.r0.n, x1 + t1, t1, at.r1.n);
-        }
-        row_gains<kLog>(a, g, bias2, t0, at.r0.n, t1, at.r1.n);
-        float2 A = make_float2(1.0f, 1.0f), H = make_float2(0.0f, 0.0f), At, Ht;
+    auto request = [&](const GatedRows<IoT>& at, int tile, int stage) {
+        const int t0 = tile * step + at.shift0, t1 = tile * step + at.shift1;
+        const bool in0 = t0 >= 0 && t0 + 8 <= L, in1 = t1 >= 0 && t1 + 8 <= L;
+        return ring.copy(stage, 0, at.row0(p.gate, p.gate_s) + t0, in0, at.row1(p.gate, p.gate_s) + t1, in1, gspan) |
+               ring.copy(stage, 1, at.row0(p.x, p.x_s) + t0, in0, at.row1(p.x, p.x_s) + t1, in1, xspan);
+    };
+    PairWalk walk(p, (int64_t)blockIdx.x * teams + team, (int64_t)gridDim.x * teams);
+    uint32_t ok_next = request(GatedRows<IoT>(p, walk, offset), 0, 0);
+    copy_async_commit();
+    int stage = 0;
+    for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+        const GatedRows<IoT> at(p, walk, offset);
+        const int n = (int)gated_length(p, at.b), n0 = at.live0 ? n : 0, n1 = at.live1 ? n : 0;
+        const int64_t chain = (int64_t)at.b * p.dim + at.d;
+        const float2 bias2 = __fmul2_rn(at.pick(p.bias, at.d), make_float2(kLog2e, kLog2e));
+        float2 carry = at.pick(p.h0, chain);
+        for (int tile = 0; tile < tiles; ++tile, stage ^= 1) {
+            const uint32_t ok = ok_next;
+            if (tile + 1 < tiles) {
+                ok_next = request(at, tile + 1, stage ^ 1);
+            } else if (block + gridDim.x < blocks) {
+                walk.advance();
+                ok_next = request(GatedRows<IoT>(p, walk, offset), 0, stage ^ 1);
+            }
+            copy_async_commit();
+            copy_async_wait<1>();
+            const int t0 = tile * step + at.shift0, t1 = tile * step + at.shift1;
+            IoT *out0 = at.row0(p.out, p.out_s), *out1 = at.row1(p.out, p.out_s);
+            float2 a[8], u[8], g[8];
+            // the whole warp inside both sequences, on vectors
+            const bool whole = __all_sync(0xffffffffu, t0 >= 0 && t1 >= 0 && t0 + 8 <= n0 && t1 + 8 <= n1 &&
+                                                           ok == 15u && on16(out0 + t0) && on16(out1 + t1));
+            ring.get(stage, 0, a);
+            ring.get(stage, 1, u);
+            if (!whole) {
+                ring.fill(a, ok, 0, at.row0(p.gate, p.gate_s) + t0, t0, n0, at.row1(p.gate, p.gate_s) + t1, t1, n1);
+                ring.fill(u, ok, 1, at.row0(p.x, p.x_s) + t0, t0, n0, at.row1(p.x, p.x_s) + t1, t1, n1);
+            }
+            row_gains<kLog>(a, g, bias2, whole, t0, n0, t1, n1);
+            float2 A = make_float2(1.0f, 1.0f), H = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (!kLog) u[i] = __fmul2_rn(g[i], u[i]);
-            H = __ffma2_rn(a[i], H, u[i]);
-            A = __fmul2_rn(A, a[i]);
-        }
-        team_scan<false>(A, H, At, Ht, lane, width);
-        join_warps<kWarps, false>(A, H, At, Ht, buf[tile & 1], warp, lane);
-        float2 h = __ffma2_rn(A, carry, H);
-        carry = __ffma2_rn(At, carry, Ht);
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (!kLog) u[i] = __fmul2_rn(g[i], u[i]);
+                H = i == 0 ? u[0] : __ffma2_rn(a[i], H, u[i]);
+                A = i == 0 ? a[0] : __fmul2_rn(A, a[i]);
+            }
+            team_scan<false>(A, H, at_lane, width);
+            float2 h;
+            if constexpr (kMulti) {
+                if (lane == 31) buf[stage][warp] = make_float4(A.x, A.y, H.x, H.y);
+                __syncthreads();
+                h = fold_warps<false>(carry, buf[stage] + warp - rank, rank, warps);
+                h = enter_lane<false, false>(A, H, h, nullptr, at_lane, width);
+            } else {
+                h = enter_lane<false, true>(A, H, carry, &carry, at_lane, width);
+            }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            h = __ffma2_rn(a[i], h, u[i]);
-            u[i] = h;
-        }
-        if (whole) {
-            store_pair_rows(out0 + t0, out1 + t1, u);
-            continue;
-        }
+            for (int i = 0; i < 8; ++i) {
+                h = __ffma2_rn(a[i], h, u[i]);
+                u[i] = h;
+            }
+            if (whole) {
+                store_pair_rows(out0 + t0, out1 + t1, u);
+                continue;
+            }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (t0 + i >= at.r0.n) u[i].x = 0.0f;
-            if (t1 + i >= at.r1.n) u[i].y = 0.0f;
+            for (int i = 0; i < 8; ++i) {
+                if (t0 + i >= n0) u[i].x = 0.0f;
+                if (t1 + i >= n1) u[i].y = 0.0f;
+            }
+            store_steps2(out0, t0, 0, at.live0 ? L : 0, out1, t1, 0, at.live1 ? L : 0, u);
         }
-        store_steps2(out0, t0, 0, at.r0.hi, out1, t1, 0, at.r1.hi, u);
+        if (offset == 0) at.put(p.last, chain, carry);
     }
-    at.put(p.last, carry);
 }
 
 // Backward: with more than one tile per chain, a first sweep keeps the states
 // entering the tiles; the second runs from the last tile to the first and reads
 // gate and x again (from L2 while the chains in flight fit there).
-template <typename IoT, bool kLog, int kWarps>
-__global__ void __launch_bounds__(kGatedThreads, 2)
-    gated_scan_rows_bwd_kernel(const __grid_constant__ GatedParams p, int width) {
-    __shared__ float4 buf[2][kGatedWarps];
-    __shared__ float4 back[2][kGatedWarps];
+template <typename IoT, bool kLog, bool kMulti>
+__global__ void __launch_bounds__(kRowThreads, 2)
+    gated_scan_rows_bwd_kernel(const __grid_constant__ GatedParams p, int warps, int width_, int64_t blocks) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    __shared__ float4 buf[2][kRowWarps], back[2][kRowWarps];
+    __shared__ float2 sums[kRowWarps];
+    const RowStages<IoT, 3> ring(raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float2 one = make_float2(1.0f, 1.0f), zero = make_float2(0.0f, 0.0f);
-    const GatedRows<kWarps, IoT> at(p, warp, lane, width);
-    const int tiles = (int)p.tiles;
-    const IoT *gate0 = row_of<IoT>(p.gate, p.gate_s, at.r0), *gate1 = row_of<IoT>(p.gate, p.gate_s, at.r1);
-    const IoT *x0 = row_of<IoT>(p.x, p.x_s, at.r0), *x1 = row_of<IoT>(p.x, p.x_s, at.r1);
-    const Span gspan = gated_span<IoT>(p, p.gate, p.gate_s), xspan = gated_span<IoT>(p, p.x, p.x_s);
-    const float2 bias2 = __fmul2_rn(at.pick(p.bias, at.r0.d, at.r1.d), make_float2(kLog2e, kLog2e));
-    float* states0 = p.chain_states + at.r0.chain * p.tiles;
-    float* states1 = p.chain_states + at.r1.chain * p.tiles;
-    float2 carry = at.pick(p.h0, at.r0.chain, at.r1.chain);
-    for (int tile = 0; tile + 1 < tiles; ++tile) {
-        const int t0 = tile * at.step + at.r0.shift, t1 = tile * at.step + at.r1.shift;
-        float2 a[8], x[8], g[8];
-        RowPair<IoT> gr, xr;
-        gr.load(gate0 + t0, gate1 + t1, gspan);
-        xr.load(x0 + t0, x1 + t1, xspan);
-        const bool whole = __all_sync(0xffffffffu, t0 >= 0 && t1 >= 0 && t0 + 8 <= at.r0.n && t1 + 8 <= at.r1.n &&
-                                                       gr.ok0 && gr.ok1 && xr.ok0 && xr.ok1);
-        gr.get(a);
-        xr.get(x);
-        if (!whole) {
-            gr.fill(a, gate0 + t0, t0, at.r0.n, gate1 + t1, t1, at.r1.n);
-            xr.fill(x, x0 + t0, t0, at.r0.n, x1 + t1, t1, at.r1.n);
-        }
-        row_gains<kLog>(a, g, bias2, t0, at.r0.n, t1, at.r1.n);
-        float2 A = one, H = zero, At, Ht;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            H = __ffma2_rn(a[i], H, kLog ? x[i] : __fmul2_rn(g[i], x[i]));
-            A = __fmul2_rn(A, a[i]);
-        }
-        team_scan<false>(A, H, At, Ht, lane, width);
-        join_warps<kWarps, false>(A, H, At, Ht, buf[tile & 1], warp, lane);
-        if (at.offset == 0) {
-            if (at.r0.live) states0[tile] = carry.x;
-            if (at.r1.live) states1[tile] = carry.y;
-        }
-        carry = __ffma2_rn(At, carry, Ht);
-    }
-    if (kWarps > 1) __syncthreads();
-    else __syncwarp();
-    const IoT *dout0 = row_of<IoT>(p.dout, p.out_s, at.r0), *dout1 = row_of<IoT>(p.dout, p.out_s, at.r1);
-    const Span dspan = gated_span<IoT>(p, p.dout, p.out_s);
-    IoT* dgate0 = const_cast<IoT*>(row_of<IoT>(p.dgate, p.dgate_s, at.r0));
-    IoT* dgate1 = const_cast<IoT*>(row_of<IoT>(p.dgate, p.dgate_s, at.r1));
-    IoT* dx0 = const_cast<IoT*>(row_of<IoT>(p.dx, p.dx_s, at.r0));
-    IoT* dx1 = const_cast<IoT*>(row_of<IoT>(p.dx, p.dx_s, at.r1));
-    float2 r_carry = at.pick(p.dlast, at.r0.chain, at.r1.chain);
-    float2 db = zero;
-    for (int tile = tiles - 1; tile >= 0; --tile) {
-        const int t0 = tile * at.step + at.r0.shift, t1 = tile * at.step + at.r1.shift;
-        float2 a[8], g[8], x[8], dd[8];
-        RowPair<IoT> gr, xr, dr;
-        gr.load(gate0 + t0, gate1 + t1, gspan);
-        xr.load(x0 + t0, x1 + t1, xspan);
-        dr.load(dout0 + t0, dout1 + t1, dspan);
-        const bool whole = __all_sync(0xffffffffu, t0 >= 0 && t1 >= 0 && t0 + 8 <= at.r0.n && t1 + 8 <= at.r1.n &&
-                                                       gr.ok0 && gr.ok1 && xr.ok0 && xr.ok1 && dr.ok0 && dr.ok1 &&
-                                                       on16(dgate0 + t0) && on16(dgate1 + t1) && on16(dx0 + t0) &&
-                                                       on16(dx1 + t1));
-        gr.get(a);
-        xr.get(x);
-        dr.get(dd);
-        if (!whole) {
-            gr.fill(a, gate0 + t0, t0, at.r0.n, gate1 + t1, t1, at.r1.n);
-            xr.fill(x, x0 + t0, t0, at.r0.n, x1 + t1, t1, at.r1.n);
-            dr.fill(dd, dout0 + t0, t0, at.r0.n, dout1 + t1, t1, at.r1.n);
-        }
-        if (tile + 1 < tiles) carry = make_float2(states0[tile], states1[tile]);
-        row_gains<kLog>(a, g, bias2, t0, at.r0.n, t1, at.r1.n);
-        float2 A = one, H = zero, At, Ht;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            H = __ffma2_rn(a[i], H, kLog ? x[i] : __fmul2_rn(g[i], x[i]));
-            A = __fmul2_rn(A, a[i]);
-        }
-        float2 B = A, R = zero, Bt, Rt;
-#pragma unroll
-        for (int i = 7; i >= 0; --i) R = __fmul2_rn(a[i], __fadd2_rn(dd[i], R));
-        team_scan<false>(A, H, At, Ht, lane, width);
-        team_scan<true>(B, R, Bt, Rt, lane, width);
-        join_warps<kWarps, false>(A, H, At, Ht, buf[tile & 1], warp, lane);
-        join_warps<kWarps, true>(B, R, Bt, Rt, back[tile & 1], warp, lane);
-        float2 h = __ffma2_rn(A, carry, H);
-        float2 r = __ffma2_rn(B, r_carry, R);
-        r_carry = __ffma2_rn(Bt, r_carry, Rt);
-        // x becomes what the decay's gradient multiplies: x_t - h_{t-1}, or h_{t-1}
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 u = kLog ? x[i] : __fmul2_rn(g[i], x[i]);
-            x[i] = kLog ? h : __ffma2_rn(h, make_float2(-1.0f, -1.0f), x[i]);
-            h = __ffma2_rn(a[i], h, u);
-        }
-#pragma unroll
-        for (int i = 7; i >= 0; --i) {
-            const float2 l = __fadd2_rn(dd[i], r);
-            r = __fmul2_rn(a[i], l);
-            dd[i] = __fmul2_rn(r, x[i]);
-            x[i] = l;
-            if constexpr (!kLog) {
-                dd[i] = __fmul2_rn(g[i], dd[i]);
-                x[i] = __fmul2_rn(g[i], l);
+    const int width = kMulti ? 32 : width_;              // lanes of a pair in a warp
+    const int teams = (kMulti ? (int)(blockDim.x >> 5) / warps : (int)blockDim.x / width);
+    const int team = kMulti ? warp / warps : (int)threadIdx.x / width;
+    const int rank = kMulti ? warp - team * warps : 0, at_lane = lane & (width - 1);
+    const int offset = rank * kWarpSteps + at_lane * kLaneSteps;
+    const int tiles = (int)p.tiles, step = (kMulti ? warps : 1) * width * kLaneSteps, L = (int)p.seqlen;
+    const Span gspan = gated_span<IoT>(p, p.gate, p.gate_s), xspan = gated_span<IoT>(p, p.x, p.x_s),
+               dspan = gated_span<IoT>(p, p.dout, p.out_s);
+    // a pair's items: tiles 0 .. tiles - 2 of the first sweep, then all backwards
+    const int64_t items = 2 * (int64_t)tiles - 1;
+    auto request = [&](const GatedRows<IoT>& at, int64_t item, int stage) {
+        const bool sweep = item < tiles - 1;
+        const int tile = (int)(sweep ? item : items - 1 - item);
+        const int t0 = tile * step + at.shift0, t1 = tile * step + at.shift1;
+        const bool in0 = t0 >= 0 && t0 + 8 <= L, in1 = t1 >= 0 && t1 + 8 <= L;
+        uint32_t ok =
+            ring.copy(stage, 0, at.row0(p.gate, p.gate_s) + t0, in0, at.row1(p.gate, p.gate_s) + t1, in1, gspan) |
+            ring.copy(stage, 1, at.row0(p.x, p.x_s) + t0, in0, at.row1(p.x, p.x_s) + t1, in1, xspan);
+        if (!sweep)
+            ok |= ring.copy(stage, 2, at.row0(p.dout, p.out_s) + t0, in0, at.row1(p.dout, p.out_s) + t1, in1, dspan);
+        return ok;
+    };
+    PairWalk walk(p, (int64_t)blockIdx.x * teams + team, (int64_t)gridDim.x * teams);
+    uint32_t ok_next = request(GatedRows<IoT>(p, walk, offset), 0, 0);
+    copy_async_commit();
+    int stage = 0;
+    for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+        const GatedRows<IoT> at(p, walk, offset);
+        const int n = (int)gated_length(p, at.b), n0 = at.live0 ? n : 0, n1 = at.live1 ? n : 0;
+        const int64_t chain = (int64_t)at.b * p.dim + at.d;
+        const float2 bias2 = __fmul2_rn(at.pick(p.bias, at.d), make_float2(kLog2e, kLog2e));
+        float2 carry = at.pick(p.h0, chain), r_carry = at.pick(p.dlast, chain);
+        float2 db = zero;
+        float* states0 = p.chain_states + chain * p.tiles;
+        float* states1 = states0 + (at.live1 ? p.tiles : 0);
+        for (int64_t item = 0; item < items; ++item, stage ^= 1) {
+            const bool sweep = item < tiles - 1;
+            const int tile = (int)(sweep ? item : items - 1 - item);
+            const uint32_t ok = ok_next;
+            if (item + 1 < items) {
+                ok_next = request(at, item + 1, stage ^ 1);
+            } else if (block + gridDim.x < blocks) {
+                walk.advance();
+                ok_next = request(GatedRows<IoT>(p, walk, offset), 0, stage ^ 1);
             }
-        }
-        if (t0 < 0 || t1 < 0 || t0 + 8 > at.r0.n || t1 + 8 > at.r1.n)
+            copy_async_commit();
+            copy_async_wait<1>();
+            const int t0 = tile * step + at.shift0, t1 = tile * step + at.shift1;
+            const bool inside = __all_sync(0xffffffffu, t0 >= 0 && t1 >= 0 && t0 + 8 <= n0 && t1 + 8 <= n1 &&
+                                                            ok == (sweep ? 15u : 63u));
+            float2 a[8], g[8], x[8];
+            ring.get(stage, 0, a);
+            ring.get(stage, 1, x);
+            if (!inside) {
+                ring.fill(a, ok, 0, at.row0(p.gate, p.gate_s) + t0, t0, n0, at.row1(p.gate, p.gate_s) + t1, t1, n1);
+                ring.fill(x, ok, 1, at.row0(p.x, p.x_s) + t0, t0, n0, at.row1(p.x, p.x_s) + t1, t1, n1);
+            }
+            row_gains<kLog>(a, g, bias2, inside, t0, n0, t1, n1);
+            float2 A = one, H = zero;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (t0 + i < 0 || t0 + i >= at.r0.n) dd[i].x = x[i].x = 0.0f;
-                if (t1 + i < 0 || t1 + i >= at.r1.n) dd[i].y = x[i].y = 0.0f;
+                const float2 u = kLog ? x[i] : __fmul2_rn(g[i], x[i]);
+                H = i == 0 ? u : __ffma2_rn(a[i], H, u);
+                A = i == 0 ? a[0] : __fmul2_rn(A, a[i]);
+            }
+            float2 B = A;
+            team_scan<false>(A, H, at_lane, width);
+            if (sweep) {
+                const float2 entering = carry;
+                if constexpr (kMulti) {
+                    if (lane == 31) buf[stage][warp] = make_float4(A.x, A.y, H.x, H.y);
+                    __syncthreads();
+                    fold_warps<false>(carry, buf[stage] + warp - rank, rank, warps);
+                } else {
+                    enter_lane<false, true>(A, H, carry, &carry, at_lane, width);
+                }
+                if (offset == 0) {
+                    if (at.live0) states0[tile] = entering.x;
+                    if (at.live1) states1[tile] = entering.y;
+                }
+                continue;
+            }
+            float2 dd[8];
+            ring.get(stage, 2, dd);
+            if (!inside)
+                ring.fill(dd, ok, 2, at.row0(p.dout, p.out_s) + t0, t0, n0, at.row1(p.dout, p.out_s) + t1, t1, n1);
+            float2 R = zero;
+#pragma unroll
+            for (int i = 7; i >= 0; --i) R = __fmul2_rn(a[i], i == 7 ? dd[7] : __fadd2_rn(dd[i], R));
+            team_scan<true>(B, R, at_lane, width);
+            float2 h, r;
+            if constexpr (kMulti) {
+                if (lane == 31) buf[stage][warp] = make_float4(A.x, A.y, H.x, H.y);
+                if (lane == 0) back[stage][warp] = make_float4(B.x, B.y, R.x, R.y);
+                __syncthreads();                 // also orders the first sweep's states before the reads below
+                if (tile + 1 < tiles) carry = make_float2(states0[tile], states1[tile]);
+                h = fold_warps<false>(carry, buf[stage] + warp - rank, rank, warps);
+                r = fold_warps<true>(r_carry, back[stage] + warp - rank, rank, warps);
+                h = enter_lane<false, false>(A, H, h, nullptr, at_lane, width);
+                r = enter_lane<true, false>(B, R, r, nullptr, at_lane, width);
+            } else {
+                __syncwarp();
+                if (tile + 1 < tiles) carry = make_float2(states0[tile], states1[tile]);
+                h = enter_lane<false, false>(A, H, carry, nullptr, at_lane, width);
+                r = enter_lane<true, true>(B, R, r_carry, &r_carry, at_lane, width);
+            }
+            // x becomes what the decay's gradient multiplies: x_t - h_{t-1}, or h_{t-1}
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 u = kLog ? x[i] : __fmul2_rn(g[i], x[i]);
+                x[i] = kLog ? h : __ffma2_rn(h, make_float2(-1.0f, -1.0f), x[i]);
+                h = __ffma2_rn(a[i], h, u);
             }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) db = __fadd2_rn(db, dd[i]);
-        if (whole) {
-            store_pair_rows(dgate0 + t0, dgate1 + t1, dd);
-            store_pair_rows(dx0 + t0, dx1 + t1, x);
-        } else {
-            store_steps2(dgate0, t0, 0, at.r0.hi, dgate1, t1, 0, at.r1.hi, dd);
-            store_steps2(dx0, t0, 0, at.r0.hi, dx1, t1, 0, at.r1.hi, x);
-        }
-    }
-    at.put(p.dh0, r_carry);
-    if (p.bias_partial != nullptr) {
-        for (int o = width / 2; o > 0; o >>= 1)
-            db = __fadd2_rn(db, make_float2(__shfl_xor_sync(0xffffffffu, db.x, o, width),
-                                            __shfl_xor_sync(0xffffffffu, db.y, o, width)));
-        if constexpr (kWarps > 1) {
-            __syncthreads();
-            if (lane == 0) buf[0][warp] = make_float4(db.x, db.y, 0.0f, 0.0f);
-            __syncthreads();
-            db = zero;
-            const int base = warp / kWarps * kWarps;
+            for (int i = 7; i >= 0; --i) {
+                const float2 l = __fadd2_rn(dd[i], r);
+                r = __fmul2_rn(a[i], l);
+                dd[i] = __fmul2_rn(r, x[i]);
+                x[i] = l;
+                if constexpr (!kLog) {
+                    dd[i] = __fmul2_rn(g[i], dd[i]);
+                    x[i] = __fmul2_rn(g[i], l);
+                }
+            }
+            if (!inside)
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) db = __fadd2_rn(db, make_float2(buf[0][base + v].x, buf[0][base + v].y));
+                for (int i = 0; i < 8; ++i) {
+                    if (t0 + i < 0 || t0 + i >= n0) dd[i].x = x[i].x = 0.0f;
+                    if (t1 + i < 0 || t1 + i >= n1) dd[i].y = x[i].y = 0.0f;
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) db = __fadd2_rn(db, dd[i]);
+            IoT *dgate0 = at.row0(p.dgate, p.dgate_s), *dgate1 = at.row1(p.dgate, p.dgate_s);
+            IoT *dx0 = at.row0(p.dx, p.dx_s), *dx1 = at.row1(p.dx, p.dx_s);
+            if (__all_sync(0xffffffffu, inside && on16(dgate0 + t0) && on16(dgate1 + t1) && on16(dx0 + t0) && on16(dx1 + t1))) {
+                store_pair_rows(dgate0 + t0, dgate1 + t1, dd);
+                store_pair_rows(dx0 + t0, dx1 + t1, x);
+            } else {
+                const int hi0 = at.live0 ? L : 0, hi1 = at.live1 ? L : 0;
+                store_steps2(dgate0, t0, 0, hi0, dgate1, t1, 0, hi1, dd);
+                store_steps2(dx0, t0, 0, hi0, dx1, t1, 0, hi1, x);
+            }
         }
-        at.put(p.bias_partial, db);
+        if (offset == 0) at.put(p.dh0, chain, r_carry);
+        if (p.bias_partial != nullptr) {
+            for (int o = width / 2; o > 0; o >>= 1)
+                db = __fadd2_rn(db, make_float2(__shfl_xor_sync(0xffffffffu, db.x, o, width),
+                                                __shfl_xor_sync(0xffffffffu, db.y, o, width)));
+            if constexpr (kMulti) {
+                if (lane == 0) sums[warp] = db;
+                __syncthreads();                 // the next writes follow another tile's barrier
+                db = zero;
+                for (int v = 0; v < warps; ++v) db = __fadd2_rn(db, sums[warp - rank + v]);
+            }
+            if (offset == 0) at.put(p.bias_partial, chain, db);
+        }
     }
 }
 
