@@ -287,6 +287,7 @@ struct GatedLayout {           // offsets in the workspace, bytes
 // 128 164 / 131, 192 178 / 186, 256 180 / 238.  fp32, L 4096: forward 128 115 / 96, 192
 // 125 / 135; backward 192 264 / 266.
 constexpr int64_t kChainMinGroups = 192, kChainMinGroupsBf16Forward = 320;
+constexpr int64_t kRowResident = 20 * 148;       // warps along time that occupy a B200
 constexpr int64_t kChainResident = 2 * 148;      // CTAs that a B200 holds
 
 // One segment per chain needs no look-back: no tickets, flags or maps.
@@ -347,7 +348,17 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
         // Lanes take 8 steps each; the row's start may lie up to phase_max steps into its tile.
         const int64_t span = L + phase_max, units = (span + kWarpSteps - 1) / kWarpSteps;
         if (chains >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
-        w->tiles = (units + kRowWarps - 1) / kRowWarps;
+        // Backward: as few tiles as possible, a second one costs a sweep.  Forward: one
+        // warp per pair of chains where pairs are plentiful (tiles hand a state on for
+        // less than warps do), more where they would not fill the GPU.  bf16, us with
+        // at most 1 / 2 / 4 / 8 warps: 16384 pairs of 2048 steps 98 / 96 / 104 / 121, of
+        // 2047 steps 127 / 147 / 139 / 166, 768 pairs of 32768 steps 143 / 107 / 82 / 86.
+        int64_t most = kRowWarps;
+        if (!backward) {
+            const int64_t pairs = d->batch * ((d->dim + 1) / 2);
+            for (most = 1; most < kRowWarps && pairs * most < kRowResident;) most *= 2;
+        }
+        w->tiles = (units + most - 1) / most;
         w->warps = (int)((units + w->tiles - 1) / w->tiles);
         w->width = 32;
         if (units == 1)

@@ -39,7 +39,11 @@
 // Layout (batch, dim, seqlen): a lane takes 8 consecutive steps of two neighbouring
 // chains, the warp composes its lanes' maps by shuffles, and 1 to 8 warps share a
 // tile of a pair through shared memory.  Chains are plentiful here (one per channel
-// instead of one per 64), so a chain stays with its warps and nothing waits.
+// instead of one per 64), so a chain stays with its warps and nothing waits; the
+// warps walk pair after pair, the next tile on its way by cp.async.  Issue-bound
+// (the scan across lanes and the addresses of every tile, beside the steps'
+// arithmetic): 8 x 4096 x 2048 bf16 forward 98 us, 63 % of the copy rate, backward
+// 227 us, 45 %.
 #pragma once
 
 #include "row_vectors.cuh"
@@ -955,7 +959,7 @@ __device__ __forceinline__ void store_pair_rows(IoT* p0, IoT* p1, const float2 (
 template <typename IoT, bool kLog, bool kMulti>
 __global__ void __launch_bounds__(kRowThreads, 3)
     gated_scan_rows_fwd_kernel(const __grid_constant__ GatedParams p, int warps, int width_, int64_t blocks) {
-    extern __shared__ __align__(16) unsigned char raw[];
+    extern __shared__ __align__(128) unsigned char raw[];
     __shared__ float4 buf[2][kRowWarps];
     const RowStages<IoT, 2> ring(raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1048,7 +1052,7 @@ __global__ void __launch_bounds__(kRowThreads, 3)
 template <typename IoT, bool kLog, bool kMulti>
 __global__ void __launch_bounds__(kRowThreads, 2)
     gated_scan_rows_bwd_kernel(const __grid_constant__ GatedParams p, int warps, int width_, int64_t blocks) {
-    extern __shared__ __align__(16) unsigned char raw[];
+    extern __shared__ __align__(128) unsigned char raw[];
     __shared__ float4 buf[2][kRowWarps], back[2][kRowWarps];
     __shared__ float2 sums[kRowWarps];
     const RowStages<IoT, 3> ring(raw);

@@ -342,11 +342,19 @@ def test_withheld_handoff_is_reported():
     assert_close("out", ops.gated_scan_fwd(**v, layout="bld"), *want["out"])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_plentiful_chains(dtype):
+    """(batch, dim, seqlen) with so many pairs of chains that one warp walks a pair's three
+    tiles forward; an odd dim leaves pairs with one chain."""
+    v, back = make(2, 2961, 701, "bdl", dtype, False, seed=17)
+    check(v, back, "bdl", False)
+
+
 @pytest.mark.parametrize("log_decay", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("batch,dim,L", [(1, 64, 7000), (2, 200, 513), (3, 72, 257), (1, 1536, 300), (5, 16, 31)])
 def test_few_chains(batch, dim, L, dtype, log_decay):
-    """Fewer than 128 groups, rows on 16-byte boundaries: segments of a chain kept on chip
+    """Too few groups for a CTA each, rows on 16-byte boundaries: segments of a chain kept on chip
     while they are joined; 7000 steps are more segments than one join group holds."""
     v, back = make(batch, dim, L, "bld", dtype, log_decay, seed=L + dim)
     check(v, back, "bld", log_decay)
