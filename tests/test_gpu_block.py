@@ -109,3 +109,55 @@ def test_prefill_then_tokens():
         outs.append((ops.gated_state_update(state, proj[:, :D], v, c["gate_b"]) @ c["w_out"])[:, None])
     close("out", torch.cat(outs, 1), out)
     close("state", state, last)
+
+
+def test_refusals():
+    """What the operators do not take is refused before anything is launched."""
+    f32 = torch.zeros(4, 6, 64, device=DEV)
+    bf = f32.bfloat16()
+    row, state = f32[0, 0], torch.zeros(4, 64, device=DEV)
+    stats = torch.ones(4, 6, device=DEV)
+    taps = torch.zeros(6, 4, device=DEV)
+    bad = [
+        lambda: ops.layer_norm_fwd(f32.cpu()),
+        lambda: ops.layer_norm_fwd(f32.half()),
+        lambda: ops.layer_norm_fwd(row.expand(6, 64)),                      # rows that overlap
+        lambda: ops.layer_norm_fwd(f32.transpose(1, 2)),                    # last dimension not contiguous
+        lambda: ops.layer_norm_fwd(f32, weight=row.bfloat16()),
+        lambda: ops.layer_norm_fwd(f32, weight=row[:63]),
+        lambda: ops.layer_norm_fwd(f32, residual=bf),                       # fp32 rows, bf16 residual
+        lambda: ops.layer_norm_fwd(f32, eps=-1.0),
+        lambda: ops.layer_norm_fwd(f32, residual=f32.clone(), residual_out=f32),
+        lambda: ops.layer_norm_bwd(f32, f32, stats),                        # mean missing
+        lambda: ops.layer_norm_bwd(f32, f32, stats[:3], mean=stats),
+        lambda: ops.layer_norm_bwd(bf, f32, stats, mean=stats, dresidual_out=bf),
+        lambda: ops.layer_norm_bwd(f32, f32, stats, mean=stats, weight=row,
+                                   workspace=torch.empty(16, dtype=torch.uint8, device=DEV)),
+        lambda: ops.gated_scan_fwd(f32, bf),
+        lambda: ops.gated_scan_fwd(f32, f32[:, :5]),
+        lambda: ops.gated_scan_fwd(f32, f32, layout="dbl"),
+        lambda: ops.gated_scan_fwd(f32[0], f32[0]),
+        lambda: ops.gated_scan_fwd(f32, f32, out=f32),
+        lambda: ops.gated_scan_fwd(f32, f32[0].expand(4, 6, 64)),           # one batch row for all
+        lambda: ops.gated_scan_fwd(f32, f32, out=f32[:1].clone().expand(4, 6, 64)),
+        lambda: ops.gated_scan_fwd(f32, f32, return_checkpoints=True),      # layout "bdl"
+        lambda: ops.gated_scan_fwd(f32, f32, seqlens=torch.ones(4, dtype=torch.int64, device=DEV)),
+        lambda: ops.gated_scan_fwd(f32, f32, flags=1 << 20),
+        lambda: ops.gated_scan_bwd(f32, f32, f32.clone(), dx=f32),
+        lambda: ops.gated_scan_bwd(f32, f32, f32.clone(), checkpoints=state),
+        lambda: ops.gated_state_update(state.bfloat16(), bf[:, 0], bf[:, 0]),
+        lambda: ops.gated_state_update(state[:, :63], f32[:, 0], f32[:, 0]),
+        lambda: ops.gated_state_update(state, f32[:, 0], bf[:, 0]),
+        lambda: ops.causal_conv1d_bwd(f32, taps, bf),
+        lambda: ops.causal_conv1d_bwd(f32, taps.new_zeros(6, 5), f32.clone()),
+        lambda: ops.causal_conv1d_bwd(f32.transpose(1, 2), taps.new_zeros(64, 4), f32.transpose(1, 2)),
+        lambda: ops.causal_conv1d_bwd(f32, taps, f32[:, :5]),
+    ]
+    for i, call in enumerate(bad):
+        try:
+            call()
+        except (ValueError, RuntimeError):
+            continue
+        pytest.fail(f"call {i} was not refused")
+    torch.cuda.synchronize()
+    assert ops.device_status() == 0

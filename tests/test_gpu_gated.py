@@ -360,22 +360,25 @@ def test_few_chains(batch, dim, L, dtype, log_decay):
     check(v, back, "bld", log_decay)
 
 
-CHAINED = [(4, 2048, 1100), (2, 4160, 700), (130, 64, 70), (3, 2728, 130), (9, 1000, 600)]
+CHAINED = [(4, 2048, 1100), (2, 4160, 700), (130, 64, 70), (3, 2728, 130), (9, 1000, 600),
+           (10, 2048, 1100), (5, 4160, 700), (321, 64, 70), (8, 2728, 130), (21, 1000, 600)]
 
 
 @pytest.mark.parametrize("log_decay", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("batch,dim,L", CHAINED)
 def test_many_chains(batch, dim, L, dtype, log_decay):
-    """128 groups of 64 channels and more: stretches of a chain handed from CTA to CTA."""
+    """From 192 groups of 64 channels on (bf16 forward: 320) stretches of a chain are handed
+    from CTA to CTA; sizes on both sides of that."""
     v, back = make(batch, dim, L, "bld", dtype, log_decay, seed=L)
     check(v, back, "bld", log_decay)
 
 
 @pytest.mark.parametrize("checkpoints", ["given", "recomputed"])
 @pytest.mark.parametrize("L", [1, 63, 65, 577])
-def test_many_chains_padded(L, checkpoints):
-    v, back = make(10, 840, L, "bld", BF, False, seed=L, ragged=True)
+@pytest.mark.parametrize("batch", [10, 25])
+def test_many_chains_padded(L, checkpoints, batch):
+    v, back = make(batch, 840, L, "bld", BF, False, seed=L, ragged=True)
     outside = (torch.arange(L, device=DEV)[None] >= v["seqlens"][:, None])[:, :, None]
     for t, bad in ((v["gate"], float("nan")), (v["x"], float("inf")), (back["dout"], float("nan"))):
         t.copy_(torch.where(outside, torch.full_like(t, bad), t))
@@ -385,11 +388,12 @@ def test_many_chains_padded(L, checkpoints):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_many_chains_strided(dtype):
+@pytest.mark.parametrize("batch", [4, 11])
+def test_many_chains_strided(dtype, batch):
     """Halves of one tensor in and out, time-major memory, neighbours untouched."""
-    v, back = make(4, 2048, 140, "bld", dtype, False, seed=30)
+    v, back = make(batch, 2048, 140, "bld", dtype, False, seed=30)
     both = torch.cat([v["gate"], v["x"]], dim=-1)
-    dboth = torch.full((4, 140, 4096 + 16), 7.0, dtype=dtype, device=DEV)
+    dboth = torch.full((batch, 140, 4096 + 16), 7.0, dtype=dtype, device=DEV)
     v2 = dict(v, gate=both[..., :2048], x=both[..., 2048:])
     _, g = check(v2, back, "bld", False,
                  bwd_kw=dict(dgate=dboth[..., :2048], dx=dboth[..., 2056:4104]))
@@ -399,8 +403,9 @@ def test_many_chains_strided(dtype):
     check(v3, dict(back, dout=tm(back["dout"])), "bld", False, fwd_kw=dict(out=tm(torch.zeros_like(v["x"]))))
 
 
-def test_many_chains_repeat_bit_for_bit_and_replay():
-    v, back = make(3, 4096, 1300, "bld", BF, False, seed=31)
+@pytest.mark.parametrize("batch", [3, 5])
+def test_many_chains_repeat_bit_for_bit_and_replay(batch):
+    v, back = make(batch, 4096, 1300, "bld", BF, False, seed=31)
     run = lambda: (ops.gated_scan_fwd(**v, layout="bld"), ops.gated_scan_bwd(**v, **back, layout="bld"))  # noqa: E731
     o, g = run()
     torch.cuda.synchronize()
@@ -416,8 +421,9 @@ def test_many_chains_repeat_bit_for_bit_and_replay():
     assert ops.device_status() == 0
 
 
-def test_many_chains_state_in_place():
-    v, _ = make(4, 2048, 700, "bld", F32, False, seed=32)
+@pytest.mark.parametrize("batch", [4, 6])
+def test_many_chains_state_in_place(batch):
+    v, _ = make(batch, 2048, 700, "bld", F32, False, seed=32)
     want = ref.gated(**v, layout="bld")
     state = v["initial_state"].clone()
     out, _ = ops.gated_scan_fwd(v["gate"], v["x"], v["gate_bias"], initial_state=state, last_state=state, layout="bld")
@@ -425,8 +431,9 @@ def test_many_chains_state_in_place():
     assert_close("last", state, *want["last_state"])
 
 
-def test_many_chains_withheld_handoff_is_reported():
-    v, _ = make(4, 2048, 2000, "bld", BF, False, seed=33)
+@pytest.mark.parametrize("batch", [4, 10])
+def test_many_chains_withheld_handoff_is_reported(batch):
+    v, _ = make(batch, 2048, 2000, "bld", BF, False, seed=33)
     ops.device_status()
     ops.gated_scan_fwd(**v, layout="bld", flags=ops.MAMBA_FLAG_TEST_WITHHOLD_HANDOFF)
     assert ops.STATUS_NAMES[ops.device_status()] == "MAMBA_ERR_TIMEOUT"
@@ -441,3 +448,36 @@ def test_rows_layout_odd_chain_counts(batch, dim, L):
     """A pair of chains with a missing second one, and pairs across two batch rows."""
     v, back = make(batch, dim, L, "bdl", BF, False, seed=L + dim, ragged=batch > 1)
     check(v, back, "bdl", False)
+
+
+def test_distances_of_extent_one():
+    """A tensor's distance along an axis of one element says nothing."""
+    v, back = make(3, 64, 1, "bld", BF, False, seed=40)
+    odd = lambda t: torch.as_strided(t.clone(), t.shape, (64, 1, 1))  # noqa: E731
+    v2 = dict(v, gate=odd(v["gate"]), x=odd(v["x"]))
+    check(v2, back, "bld", False)
+    v, back = make(1, 64, 90, "bld", BF, False, seed=41)
+    odd = lambda t: torch.as_strided(t.clone(), t.shape, (1, 64, 1))  # noqa: E731
+    v2 = dict(v, gate=odd(v["gate"]), x=odd(v["x"]))
+    check(v2, back, "bld", False)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim,L", [(64, 90), (67, 90), (2048, 90), (67, 1300), (256, 1300), (1536, 1300)])
+def test_concurrent_streams(dim, L, dtype):
+    """Two calls at once on streams of their own, each with its own workspace."""
+    sides = [make(11, dim, L, "bld", dtype, False, seed=s) for s in (50, 51)]
+    streams = [torch.cuda.Stream() for _ in sides]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for (v, back), stream in zip(sides, streams):
+            with torch.cuda.stream(stream):
+                got.append((ops.gated_scan_fwd(**v, layout="bld"), ops.gated_scan_bwd(**v, **back, layout="bld")))
+    torch.cuda.synchronize()
+    for i, (out, g) in enumerate(got):
+        v, back = sides[i % 2]
+        want = ref.gated(**v, layout="bld", **back)
+        assert_close("out", out, *want["out"])
+        for k in g:
+            assert_close(k, g[k], *want[k])
