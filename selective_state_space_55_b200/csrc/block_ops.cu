@@ -59,21 +59,27 @@ struct NormPlan {
     int64_t slices;     // wide backward: row slices of the column sums
 };
 
-// Rows with a team each.  Few rows (fewer than two per SM) are spread over many
-// warps, one or two chunks of 8 elements per lane, for the shortest way through;
-// many rows take as many chunks per lane as waste the fewest lanes, the larger
-// number first (2560 columns: 5 chunks on 2 warps forward, 2 on 5 backward).
+// Rows with a team each.  bf16 with a residual, us:
+//  - few rows forward (fewer than two per SM): one or two chunks of 8 elements per
+//    lane on many warps, the shortest way through a row (200 x 2560: 8 against 27);
+//  - many rows forward: as many chunks per lane as waste the fewest lanes, the larger
+//    number first (32768 x 2560: 5 chunks on 2 warps 119, 2 on 5 warps 152; 768
+//    columns, 65536 rows: 3 on 1 warp 74, 2 on 2 warps 92);
+//  - backward: two chunks, whatever lanes that wastes, because fewer teams keep more
+//    column sums (32768 x 2560: 127 against 221 with one), but one chunk where rows x
+//    256-column units leave less than 176 per SM (1000 x 2560: 18 against 25, 2000: 25
+//    against 29, 4000: 39 against 35).
 NormPlan plan_norm(int64_t rows, int64_t dim, int sms, bool backward) {
     NormPlan n{};
     const int64_t units = (dim + 255) / 256;               // chunks of a whole warp
     const int most = backward || rows < 2 * (int64_t)sms ? kNormFewChunks : kNormFwdChunks;
+    const bool few = backward ? rows < 176 * (int64_t)sms / units : rows < 2 * (int64_t)sms;
     int64_t best = 0;
     for (int v = most; v >= 1; --v) {
         if (v == 7) continue;                               // not built
         const int64_t warps = (units + v - 1) / v;
         if (warps > (v <= kNormFewChunks ? kNormFewWarps : kNormCtaWarps)) continue;
-        const bool few = rows < 2 * (int64_t)sms;
-        // few rows: the smallest number that fits; backward: two, whatever lanes that wastes
+        // few rows: the smallest number that fits
         if (n.chunks == 0 || few || (!backward && warps * v < best)) {
             n.chunks = v;
             best = warps * v;
@@ -129,7 +135,8 @@ template <typename Kernel>
 cudaError_t launch_norm_kernel(Kernel kernel, const NormParams& prm, NormPlan& n, size_t fixed, size_t stage,
                                NormResident* resident, bool* attr_done, int dev, int sms, cudaStream_t stream) {
     // as many stages, two to four, as leave room for the CTAs that the registers
-    // allow (512 threads of 128)
+    // allow (512 threads of 128); with two, 32768 x 2560 bf16 backward takes 166 us
+    // instead of 127
     constexpr int most = 226 * 1024;             // beside the kernels' static part
     const size_t share = most / std::max(1, 512 / (n.warps * n.teams * 32));
     int stages = stage == 0 ? 0 : kNormStages;
@@ -315,7 +322,9 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
         }
         if (backward && recompute) w->enter = take((size_t)d->batch * w->blocks * d->dim * sizeof(float));
         if (backward) w->bias = take((size_t)d->batch * w->segments * d->dim * sizeof(float));
-        // Chained stretches: some 4 items per resident CTA, 8 tiles or more each.
+        // Chained stretches: some 4 items per resident CTA, 8 tiles or more each (bf16 8 x
+        // 2048 x 4096, us with 1 / 4 / 8: forward 104 / 94 / 96, backward 174 / 168 / 164;
+        // backward 8 x 4096 x 2048 178 / 180 / 184).
         w->chain_groups = d->batch * ((d->dim + kChainChannels - 1) / kChainChannels);
         const int64_t want = (4 * kChainResident + w->chain_groups - 1) / w->chain_groups;
         w->chain_stretches = std::max<int64_t>(1, std::min<int64_t>(want, w->blocks / 8));
@@ -667,15 +676,28 @@ cudaError_t copy_or_zero(float* dst, const float* src, size_t bytes, cudaStream_
 
 struct ConvBwdPlan { int64_t stretch_tiles, stretches; size_t bytes; };
 
-// A warp per pair of rows; rows are cut into stretches of whole tiles while
-// that leaves fewer than 48 warps per SM.
+// A warp per pair of rows, or several, each with a stretch of whole tiles: enough of
+// them to occupy the 16 warps that an SM holds.  A stretch costs about 4 tiles beside
+// its own (its sums, its ring's first fill), and a started last wave about half a wave.
+// bf16, us: 1 x 5120 x 2048 in 1 / 2 / 3 stretches 35 / 43 / 49; 1 x 1536 x 65536 in 2 /
+// 3 / 4 / 10 stretches 186 / 158 / 184 / 168.
 mamba_status_t plan_conv_bwd(const mamba_dims_t* d, int width, int sms, ConvBwdPlan* n) {
     const int64_t chains = d->batch * d->dim;
     const int es = dtype_bytes(d->io_dtype);
     const int64_t tiles = std::max<int64_t>(1, (d->seqlen + 16 / es - 1 + kWarpSteps - 1) / kWarpSteps);
     const int64_t pairs = (chains + 1) / 2;
-    const int64_t want = pairs > 0 ? ((int64_t)sms * 48 + pairs - 1) / pairs : 1;
-    n->stretches = std::max<int64_t>(1, std::min<int64_t>(tiles, want));
+    const double resident = 16.0 * sms;
+    const int64_t most = std::min<int64_t>(tiles, (int64_t)(4 * resident) / std::max<int64_t>(pairs, 1) + 1);
+    double best = 0;
+    n->stretches = 1;
+    for (int64_t s = 1; s <= std::min<int64_t>(most, 1024); ++s) {
+        const double waves = (double)s * pairs / resident;
+        const double cost = (waves <= 1 ? 1.0 : waves + 0.5) * (double)((tiles + s - 1) / s + 4);
+        if (s == 1 || cost < best) {
+            best = cost;
+            n->stretches = s;
+        }
+    }
     n->stretch_tiles = (tiles + n->stretches - 1) / n->stretches;
     n->stretches = (tiles + n->stretch_tiles - 1) / n->stretch_tiles;
     if (pairs * n->stretches / kConvBwdWarps >= kLimit31 - 1) return MAMBA_ERR_UNSUPPORTED;
