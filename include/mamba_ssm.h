@@ -509,7 +509,8 @@ MAMBA_API mamba_status_t mamba_causal_conv1d_update(void *conv_state, const void
  * dbias and dinitial_conv_state may be NULL (not computed).
  * dims->workspace: at least mamba_causal_conv1d_bwd_workspace_bytes(dims, width)
  * bytes, 256-byte aligned, not shared by calls that overlap on the GPU.  The
- * sums are added in a fixed order: results repeat bit for bit.
+ * sums are added in a fixed order: results repeat bit for bit.  seqlen up to
+ * 2^31 - 65536 (MAMBA_ERR_UNSUPPORTED otherwise).
  */
 MAMBA_API size_t mamba_causal_conv1d_bwd_workspace_bytes(const mamba_dims_t *dims, int width);
 
@@ -548,6 +549,8 @@ MAMBA_API mamba_status_t mamba_causal_conv1d_bwd(
  *
  * Arithmetic and states are fp32.  In the log-decay form a product of decays
  * over many steps must stay finite in fp32, which f_t <= 0 guarantees.
+ * seqlen up to 2^31 - 65536, and in the (batch, dim, seqlen) layout batch dim below
+ * 2^31 - 1 (MAMBA_ERR_UNSUPPORTED otherwise).
  */
 typedef struct {
     int64_t batch;   /* elements between batch rows */
@@ -578,6 +581,7 @@ typedef struct {
  * Forward.
  *   gate_bias        (dim,) fp32 or NULL;  initial_state (batch, dim) fp32 or NULL
  *   last_state       (batch, dim) fp32 or NULL; may be the initial_state buffer
+ *                    (partial overlap: MAMBA_ERR_INVALID_ARG)
  *   checkpoints      MAMBA_FLAG_LAYOUT_BLD only (NULL otherwise): NULL, or
  *                    (batch, ceil(seqlen / 64), dim) fp32, receives the state
  *                    entering each block of 64 steps, for the backward
@@ -645,7 +649,7 @@ MAMBA_API mamba_status_t mamba_gated_state_update(float *state, const void *gate
  * residual_dtype is io_dtype or MAMBA_F32.  Rows are contiguous, `*_stride`
  * elements apart (0: packed; below dim: MAMBA_ERR_INVALID_ARG).  residual_out may be the residual
  * buffer itself and out may be x, with the same stride; otherwise outputs must
- * not alias inputs or each other.
+ * not alias inputs or each other.  dim up to 2^28 (MAMBA_ERR_UNSUPPORTED otherwise).
  */
 typedef struct {
     int64_t rows, dim;

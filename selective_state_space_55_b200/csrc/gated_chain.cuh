@@ -15,6 +15,13 @@
 // short; a stretch starts from the state that its predecessor published, which
 // belongs to a CTA that is running or done.  Every wait is bounded; one that
 // runs out is recorded and the call ends with undefined outputs.
+//
+// Measured, sigmoid gate (copy rate 6529 GB/s): bf16 8 x 2048 x 4096 (batch, seqlen,
+// dim) forward 94 us, 4.28 TB/s, 66 %, backward from checkpoints 168 us, 4.02 TB/s,
+// 62 %; 16 x 2048 x 5120 forward 190 us, 81 %; fp32 4 x 2048 x 4096 82 and 154 us,
+// 75 and 67 %.  Bound by issue (about 25 instructions per element forward, the
+// sigmoid's two special functions among them) and, with fewer groups than places
+// for CTAs, by the time a tile takes from its arrival to the next state.
 #pragma once
 
 #include "gated_scan.cuh"
@@ -481,7 +488,9 @@ __global__ void __launch_bounds__(kChainThreads, 2)
 // (gated_join): phase one reads a block for its map, phase two again for its
 // outputs, which replace x there and leave by TMA.  HBM sees each input once; the
 // steps' arithmetic is done twice.  Three CTAs per SM cover one another's loads
-// and joins.
+// and joins.  bf16, 1 x 131072 x 1536 (batch, seqlen, dim), log decay, last state: 342
+// us, 3.54 TB/s, 54 %; 1 x 4096 x 4096 45 us (a CTA per chain: 115).  Bound by the waits
+// for earlier segments' maps; 32 steps per warp measured best.
 template <typename IoT>
 struct SegmentSizes {
     static constexpr int kSteps = sizeof(IoT) == 2 ? 32 : 16;                      // per warp

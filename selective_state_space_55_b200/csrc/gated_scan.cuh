@@ -34,7 +34,9 @@
 // fp32x2.  Segments are handed out by a counter, the earliest steps of all chains
 // first, so that every segment's predecessors belong to CTAs that are running or
 // done; the wait is bounded all the same.  What TMA can move has kernels of its own
-// (gated_chain.cuh).
+// (gated_chain.cuh).  Measured, bf16: 1 x 131072 x 1536 backward 543 us, 57 % of the
+// copy rate; 8 x 2047 x 4095 forward 490 us, backward 1200 us, where rows start
+// anywhere and every element is a load of its own.
 //
 // Layout (batch, dim, seqlen): a lane takes 8 consecutive steps of two neighbouring
 // chains, the warp composes its lanes' maps by shuffles, and 1 to 8 warps share a
@@ -1234,7 +1236,8 @@ constexpr int kGatedUpdateThreads = 128;
 
 // kN channels per thread (8: vectors; 1: any alignment and size).  One read
 // and one write of the fp32 state beside gate, x and out: HBM-bound for large
-// batches, launch latency below.
+// batches, launch latency below (1 x 4096 and 128 x 4096 bf16: 8 us in a replayed
+// graph with cold caches, 9 us called from Python).
 template <typename IoT, bool kLog, int kN>
 __global__ void __launch_bounds__(kGatedUpdateThreads)
     gated_update_kernel(const __grid_constant__ GatedUpdateParams p) {

@@ -20,7 +20,14 @@
 // the spread costs no digits.  The backward's column sums stay in the registers
 // of the lane that owns the columns while the CTA walks its rows; each CTA
 // leaves one partial row per sum, and a second launch adds the partial rows in
-// a fixed order (no atomics: results repeat bit for bit).
+// a fixed order (no atomics: results repeat bit for bit).  With few chunks per lane
+// a team's rows come through a ring of bulk copies in shared memory, because the
+// registers hold one row only.
+//
+// Measured, bf16 with a residual (copy rate 6529 GB/s): 32768 x 2560 forward 119 us,
+// 5.65 TB/s, 87 %; backward 127 us, 5.29 TB/s, 81 %, the rest being the barriers of
+// the two row reductions; 8 x 2560 forward 8 us, latency.  Columns that are not a
+// multiple of 8 move element by element: 32768 x 2559 203 and 276 us.
 #pragma once
 
 #include "row_vectors.cuh"
