@@ -762,8 +762,11 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False
         residual_out = _like(residual)
     mean = rstd = None
     if return_stats:
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-        mean = None if rms else _like(rstd)
+        lead = tuple(shape[:-1])
+        if rms:
+            rstd = torch.empty(lead, dtype=torch.float32, device=device)
+        else:                   # one allocation for both
+            mean, rstd = torch.empty((2, *lead), dtype=torch.float32, device=device).unbind(0)
     dims = _NORM.pack(x.numel() // dim if dim else 0, dim, _DTYPE_CODE[io], _DTYPE_CODE[rdt], bool(rms), eps,
                       xs, ys, rs, ss, 0, 0, 0)
     _finish("mamba_layer_norm_fwd", library().mamba_layer_norm_fwd(
