@@ -342,12 +342,17 @@ def test_withheld_handoff_is_reported():
     assert_close("out", ops.gated_scan_fwd(**v, layout="bld"), *want["out"])
 
 
+@pytest.mark.parametrize("ragged,log_decay", [(False, False), (True, False), (True, True)])
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_plentiful_chains(dtype):
+def test_plentiful_chains(dtype, ragged, log_decay):
     """(batch, dim, seqlen) with so many pairs of chains that one warp walks a pair's three
     tiles forward; an odd dim leaves pairs with one chain."""
-    v, back = make(2, 2961, 701, "bdl", dtype, False, seed=17)
-    check(v, back, "bdl", False)
+    v, back = make(2, 2961, 701, "bdl", dtype, log_decay, seed=17, ragged=ragged)
+    if ragged:
+        outside = (torch.arange(701, device=DEV)[None] >= v["seqlens"][:, None])[:, None, :]
+        for t in (v["gate"], v["x"], back["dout"]):
+            t.copy_(torch.where(outside, torch.full_like(t, float("nan")), t))
+    check(v, back, "bdl", log_decay)
 
 
 @pytest.mark.parametrize("log_decay", [False, True])
