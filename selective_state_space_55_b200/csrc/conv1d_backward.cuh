@@ -79,10 +79,11 @@ struct ConvRow {
         dx = static_cast<IoT*>(p.dx) + at;
         init = p.init != nullptr ? static_cast<const IoT*>(p.init) + chain * kW : nullptr;
         dfinal = p.dfinal != nullptr ? static_cast<const IoT*>(p.dfinal) + chain * kW : nullptr;
-        begin = (int)(stretch * p.stretch_tiles * kWarpSteps) - row_phase(x);
-        const int end = begin + (int)p.stretch_tiles * kWarpSteps, L = (int)p.seqlen;
+        // whole stretches: the last one may end far behind the row, past 32 bits
+        const int64_t steps = p.stretch_tiles * kWarpSteps, end = (stretch + 1) * steps - row_phase(x);
+        begin = (int)(end - steps);
         lo = begin > 0 ? begin : 0;
-        hi = live ? (end < L ? end : L) : lo;
+        hi = live ? (int)(end < p.seqlen ? end : p.seqlen) : lo;
     }
 
     // x_s at any time: the row, the initial state before it, 0 elsewhere

@@ -123,3 +123,26 @@ def test_saturated_activation():
     v["bias"].zero_()
     g = check(v)
     assert torch.isfinite(g["dx"]).all()
+
+
+def test_longest_rows():
+    """The documented limit, 2^31 - 65536 steps: the last stretch of a row ends at 2^31.  Small
+    whole numbers in the last 2.2 million steps and zeros before them, so every product and
+    partial sum (below 2^24) is exact."""
+    L, n, W = 2 ** 31 - 65536, 2_200_000, 4
+    g = torch.Generator(device=DEV)
+    g.manual_seed(10)
+    x, dout = (torch.zeros(1, 2, L, dtype=BF, device=DEV) for _ in range(2))
+    xt = torch.randint(0, 3, (2, n), generator=g, device=DEV).double()
+    dt = torch.randint(0, 2, (2, n), generator=g, device=DEV).double()
+    x[0, :, L - n:], dout[0, :, L - n:] = xt.to(BF), dt.to(BF)
+    w = torch.tensor([[1.0, -2.0, 1.0, 2.0], [2.0, 1.0, -1.0, 1.0]], device=DEV)
+    got = ops.causal_conv1d_bwd(x, w, dout, bias=torch.zeros(2, device=DEV), silu=False)
+    seq, after = (torch.nn.functional.pad(t, p) for t, p in ((xt, (W - 1, 0)), (dt, (0, W - 1))))
+    dw = torch.stack([(dt * seq[:, k:k + n]).sum(1) for k in range(W)], 1)
+    dx = sum(w[:, k:k + 1].double() * after[:, W - 1 - k:W - 1 - k + n] for k in range(W))
+    assert torch.equal(got["dweight"].double(), dw)
+    assert torch.equal(got["dbias"].double(), dt.sum(1))
+    assert torch.equal(got["dx"][0, :, L - n:].double(), dx)
+    # the gradient reaches W - 1 steps further back, no more
+    assert not got["dx"][0, :, :L - n - W + 1].any()
