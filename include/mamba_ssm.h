@@ -605,7 +605,9 @@ MAMBA_API mamba_status_t mamba_gated_scan_fwd(const void *gate, const void *x,
  *   dgate_bias_d = sum_{b,t} dgate_t,  dinitial_state = a_0 l_0
  *   checkpoints      the forward's, from the same inputs; NULL: the states are
  *                    recomputed (one more pass over gate and x)
- *   dgate_bias (dim,), dinitial_state (batch, dim) fp32: NULL when not wanted
+ *   dgate_bias (dim,), dinitial_state (batch, dim) fp32: NULL when not wanted;
+ *                    dinitial_state may be the dlast_state buffer (partial overlap:
+ *                    MAMBA_ERR_INVALID_ARG)
  * dgate and dx must not alias inputs or each other.  Sums are added in a fixed
  * order: results repeat bit for bit.  The workspace is smaller with the
  * forward's checkpoints (have_checkpoints != 0 in the query).

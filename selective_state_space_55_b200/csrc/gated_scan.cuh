@@ -644,6 +644,9 @@ __global__ void __launch_bounds__(kGatedThreads, 2)
             }
         }
         // the pointers now stand at the block's end, in whole groups of kGatedSub steps
+        float2 r[kGatedPairs];
+        // before the barrier: dh0 may replace dlast, and block 0 may be done early
+        load_state<kVec>(p.dlast, at.b, p.dim, at.c, r);
         const MapStore ms = pack_maps(m);
         sA[warp][lane] = ms.A;
         sH[warp][lane] = ms.H;
@@ -655,8 +658,6 @@ __global__ void __launch_bounds__(kGatedThreads, 2)
             move(-kGatedSub);
             load(ra, (at.left - 1) / kGatedSub * kGatedSub);
         }
-        float2 r[kGatedPairs];
-        load_state<kVec>(p.dlast, at.b, p.dim, at.c, r);
         gated_enter<true>(p, at, warp, lane, sA, sH, entering, r);
 
         float2 db[kGatedPairs] = {zero, zero};

@@ -1,4 +1,6 @@
 """Gated linear recurrence (forward, backward, one token) against its 64-bit form."""
+import ctypes
+
 import pytest
 import torch
 
@@ -486,3 +488,32 @@ def test_concurrent_streams(dim, L, dtype):
         assert_close("out", out, *want["out"])
         for k in g:
             assert_close(k, g[k], *want[k])
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("layout,batch,dim,L", [("bld", 5, 96, 65), ("bld", 5, 96, 512), ("bld", 3, 70, 300),
+                                                ("bld", 2, 64, 7000), ("bld", 25, 840, 577), ("bdl", 3, 70, 300),
+                                                ("bdl", 2, 5, 4100)])
+def test_state_gradient_in_place(layout, batch, dim, L, ragged):
+    """dinitial_state in dlast_state's buffer (the C entry point): the warps of a short chain, the
+    segments of a long one and the chained stretches all read it before it is replaced."""
+    v, back = make(batch, dim, L, layout, BF, False, seed=L + dim, ragged=ragged)
+    want = ref.gated(**v, **back, layout=layout)
+    lib, flags = ops.library(), ops.MAMBA_FLAG_LAYOUT_BLD if layout == "bld" else 0
+    dims = ops.GatedDims(batch=batch, dim=dim, seqlen=L, io_dtype=ops.MAMBA_BF16, flags=flags,
+                         seqlens=v["seqlens"].data_ptr() if ragged else None)
+    need = lib.mamba_gated_scan_bwd_workspace_bytes(ctypes.byref(dims), 0)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    dims.workspace, dims.workspace_bytes = ws.data_ptr(), need
+    for _ in range(3):
+        state, dgate, dx = back["dlast_state"].clone(), torch.empty_like(v["x"]), torch.empty_like(v["x"])
+        rc = lib.mamba_gated_scan_bwd(
+            v["gate"].data_ptr(), v["x"].data_ptr(), v["gate_bias"].data_ptr(), v["initial_state"].data_ptr(), None,
+            back["dout"].data_ptr(), state.data_ptr(), dgate.data_ptr(), dx.data_ptr(), None, state.data_ptr(),
+            ctypes.byref(dims), torch.cuda.current_stream().cuda_stream)
+        assert rc == ops.MAMBA_OK
+        torch.cuda.synchronize()
+        assert_close("dinitial_state", state, *want["dinitial_state"])
+        assert_close("dgate", dgate, *want["dgate"])
+        assert_close("dx", dx, *want["dx"])
+    assert ops.device_status() == 0
