@@ -128,7 +128,7 @@ __device__ __forceinline__ void ring_put(unsigned char* row, int lane, float2 v)
 }
 
 __device__ __forceinline__ float2 chain_load2(const float* p, int64_t d, int64_t dim) {
-    return make_float2(d < dim ? __ldcg(p + d) : 0.0f, d + 1 < dim ? __ldcg(p + d + 1) : 0.0f);
+    return make_float2(d < dim ? load_ordered(p + d) : 0.0f, d + 1 < dim ? load_ordered(p + d + 1) : 0.0f);
 }
 
 __device__ __forceinline__ void chain_store2(float* p, int64_t d, int64_t dim, float2 v) {
@@ -207,7 +207,7 @@ __device__ __forceinline__ bool chain_receive(const ChainParams& p, const ChainT
             return false;
         }
     }
-    *h = __ldcg(reinterpret_cast<const float2*>(p.handoff + k * kChainChannels) + lane);
+    *h = load_ordered(reinterpret_cast<const float2*>(p.handoff + k * kChainChannels) + lane);
     return true;
 }
 

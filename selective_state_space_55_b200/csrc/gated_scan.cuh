@@ -171,6 +171,30 @@ __device__ __forceinline__ void store_release(unsigned int* p, unsigned int v) {
     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// Loads from L2 of what other CTAs hand on, and of the start states (whose buffer
+// the last states may share).  They stay on their side of the waits, barriers and
+// publications around them: the cached-load intrinsics do not promise that.
+__device__ __forceinline__ float load_ordered(const float* p) {
+    float v;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 load_ordered(const float2* p) {
+    float2 v;
+    asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 load_ordered(const float4* p) {
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // ------------------------------------------------ (batch, seqlen, dim) layout
 
 constexpr int kGatedPairs = kGatedChannels / 64;            // pairs of channels per lane
@@ -372,9 +396,10 @@ __device__ __forceinline__ bool gated_join(const GatedLinks& links, int64_t grou
         if (lane == 0) record_device_error(MAMBA_ERR_TIMEOUT);
         return false;
     }
+    __syncwarp();                                // what a lane has acquired, the warp may read
     if (join > 0)
 #pragma unroll
-        for (int k = 0; k < kP; ++k) h[k] = __ldcg(states + (join * kP + k) * 32);
+        for (int k = 0; k < kP; ++k) h[k] = load_ordered(states + (join * kP + k) * 32);
     constexpr int kBatch = 8;                    // maps asked for together
     for (int c = 0; c < before; c += kBatch) {
         float4 m[kBatch][kP];
@@ -382,7 +407,7 @@ __device__ __forceinline__ bool gated_join(const GatedLinks& links, int64_t grou
         for (int i = 0; i < kBatch; ++i)
 #pragma unroll
             for (int k = 0; k < kP; ++k)
-                m[i][k] = c + i < before ? __ldcg(maps + ((first + c + i) * kP + k) * 32)
+                m[i][k] = c + i < before ? load_ordered(maps + ((first + c + i) * kP + k) * 32)
                                          : make_float4(1.0f, 1.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)

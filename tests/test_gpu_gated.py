@@ -517,3 +517,20 @@ def test_state_gradient_in_place(layout, batch, dim, L, ragged):
         assert_close("dgate", dgate, *want["dgate"])
         assert_close("dx", dx, *want["dx"])
     assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("layout,batch,dim,L", [("bld", 2, 64, 7000), ("bld", 2, 67, 7000), ("bld", 3, 96, 257),
+                                                ("bld", 25, 840, 1300), ("bdl", 3, 70, 5000)])
+def test_long_state_in_place(layout, batch, dim, L, dtype):
+    """last_state in initial_state's buffer where many segments or stretches read the start: each
+    has read it before the last of them replaces it."""
+    v, _ = make(batch, dim, L, layout, dtype, False, seed=L + dim)
+    want = ref.gated(**v, layout=layout)
+    for _ in range(3):
+        state = v["initial_state"].clone()
+        out, _ = ops.gated_scan_fwd(v["gate"], v["x"], v["gate_bias"], initial_state=state, last_state=state,
+                                    layout=layout)
+        assert_close("out", out, *want["out"])
+        assert_close("last", state, *want["last_state"])
+    assert ops.device_status() == 0
