@@ -563,8 +563,10 @@ typedef struct {
     int32_t log_decay;
     int32_t flags;             /* MAMBA_FLAG_LAYOUT_BLD; MAMBA_FLAG_TEST_WITHHOLD_HANDOFF (test
                                 * only: in the (batch, seqlen, dim) layout no segment hands its
-                                * state on, every wait runs out after some 0.3 s and
-                                * mamba_device_status() reports MAMBA_ERR_TIMEOUT) */
+                                * state on, the first waits run out after some 0.3 s, the
+                                * others of the call then give up too, however many segments
+                                * are left, and mamba_device_status() reports
+                                * MAMBA_ERR_TIMEOUT) */
     int32_t reserved;
     const int32_t *seqlens;    /* device, (batch,), or NULL */
     mamba_strides_t gate, x;

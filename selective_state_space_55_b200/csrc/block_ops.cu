@@ -275,7 +275,7 @@ mamba_status_t check_gated(const mamba_gated_dims_t* d) {
 bool gated_bld(const mamba_gated_dims_t* d) { return (d->flags & MAMBA_FLAG_LAYOUT_BLD) != 0; }
 
 struct GatedLayout {           // offsets in the workspace, bytes
-    size_t tickets, flags, flags2, zeroed, maps, joins, enter, bias, states, total;
+    size_t counters, flags, flags2, zeroed, maps, joins, enter, bias, states, total;
     int64_t blocks, segments, groups_per_row, groups, items;
     int64_t tiles;
     int warps, width;          // (batch, seqlen, dim): blocks per segment; else warps and lanes per chain
@@ -313,7 +313,7 @@ mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool rec
         w->items = w->groups * w->segments;
         if (w->items >= kLimit31 / 2) return MAMBA_ERR_UNSUPPORTED;
         if (w->segments > 1) {
-            w->tickets = take(2 * sizeof(unsigned int));
+            w->counters = take(3 * sizeof(unsigned int));      // two tickets, the mark of a wait that ran out
             w->flags = take((size_t)w->items * sizeof(unsigned int));
             if (backward && recompute) w->flags2 = take((size_t)w->items * sizeof(unsigned int));
             w->zeroed = off;
@@ -508,6 +508,7 @@ mamba_status_t run_gated_chain(const GatedParams& g, const GatedLayout& w, const
     prm.withhold = g.links.withhold;
     if (prm.stretches > 1) {
         prm.ticket = reinterpret_cast<unsigned int*>(ws + w.chain_zeroed);
+        prm.failed = prm.ticket + 1;
         prm.flags = reinterpret_cast<unsigned int*>(ws + w.chain_zeroed + 256);
         prm.handoff = reinterpret_cast<float*>(ws + w.chain_handoff);
         if (cudaMemsetAsync(ws + w.chain_zeroed, 0, w.chain_zeroed_bytes, stream) != cudaSuccess) return MAMBA_ERR_CUDA;
@@ -563,6 +564,7 @@ mamba_status_t run_gated_segments(const GatedParams& g, const GatedLayout& w, co
     prm.links.withhold = g.links.withhold;
     if (w.seg_segments > 1) {
         prm.ticket = reinterpret_cast<unsigned int*>(ws + w.seg_zeroed);
+        prm.links.failed = prm.ticket + 1;
         prm.links.flags = reinterpret_cast<unsigned int*>(ws + w.seg_zeroed + 256);
         prm.links.maps = reinterpret_cast<float4*>(ws + w.seg_maps);
         prm.links.states = reinterpret_cast<float2*>(ws + w.seg_states);
@@ -653,7 +655,8 @@ void gated_apply_layout(const GatedLayout& w, uint8_t* ws, GatedParams* prm) {
     prm->groups_per_row = w.groups_per_row;
     prm->groups = w.groups;
     prm->items = w.items;
-    prm->ticket = w.zeroed ? reinterpret_cast<unsigned int*>(ws + w.tickets) : nullptr;
+    prm->ticket = w.zeroed ? reinterpret_cast<unsigned int*>(ws + w.counters) : nullptr;
+    prm->links.failed = reinterpret_cast<unsigned int*>(ws + w.counters) + 2;
     prm->links.segments = w.segments;
     prm->links.flags = reinterpret_cast<unsigned int*>(ws + w.flags);
     prm->links.maps = reinterpret_cast<float4*>(ws + w.maps);

@@ -49,6 +49,7 @@ struct ChainParams {
     float* handoff;                // [groups][stretches][64]
     unsigned int* flags;           // [groups][stretches]
     unsigned int* ticket;
+    unsigned int* failed;          // 0, or 1 once a wait of this call has run out
     int64_t dim, seqlen;
     int64_t tiles;                 // per chain
     int64_t groups_per_row, groups;
@@ -201,9 +202,13 @@ __device__ __forceinline__ bool chain_receive(const ChainParams& p, const ChainT
     unsigned int poll = 0;
     while (load_acquire(p.flags + k) == 0u) {
         if (*failed) return false;
+        if (gated_look(poll) && load_acquire(p.failed) != 0u) {
+            *failed = 1;
+            return false;
+        }
         if (++poll == kGatedPollLimit) {
             *failed = 1;
-            record_device_error(MAMBA_ERR_TIMEOUT);
+            gated_give_up(p.failed);
             return false;
         }
     }
@@ -627,6 +632,7 @@ __global__ void __launch_bounds__(kChainWarps * 32, 3)
         if (__syncthreads_or(failed)) break;
         const int64_t following = sh.next_slot;
         prefetch(following);                     // HBM works while the CTA waits for the join
+        bool lost = false;
         if (warp == 0) {
             if (p.ticket != nullptr) {
                 float2 At[1] = {one}, Ht[1] = {zero};
@@ -636,7 +642,7 @@ __global__ void __launch_bounds__(kChainWarps * 32, 3)
                     Ht[0] = __ffma2_rn(make_float2(m.x, m.y), Ht[0], make_float2(m.z, m.w));
                     At[0] = __fmul2_rn(At[0], make_float2(m.x, m.y));
                 }
-                gated_join<1>(p.links, group, pos, lane, At, Ht, start);
+                lost = !gated_join<1>(p.links, group, pos, lane, At, Ht, start);
             }
             float2 h = start[0];
 #pragma unroll
@@ -646,7 +652,8 @@ __global__ void __launch_bounds__(kChainWarps * 32, 3)
                 h = __ffma2_rn(make_float2(m.x, m.y), h, make_float2(m.z, m.w));
             }
         }
-        __syncthreads();
+        // a wait that ran out is recorded: the CTA takes no further item, the call's outputs are undefined
+        if (__syncthreads_or(lost)) break;
         float2 h = sh.entering[warp][lane];
         if (t < p.seqlen) {
             if (p.enter != nullptr && t % kChainTile == 0)

@@ -69,6 +69,7 @@ struct GatedLinks {
     float4* maps;                 // [groups][segments][pairs][32]: a lane's maps
     float2* states;               // [groups][segments / kGatedJoin][pairs][32]: states entering a join group
     unsigned int* flags;          // [groups][segments]: 0, 1 = map published, 2 = state published
+    unsigned int* failed;         // 0, or 1 once a wait of this call has run out
     int64_t segments;
     int withhold;                 // test only: publish nothing
 };
@@ -103,7 +104,11 @@ struct GatedParams {
     int64_t tiles;                // (batch, dim, seqlen): per chain
 };
 
+// A wait that runs out (some 0.3 s) is recorded, and marked for the call: every
+// other wait of the call looks at the mark now and then, and the CTAs leave instead
+// of waiting as long for each item that is left.
 constexpr unsigned int kGatedPollLimit = 1u << 19;
+constexpr unsigned int kGatedPollsPerLook = 64;
 
 // g and a of the sigmoid gate from f log2(e).  With e = exp(-f): g = 1 / (1 + e),
 // and a = e g for f >= 0, 1 - g (rounded to nearest) for f < 0: there a is close
@@ -193,6 +198,16 @@ __device__ __forceinline__ float4 load_ordered(const float4* p) {
                  : "l"(p)
                  : "memory");
     return v;
+}
+
+// Time to look whether another wait of this call has run out?
+__device__ __forceinline__ bool gated_look(unsigned int poll) {
+    return poll % kGatedPollsPerLook == kGatedPollsPerLook - 1;
+}
+
+__device__ __forceinline__ void gated_give_up(unsigned int* failed) {
+    record_device_error(MAMBA_ERR_TIMEOUT);
+    store_release(failed, 1u);
 }
 
 // ------------------------------------------------ (batch, seqlen, dim) layout
@@ -366,7 +381,7 @@ __device__ __forceinline__ void gated_publish(const GatedLinks& links, unsigned 
 // publishes the state that leaves it, the others their maps; a segment waits for
 // the state entering its group and the maps of the group's earlier segments, and
 // folds them in order.  h is the state entering position 0 and becomes the one
-// entering pos.  False when the wait ran out.
+// entering pos.  False when the wait, or another of the call, ran out.
 template <int kP>
 __device__ __forceinline__ bool gated_join(const GatedLinks& links, int64_t group, int64_t pos, int lane,
                                            const float2 (&A)[kP], const float2 (&H)[kP], float2 (&h)[kP]) {
@@ -391,9 +406,10 @@ __device__ __forceinline__ bool gated_join(const GatedLinks& links, int64_t grou
     for (; poll < kGatedPollLimit; ++poll) {
         if (!ready) ready = load_acquire(mine) >= (wait_state ? 2u : 1u);
         if (__all_sync(0xffffffffu, ready)) break;
+        if (gated_look(poll) && __any_sync(0xffffffffu, load_acquire(links.failed) != 0u)) return false;
     }
     if (poll == kGatedPollLimit) {
-        if (lane == 0) record_device_error(MAMBA_ERR_TIMEOUT);
+        if (lane == 0) gated_give_up(links.failed);
         return false;
     }
     __syncwarp();                                // what a lane has acquired, the warp may read
@@ -433,11 +449,13 @@ __device__ __forceinline__ int64_t gated_first_item(const GatedParams& p, int64_
 
 // Joins the warps' maps (in shared memory) and the segments': h, the state
 // entering position 0 of the chain, becomes the one entering this warp's block.
+// False, for the whole CTA, when a wait ran out: it takes no further item.
 template <bool kReverse>
-__device__ __forceinline__ void gated_enter(const GatedParams& p, const GatedBlockAt& at, int warp, int lane,
+__device__ __forceinline__ bool gated_enter(const GatedParams& p, const GatedBlockAt& at, int warp, int lane,
                                             const float4 (&sA)[kGatedWarps][32], const float4 (&sH)[kGatedWarps][32],
                                             float4 (&entering)[32], float2 (&h)[kGatedPairs]) {
     const int warps = blockDim.x >> 5;
+    bool lost = false;
     const int rank = kReverse ? warps - 1 - warp : warp;             // in scan order
     if (p.ticket != nullptr && warp == 0) {
         Maps all = identity_maps();
@@ -447,7 +465,7 @@ __device__ __forceinline__ void gated_enter(const GatedParams& p, const GatedBlo
         }
         float2 e[kGatedPairs] = {h[0], h[1]};
         // a wait that ran out is recorded; the call's outputs are undefined then
-        gated_join<kGatedPairs>(p.links, at.group, at.pos, lane, all.A, all.H, e);
+        lost = !gated_join<kGatedPairs>(p.links, at.group, at.pos, lane, all.A, all.H, e);
         entering[lane] = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
     }
     Maps mine = identity_maps();
@@ -456,13 +474,14 @@ __device__ __forceinline__ void gated_enter(const GatedParams& p, const GatedBlo
         mine = compose(mine, unpack_maps(sA[w][lane], sH[w][lane]));
     }
     if (p.ticket != nullptr) {
-        __syncthreads();
+        if (__syncthreads_or(lost)) return false;
         const float4 e = entering[lane];
         h[0] = make_float2(e.x, e.y);
         h[1] = make_float2(e.z, e.w);
     }
 #pragma unroll
     for (int k = 0; k < kGatedPairs; ++k) h[k] = __ffma2_rn(mine.A[k], h[k], mine.H[k]);
+    return true;
 }
 
 template <bool kVec>
@@ -548,7 +567,7 @@ __global__ void __launch_bounds__(kGatedThreads, sizeof(IoT) == 2 ? 4 : 2)
             if (threadIdx.x == 0) next_slot = coming;
             __syncthreads();
             if (p.ticket != nullptr) following = next_slot;
-            gated_enter<false>(p, at, warp, lane, sA, sH, entering, h);
+            if (!gated_enter<false>(p, at, warp, lane, sA, sH, entering, h)) break;
         }
         if (at.rows > 0 && p.enter != nullptr)
             store_quad<float, kVec>(p.enter + (at.b * p.blocks + at.block) * p.dim + at.c.d, live, h[0], h[1]);
@@ -683,7 +702,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2)
             move(-kGatedSub);
             load(ra, (at.left - 1) / kGatedSub * kGatedSub);
         }
-        gated_enter<true>(p, at, warp, lane, sA, sH, entering, r);
+        if (!gated_enter<true>(p, at, warp, lane, sA, sH, entering, r)) break;
 
         float2 db[kGatedPairs] = {zero, zero};
         IoT* dgate = static_cast<IoT*>(p.dgate) + at.b * p.dgate_s.batch + at.t * p.dgate_s.row + at.c.d;

@@ -1,5 +1,6 @@
 """Gated linear recurrence (forward, backward, one token) against its 64-bit form."""
 import ctypes
+import time
 
 import pytest
 import torch
@@ -534,3 +535,33 @@ def test_long_state_in_place(layout, batch, dim, L, dtype):
         assert_close("out", out, *want["out"])
         assert_close("last", state, *want["last_state"])
     assert ops.device_status() == 0
+
+
+WITHHELD = [("fwd", 1, 8, 1 << 21, True), ("fwd", 1, 7, 1 << 21, True), ("bwd", 1, 8, 1 << 21, True),
+            ("bwd", 1, 8, 1 << 21, False), ("bwd", 2, 7, 1 << 20, True), ("bwd", 10, 2048, 2000, True)]
+
+
+@pytest.mark.parametrize("call,batch,dim,L,checkpoints", WITHHELD)
+def test_withheld_handoff_ends_the_whole_call(call, batch, dim, L, checkpoints):
+    """Thousands of segments that never hand on (thousands of waits of some 0.3 s, were each to run
+    out by itself): the call ends soon, the status says so, and the next call is right again."""
+    v, back = make(batch, dim, L, "bld", BF, True, seed=dim)
+
+    def run(flags=0):
+        if call == "fwd":
+            return {"out": ops.gated_scan_fwd(**v, log_decay=True, layout="bld", flags=flags)}
+        return ops.gated_scan_bwd(**v, **back, checkpoints=ck, log_decay=True, layout="bld", flags=flags)
+
+    ck = ops.gated_scan_fwd(**v, log_decay=True, layout="bld", return_checkpoints=True)[1] if checkpoints else None
+    good = run()
+    assert ops.device_status() == 0
+    start = time.perf_counter()
+    run(ops.MAMBA_FLAG_TEST_WITHHOLD_HANDOFF)
+    torch.cuda.synchronize()
+    took = time.perf_counter() - start
+    assert ops.STATUS_NAMES[ops.device_status()] == "MAMBA_ERR_TIMEOUT"
+    assert took < 1.5, took
+    again = run()
+    assert ops.device_status() == 0
+    for k in good:
+        assert torch.equal(good[k], again[k]), k
