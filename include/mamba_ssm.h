@@ -649,6 +649,7 @@ MAMBA_API mamba_status_t mamba_gated_state_update(float *state, const void *gate
  *   residual_out     (rows, dim) residual_dtype or NULL: s, for the next block
  *   weight, bias     (dim,) fp32; NULL: ones, zeros
  *   mean, rstd       (rows,) fp32 or NULL: kept for the backward (mean is 0 with rms)
+ *                    (dim == 0: NaN, the moments of nothing)
  * The norm is taken of the fp32 sum, before s is rounded to residual_dtype.
  * residual_dtype is io_dtype or MAMBA_F32.  Rows are contiguous, `*_stride`
  * elements apart (0: packed; below dim: MAMBA_ERR_INVALID_ARG).  residual_out may be the residual

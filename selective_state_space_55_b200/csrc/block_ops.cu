@@ -753,7 +753,14 @@ MAMBA_API mamba_status_t mamba_layer_norm_fwd(const void* x, const void* residua
     const mamba_status_t st = check_norm(dims);
     if (st != MAMBA_OK) return st;
     if (!(dims->eps >= 0.0f)) return MAMBA_ERR_INVALID_ARG;
-    if (dims->rows == 0 || dims->dim == 0) return MAMBA_OK;
+    if (dims->rows == 0) return MAMBA_OK;
+    if (dims->dim == 0) {               // moments of nothing: 0 / 0 (all bits set is a NaN)
+        if ((mean && !aligned(mean, 4)) || (rstd && !aligned(rstd, 4))) return MAMBA_ERR_ALIGN;
+        const size_t bytes = (size_t)dims->rows * sizeof(float);
+        cudaError_t e = mean != nullptr ? cudaMemsetAsync(mean, dims->rms ? 0 : 0xff, bytes, stream) : cudaSuccess;
+        if (e == cudaSuccess && rstd != nullptr) e = cudaMemsetAsync(rstd, 0xff, bytes, stream);
+        return status_of(e);
+    }
     if (x == nullptr || out == nullptr) return MAMBA_ERR_INVALID_ARG;
     const int es = dtype_bytes(dims->io_dtype), rs = dtype_bytes(dims->residual_dtype);
     if (!aligned(x, es) || !aligned(out, es) || (residual && !aligned(residual, rs)) ||

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import struct
 from pathlib import Path
 
@@ -736,7 +737,7 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False
     (default: a new tensor when ``residual`` is given; it may be ``residual``
     itself, and ``out`` may be x).  Returns ``out``; with a residual or a
     residual_out, (out, residual_out); with ``return_stats``, mean (None for
-    ``rms``) and rstd, fp32 in x's leading shape, are appended.
+    ``rms``) and rstd, fp32 in x's leading shape, are appended (NaN where dim is 0).
     """
     device, io, shape = _needs_cuda("x", x)
     if stream is not None or device.index != torch._C._cuda_getDevice():
@@ -767,7 +768,8 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False
             rstd = torch.empty(lead, dtype=torch.float32, device=device)
         else:                   # one allocation for both
             mean, rstd = torch.empty((2, *lead), dtype=torch.float32, device=device).unbind(0)
-    dims = _NORM.pack(x.numel() // dim if dim else 0, dim, _DTYPE_CODE[io], _DTYPE_CODE[rdt], bool(rms), eps,
+    rows = x.numel() // dim if dim else math.prod(shape[:-1])
+    dims = _NORM.pack(rows, dim, _DTYPE_CODE[io], _DTYPE_CODE[rdt], bool(rms), eps,
                       xs, ys, rs, ss, 0, 0, 0)
     _finish("mamba_layer_norm_fwd", library().mamba_layer_norm_fwd(
         x.data_ptr(), residual.data_ptr() if residual is not None else 0, wp, bp, out.data_ptr(),

@@ -1,4 +1,6 @@
 """Layer norm with the residual add, forward and backward, against its 64-bit form."""
+import ctypes
+
 import pytest
 import torch
 
@@ -199,3 +201,19 @@ def test_stream_of_its_own():
     out, s = ops.layer_norm_fwd(v["x"], v["weight"], v["bias"], residual=v["residual"], stream=st)
     st.synchronize()
     assert_close("out", out, *ref.norm_fwd(v["x"], v["weight"], v["bias"], v["residual"])["out"])
+
+
+@pytest.mark.parametrize("rms", [False, True])
+def test_no_columns(rms):
+    """The moments of empty rows are 0 / 0, not what the buffers held before."""
+    x = torch.empty(3, 5, 0, device=DEV)
+    stats = torch.full((2, 3, 5), 7.0, device=DEV)
+    dims = ops.NormDims(rows=15, dim=0, rms=rms, eps=1e-5)
+    rc = ops.library().mamba_layer_norm_fwd(None, None, None, None, None, None, stats[0].data_ptr(), stats[1].data_ptr(),
+                                            ctypes.byref(dims), torch.cuda.current_stream().cuda_stream)
+    assert rc == ops.MAMBA_OK
+    assert stats[1].isnan().all() and ((stats[0] == 0).all() if rms else stats[0].isnan().all())
+    out, mean, rstd = ops.layer_norm_fwd(x, rms=rms, return_stats=True)
+    assert out.shape == (3, 5, 0) and rstd.isnan().all() and (mean is None if rms else mean.isnan().all())
+    g = ops.layer_norm_bwd(x, x, rstd, mean=mean, weight=torch.empty(0, device=DEV), rms=rms)
+    assert g["dx"].shape == (3, 5, 0) and g["dweight"].shape == (0,)
