@@ -248,7 +248,7 @@ struct NormRing {
     int64_t coming, rows, step;
     int stages, stage;
     uint32_t parity;
-    bool failed;
+    int failed;                              // waits since one ran out, that one included
 
     // Tensor k (null: there is none) with rows of `dim` elements.
     template <typename T>
@@ -268,7 +268,7 @@ struct NormRing {
         stages = n_stages;
         stage = 0;
         parity = 0;
-        failed = false;
+        failed = 0;
         coming = first;
         rows = n_rows;
         if (threadIdx.x == 0) {
@@ -278,7 +278,7 @@ struct NormRing {
     }
     // The next row into stage `to`; one thread of the team.
     __device__ __forceinline__ void request(int to) {
-        if (coming < rows) {
+        if (coming < rows && failed == 0) {
             const uint32_t bar = bars + 8 * to, dst = data + to * stage_bytes;
             uint32_t total = 0;
 #pragma unroll
@@ -292,10 +292,18 @@ struct NormRing {
 #pragma unroll
         for (int k = 0; k < kTensors; ++k) from[k] += stride[k];
     }
+    // A wait that runs out is recorded and the call's outputs are undefined.  Nothing
+    // more is asked for then, and one more wait per stage keeps the CTA's shared memory
+    // until the copies under way have landed.
     __device__ __forceinline__ void wait() {
-        if (!failed && !mbar_wait_bounded(bars + 8 * stage, parity)) {
-            failed = true;
+        const uint32_t bar = bars + 8 * stage;
+        if (failed == 0) {
+            if (mbar_wait_bounded(bar, parity)) return;
             record_device_error(MAMBA_ERR_TIMEOUT);
+        }
+        if (failed < stages) {
+            mbar_wait_bounded(bar, parity);
+            ++failed;
         }
     }
     // Eight elements of tensor k from column col on; 0 where there are none.
