@@ -178,7 +178,9 @@ def norm_bwd(dout, s, rstd, mean=None, weight=None, dresidual_out=None, rms=Fals
 
 # ---------------------------------------------------------------- convolution
 
-def conv_bwd(x, weight, dout, bias=None, initial_conv_state=None, dfinal_conv_state=None, silu=True):
+def conv_bwd(x, weight, dout, bias=None, initial_conv_state=None, dfinal_conv_state=None, silu=True, depth=None):
+    """depth: roundings that a term of the sums over batch and time goes through, at most (default:
+    one per term)."""
     x, w, dy = d64(x), d64(weight), d64(dout)
     B, D, L = x.shape
     W = w.shape[1]
@@ -205,10 +207,11 @@ def conv_bwd(x, weight, dout, bias=None, initial_conv_state=None, dfinal_conv_st
         f = d64(dfinal_conv_state)
         se[:, :, L:] += 2 * U * (f.abs() + ds[:, :, L:].abs())
         ds[:, :, L:] += f
+    depth = B * L + 64 if depth is None else depth
     terms = [dp * tap(k) for k in range(W)]
     dw = torch.stack([t.sum((0, 2)) for t in terms], 1)
-    we = torch.stack([(derr * tap(k).abs()).sum((0, 2)) + (B * L + 64) * U * terms[k].abs().sum((0, 2))
+    we = torch.stack([(derr * tap(k).abs()).sum((0, 2)) + depth * U * terms[k].abs().sum((0, 2))
                       for k in range(W)], 1)
     return {"dx": (ds[:, :, W:], se[:, :, W:]), "dinitial_conv_state": (ds[:, :, :W], se[:, :, :W]),
             "dweight": (dw, we),
-            "dbias": (dp.sum((0, 2)), derr.sum((0, 2)) + (B * L + 64) * U * dp.abs().sum((0, 2)))}
+            "dbias": (dp.sum((0, 2)), derr.sum((0, 2)) + depth * U * dp.abs().sum((0, 2)))}

@@ -1,4 +1,6 @@
 """Backward of the short causal convolution against its 64-bit form."""
+import ctypes
+
 import pytest
 import torch
 
@@ -146,3 +148,29 @@ def test_longest_rows():
     assert torch.equal(got["dx"][0, :, L - n:].double(), dx)
     # the gradient reaches W - 1 steps further back, no more
     assert not got["dx"][0, :, :L - n - W + 1].any()
+
+
+RING = 4                       # tiles of 256 steps on their way to a warp, at most
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("batch,dim,L,W,state", [
+    (5, 1000, 1300, 4, True), (5, 1000, 2048, 4, False), (1, 3001, 2300, 3, True), (1, 5120, 2047, 4, True),
+    (3, 700, 4000, 2, True), (1, 1001, 8003, 4, True), (1, 301, 20001, 4, False), (2, 1200, 4096, 1, True)])
+def test_many_tiles_per_stretch(batch, dim, L, W, state, dtype):
+    """A warp walks more tiles than its ring holds, in one stretch per row or several: what one tile
+    leaves for the next, the neighbours taken from the ring's next stage and the reuse of its slots."""
+    v = make(batch, dim, L, W, dtype, seed=L + W, state=state)
+    dims = ops.make_scan_dims(batch=batch, dim=dim, dstate=1, seqlen=L, io_dtype=dtype, bc_dtype=dtype)
+    room = ops.library().mamba_causal_conv1d_bwd_workspace_bytes(ctypes.byref(dims), W)
+    stretches = room // (batch * (W + 1) * dim * 4)           # one row of sums for each
+    phase = 0 if (L * v["x"].element_size()) % 16 == 0 else 16 // v["x"].element_size() - 1
+    tiles = -(-(L + phase) // 256) // stretches
+    assert tiles > RING, (tiles, stretches)
+    # a lane's eight steps of every tile (the tensors' phase adds one at most), five joins of
+    # lanes, the stretches' rows by 32 warps and the sum of those
+    depth = 8 * (tiles + 2) + 5 + batch * stretches // 32 + 1 + 32
+    want = ref.conv_bwd(**v, depth=depth)
+    g = ops.causal_conv1d_bwd(**v)
+    for k in g:
+        assert_close(k, g[k], *want[k])

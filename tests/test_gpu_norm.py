@@ -217,3 +217,40 @@ def test_no_columns(rms):
     assert out.shape == (3, 5, 0) and rstd.isnan().all() and (mean is None if rms else mean.isnan().all())
     g = ops.layer_norm_bwd(x, x, rstd, mean=mean, weight=torch.empty(0, device=DEV), rms=rms)
     assert g["dx"].shape == (3, 5, 0) and g["dweight"].shape == (0,)
+
+
+# columns that take 1, 2, 3, 4, 5, 6 and 8 chunks of 8 per lane with many rows, on vectors and
+# element by element
+CHUNKS = [256, 255, 512, 509, 768, 767, 1024, 1021, 1280, 1275, 1536, 1529, 2048, 2041, 2560, 2555]
+
+
+@pytest.mark.parametrize("dim", CHUNKS)
+@pytest.mark.parametrize("dtype,res", [(BF, "none"), (BF, "same"), (BF, "fp32"), (F32, "same")])
+def test_many_rows_at_every_chunk_count(dtype, res, dim):
+    check(make(331, dim, dtype, res, seed=dim), rms=dim % 3 == 0)
+
+
+@pytest.mark.parametrize("rows,dim", [(13100, 512), (13100, 509), (6600, 1024), (6600, 1021), (2700, 2560), (2700, 2555),
+                                      (1700, 4096)])
+@pytest.mark.parametrize("dtype,res", [(BF, "same"), (BF, "fp32"), (F32, "same")])
+def test_backward_of_many_rows(dtype, res, rows, dim):
+    """So many rows that the backward takes two chunks per lane: 1, 2, 5 and 8 warps per row, 8 to
+    1 rows side by side."""
+    check(make(rows, dim, dtype, res, seed=dim))
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 8), (3, 2560), (331, 1280), (2000, 2555), (13100, 512), (13100, 509),
+                                      (6600, 1024), (2700, 2560), (2700, 2555), (1700, 4096), (40000, 96), (3000, 9000),
+                                      (1500, 8193)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_column_sums_hold_every_row_once(dtype, rows, dim):
+    """Small whole numbers and rstd = 1: dweight and dbias are exact (far below 2^24)."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(rows + dim)
+    pick = lambda: torch.randint(-2, 3, (rows, dim), generator=g, device=DEV)  # noqa: E731
+    s, dout = pick(), pick()
+    mean = torch.randint(-1, 2, (rows,), generator=g, device=DEV)
+    got = ops.layer_norm_bwd(dout.to(dtype), s.to(dtype), torch.ones(rows, device=DEV), mean=mean.float(),
+                             weight=torch.ones(dim, device=DEV), bias=torch.zeros(dim, device=DEV))
+    assert torch.equal(got["dweight"].long(), (dout * (s - mean[:, None])).sum(0))
+    assert torch.equal(got["dbias"].long(), dout.sum(0))
