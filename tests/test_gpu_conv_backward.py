@@ -174,3 +174,18 @@ def test_many_tiles_per_stretch(batch, dim, L, W, state, dtype):
     g = ops.causal_conv1d_bwd(**v)
     for k in g:
         assert_close(k, g[k], *want[k])
+
+
+@pytest.mark.parametrize("L", [32768, 32763])
+def test_offsets_beyond_32_bits(L):
+    """More than 2^31 elements per tensor: the last channels."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(60)
+    x, dout = (torch.randn(2, 35001, L, generator=g, device=DEV, dtype=BF) for _ in range(2))
+    assert x.numel() > 2 ** 31
+    w, b = torch.randn(35001, 4, generator=g, device=DEV), torch.randn(35001, generator=g, device=DEV)
+    got = ops.causal_conv1d_bwd(x, w, dout, bias=b)
+    want = ref.conv_bwd(x[:, -3:], w[-3:], dout[:, -3:], b[-3:], depth=8 * (L // 256 + 2) + 64)
+    assert_close("dx", got["dx"][:, -3:], *want["dx"])
+    assert_close("dweight", got["dweight"][-3:], *want["dweight"])
+    assert_close("dbias", got["dbias"][-3:], *want["dbias"])

@@ -565,3 +565,41 @@ def test_withheld_handoff_ends_the_whole_call(call, batch, dim, L, checkpoints):
     assert ops.device_status() == 0
     for k in good:
         assert torch.equal(good[k], again[k]), k
+
+
+@pytest.mark.parametrize("layout,batch,dim,L,ragged", [
+    ("bld", 25, 840, 577, True), ("bld", 13, 1024, 200, False), ("bld", 4, 67, 700, False), ("bld", 2, 64, 5000, True),
+    ("bld", 9, 300, 64, False), ("bdl", 3, 70, 1000, True), ("bdl", 5, 33, 2047, False), ("bdl", 2, 3, 5000, False),
+    ("bdl", 40, 65, 30, True)])
+def test_bias_gradient_holds_every_step_once(layout, batch, dim, L, ragged):
+    """In fp32 dgate_bias is the sum of the dgate that the call returns, to the roundings of a sum
+    in which no term passes more than L + batch + 64 of them."""
+    v, back = make(batch, dim, L, layout, F32, False, seed=L, ragged=ragged)
+    g = ops.gated_scan_bwd(**v, **back, layout=layout)
+    terms = g["dgate"].double().sum(1 if layout == "bld" else 2), g["dgate"].double().abs().sum(1 if layout == "bld" else 2)
+    off = (g["dgate_bias"].double() - terms[0].sum(0)).abs()
+    assert (off <= (L + batch + 64) * ref.U * terms[1].sum(0)).all()
+
+
+@pytest.mark.parametrize("layout,shape", [("bld", (70, 8192, 4096)), ("bld", (70, 8192, 4095)), ("bld", (1, 1 << 24, 136)),
+                                          ("bdl", (2, 35001, 32760))])
+def test_offsets_beyond_32_bits(layout, shape):
+    """More than 2^31 elements per tensor: the last channels of the last batch row."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(60)
+    gate, x, dout = (torch.randn(shape, generator=g, device=DEV, dtype=BF) for _ in range(3))
+    dim = shape[2] if layout == "bld" else shape[1]
+    assert gate.numel() > 2 ** 31
+    bias = torch.full((dim,), 1.0, device=DEV)
+    out, last = ops.gated_scan_fwd(gate, x, bias, layout=layout, return_last_state=True)
+    grads = ops.gated_scan_bwd(gate, x, dout, layout=layout)
+    # gates around 1 forget within some 30 steps: the last 1000 steps tell nothing of those before
+    tail = (lambda t: t[-1:, -1000:, -3:]) if layout == "bld" else (lambda t: t[-1:, -3:, -1000:])
+    late = (lambda t: t[:, 500:]) if layout == "bld" else (lambda t: t[..., 500:])
+    want = ref.gated(tail(gate), tail(x), bias[-3:], layout=layout)
+    assert_close("out", late(tail(out)), *(late(t) for t in want["out"]))
+    assert_close("last", last[-1:, -3:], *want["last_state"])
+    want = ref.gated(tail(gate), tail(x), layout=layout, dout=tail(dout))
+    for k in ("dgate", "dx"):
+        assert_close(k, late(tail(grads[k])), *(late(t) for t in want[k]))
+    assert ops.device_status() == 0

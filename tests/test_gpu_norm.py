@@ -254,3 +254,23 @@ def test_column_sums_hold_every_row_once(dtype, rows, dim):
                              weight=torch.ones(dim, device=DEV), bias=torch.zeros(dim, device=DEV))
     assert torch.equal(got["dweight"].long(), (dout * (s - mean[:, None])).sum(0))
     assert torch.equal(got["dbias"].long(), dout.sum(0))
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements per tensor: the last rows, and every row once in the sums."""
+    rows, dim = 1_100_000, 2048
+    g = torch.Generator(device=DEV)
+    g.manual_seed(60)
+    x, dout = (torch.randn(rows, dim, generator=g, device=DEV, dtype=BF) for _ in range(2))
+    res = torch.randn(rows, dim, generator=g, device=DEV, dtype=BF)
+    out, s, mean, rstd = ops.layer_norm_fwd(x, residual=res, return_stats=True)
+    want = ref.norm_fwd(x[-5:], residual=res[-5:])
+    assert_close("out", out[-5:], *want["out"])
+    assert_close("residual_out", s[-5:], *want["residual_out"])
+    grad = ops.layer_norm_bwd(dout, s, rstd, mean=mean, bias=torch.zeros(dim, device=DEV))
+    want = ref.norm_bwd(dout[-5:], s[-5:], rstd[-5:], mean[-5:])
+    assert_close("dx", grad["dx"][-5:], *want["dx"])
+    # bf16 whole numbers: exact sums
+    dout = torch.randint(0, 3, (rows, dim), generator=g, device=DEV, dtype=torch.int8).to(BF)
+    grad = ops.layer_norm_bwd(dout, s, rstd, mean=mean, bias=torch.zeros(dim, device=DEV))
+    assert torch.equal(grad["dbias"].double(), sum(part.double().sum(0) for part in dout.split(100_000)))
