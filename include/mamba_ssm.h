@@ -506,7 +506,9 @@ MAMBA_API mamba_status_t mamba_causal_conv1d_update(void *conv_state, const void
  *   initial_conv_state, dfinal_conv_state, dinitial_conv_state
  *                                     (batch, dim, width), io_dtype
  * bias, initial_conv_state and dfinal_conv_state may be NULL as in the forward;
- * dbias and dinitial_conv_state may be NULL (not computed).
+ * dbias and dinitial_conv_state may be NULL (not computed).  fp32 arithmetic; silu's
+ * sigmoid comes from the GPU's approximate exponential and reciprocal, off by at most 16
+ * 2^-24, for fp32 tensors too.
  * dims->workspace: at least mamba_causal_conv1d_bwd_workspace_bytes(dims, width)
  * bytes, 256-byte aligned, not shared by calls that overlap on the GPU.  The
  * sums are added in a fixed order: results repeat bit for bit.  seqlen up to
@@ -547,8 +549,11 @@ MAMBA_API mamba_status_t mamba_causal_conv1d_bwd(
  * dout are not used, whatever they hold (NaN included); out, dgate and dx are
  * written as 0 there; last_state is the state after the row's own last step.
  *
- * Arithmetic and states are fp32.  In the log-decay form a product of decays
- * over many steps must stay finite in fp32, which f_t <= 0 guarantees.
+ * Arithmetic and states are fp32.  Gates and decays come from the GPU's approximate
+ * exponential and reciprocal, for fp32 tensors too: each is off by at most (16 + 2 |f_t|)
+ * 2^-24 of its value, without a bias where the decay is near 1, and values below 2^-126
+ * count as 0.  In the log-decay form a product of decays over many steps must stay finite
+ * in fp32, which f_t <= 0 guarantees.
  * seqlen up to 2^31 - 65536, and in the (batch, dim, seqlen) layout batch dim below
  * 2^31 - 1 (MAMBA_ERR_UNSUPPORTED otherwise).
  */

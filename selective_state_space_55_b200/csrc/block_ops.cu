@@ -76,7 +76,7 @@ NormPlan plan_norm(int64_t rows, int64_t dim, int sms, bool backward) {
     const bool few = backward ? rows < 176 * (int64_t)sms / units : rows < 2 * (int64_t)sms;
     int64_t best = 0;
     for (int v = most; v >= 1; --v) {
-        if (v == 7) continue;                               // not built
+        if (v == 7) continue;                               // not built: 1537 to 1792 columns take 8
         const int64_t warps = (units + v - 1) / v;
         if (warps > (v <= kNormFewChunks ? kNormFewWarps : kNormCtaWarps)) continue;
         // few rows: the smallest number that fits
@@ -294,8 +294,11 @@ struct GatedLayout {           // offsets in the workspace, bytes
 // 128 164 / 131, 192 178 / 186, 256 180 / 238.  fp32, L 4096: forward 128 115 / 96, 192
 // 125 / 135; backward 192 264 / 266.
 constexpr int64_t kChainMinGroups = 192, kChainMinGroupsBf16Forward = 320;
-constexpr int64_t kRowResident = 20 * 148;       // warps along time that occupy a B200
-constexpr int64_t kChainResident = 2 * 148;      // CTAs that a B200 holds
+// What the plans take a B200 to hold (the workspace query must not depend on more than the
+// sizes): 20 warps per SM along time, and two CTAs of the chained kernels per SM, which is
+// the backward's and the fp32 forward's number (bf16 forward: three).
+constexpr int64_t kRowResident = 20 * 148;
+constexpr int64_t kChainResident = 2 * 148;
 
 // One segment per chain needs no look-back: no tickets, flags or maps.
 mamba_status_t gated_layout(const mamba_gated_dims_t* d, bool backward, bool recompute, int phase_max,

@@ -20,9 +20,12 @@
 // launch adds the partials in a fixed order.
 //
 // Measured, W = 4 with silu (copy rate 6529 GB/s): 16 x 5120 x 2048 bf16 266 us, 3.78
-// TB/s, 58 %: some 32 instructions per element, the packed FMA pipe first, with the
-// 16 warps that the ring and the registers leave; 8 x 5120 x 2048 fp32 252 us, 61 %.
-// Rows of odd length lose the aligned stores: 16 x 5120 x 1023 bf16 252 us, 31 %.
+// TB/s, 58 %; 8 x 5120 x 2048 fp32 252 us, 61 %.  Bound by latency: the ring and the
+// registers leave 16 warps per SM, four per scheduler, which use 56 % of the issue
+// slots (32 instructions per element) and wait for fixed latencies first.  Rows of odd
+// length: 16 x 5120 x 1023 bf16 254 us, 30 %; of a row's five tiles, because it starts
+// up to 7 steps past a boundary, the first and the last fetch their neighbours element
+// by element and mask their ends.
 #pragma once
 
 #include "conv1d.cuh"

@@ -18,10 +18,14 @@
 //
 // Measured, sigmoid gate (copy rate 6529 GB/s): bf16 8 x 2048 x 4096 (batch, seqlen,
 // dim) forward 94 us, 4.28 TB/s, 66 %, backward from checkpoints 168 us, 4.02 TB/s,
-// 62 %; 16 x 2048 x 5120 forward 190 us, 81 %; fp32 4 x 2048 x 4096 82 and 154 us,
-// 75 and 67 %.  Bound by issue (about 25 instructions per element forward, the
-// sigmoid's two special functions among them) and, with fewer groups than places
-// for CTAs, by the time a tile takes from its arrival to the next state.
+// 62 %; 16 x 2048 x 5120 forward 188 us, 82 %; fp32 4 x 2048 x 4096 82 and 154 us,
+// 75 and 67 %.  Neither memory nor the issue slots are full (8 x 1024 x 4096: DRAM 44 %
+// of its peak both ways, 58 % of the issue slots forward at 25 instructions per
+// element, 53 % backward at 45).  The warps stall on long-latency results first (2.5
+// cycles per instruction forward; the polls of a hand-off count there) and on fixed
+// latencies; all eight meet at a barrier in every tile, between its maps and its
+// results.  Rounds of CTAs count too: 8 x 2048 x 4096 gives 1536 stretches to 444
+// places for CTAs forward, 3.5 rounds; 16 x 2048 x 5120 gives 2.9, better filled.
 #pragma once
 
 #include "gated_scan.cuh"
@@ -501,8 +505,8 @@ __global__ void __launch_bounds__(kChainThreads, 2)
 // outputs, which replace x there and leave by TMA.  HBM sees each input once; the
 // steps' arithmetic is done twice.  Three CTAs per SM cover one another's loads
 // and joins, and each asks L2 for its next segment before it joins.  bf16, 1 x 131072
-// x 1536 (batch, seqlen, dim), log decay, last state: 324 us, 3.74 TB/s, 57 % (342 without
-// the request to L2); 1 x 4096 x 4096 45 us (a CTA per chain: 115).  Bound by the waits
+// x 1536 (batch, seqlen, dim), log decay, last state: 324 us, 3.73 TB/s, 57 % (342 without
+// the request to L2); 1 x 4096 x 4096 47 us (a CTA per chain: 115).  Bound by the waits
 // for earlier segments' maps; 32 steps per warp measured best.
 template <typename IoT>
 struct SegmentSizes {

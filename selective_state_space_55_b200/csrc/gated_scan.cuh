@@ -34,18 +34,20 @@
 // fp32x2.  Segments are handed out by a counter, the earliest steps of all chains
 // first, so that every segment's predecessors belong to CTAs that are running or
 // done; the wait is bounded all the same.  What TMA can move has kernels of its own
-// (gated_chain.cuh).  Measured, bf16: 1 x 131072 x 1536 backward 543 us, 57 % of the
-// copy rate; 8 x 2047 x 4095 forward 490 us, backward 1200 us, where rows start
-// anywhere and every element is a load of its own.
+// (gated_chain.cuh).  Measured, bf16: 1 x 131072 x 1536 backward 555 us, 56 % of the
+// copy rate (without checkpoints 792); 8 x 2047 x 4095 forward 500 us, 12 %, backward
+// 1217 us, 9 %, where rows start anywhere: every element is a load of its own, twice,
+// and a store of its own.
 //
 // Layout (batch, dim, seqlen): a lane takes 8 consecutive steps of two neighbouring
 // chains, the warp composes its lanes' maps by shuffles, and 1 to 8 warps share a
 // tile of a pair through shared memory.  Chains are plentiful here (one per channel
 // instead of one per 64), so a chain stays with its warps and nothing waits; the
-// warps walk pair after pair, the next tile on its way by cp.async.  Issue-bound
-// (the scan across lanes and the addresses of every tile, beside the steps'
-// arithmetic): 8 x 4096 x 2048 bf16 forward 98 us, 63 % of the copy rate, backward
-// 227 us, 45 %.
+// warps walk pair after pair, the next tile on its way by cp.async.  Bound by issue (75
+// and 67 % of the slots on 8 x 4096 x 1024: the scan across lanes and the addresses of
+// every tile, beside the steps' arithmetic): 8 x 4096 x 2048 bf16 forward 98 us, 63 % of
+// the copy rate, backward 229 us, 45 %.  A backward row that needs a second tile pays a
+// sweep for it: 2047 steps, whose rows start up to 7 past a boundary, take 381 us.
 #pragma once
 
 #include "row_vectors.cuh"

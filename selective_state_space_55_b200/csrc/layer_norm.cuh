@@ -26,8 +26,11 @@
 //
 // Measured, bf16 with a residual (copy rate 6529 GB/s): 32768 x 2560 forward 119 us,
 // 5.65 TB/s, 87 %; backward 127 us, 5.29 TB/s, 81 %, the rest being the barriers of
-// the two row reductions; 8 x 2560 forward 8 us, latency.  Columns that are not a
-// multiple of 8 move element by element: 32768 x 2559 203 and 276 us.
+// the two row reductions; 8 x 2560 forward 8 us, latency.  fp32: 248 and 236 us, 83 and
+// 87 %.  Columns that are not a multiple of 8 move element by element: 32768 x 2559 203
+// and 276 us, 51 and 37 %.  4096 x 16384: forward, 8 chunks per lane on 8 warps, 166 us,
+// 50 %; backward, beyond the registers, where s and dout are read three times, 332 us,
+// 25 %.
 #pragma once
 
 #include "row_vectors.cuh"
