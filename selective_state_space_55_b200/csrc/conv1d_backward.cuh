@@ -82,11 +82,12 @@ struct ConvRow {
         dx = static_cast<IoT*>(p.dx) + at;
         init = p.init != nullptr ? static_cast<const IoT*>(p.init) + chain * kW : nullptr;
         dfinal = p.dfinal != nullptr ? static_cast<const IoT*>(p.dfinal) + chain * kW : nullptr;
-        // whole stretches: the last one may end far behind the row, past 32 bits
-        const int64_t steps = p.stretch_tiles * kWarpSteps, end = (stretch + 1) * steps - row_phase(x);
-        begin = (int)(end - steps);
+        // counted in tiles, because the last stretch may end far behind the row, past 32 bits of steps
+        const int phase = row_phase(x), L = (int)p.seqlen, tiles = (L + phase + kWarpSteps - 1) / kWarpSteps;
+        const int first = (int)stretch * (int)p.stretch_tiles, end = first + (int)p.stretch_tiles;
+        begin = first * kWarpSteps - phase;
         lo = begin > 0 ? begin : 0;
-        hi = live ? (int)(end < p.seqlen ? end : p.seqlen) : lo;
+        hi = live ? (end < tiles ? end * kWarpSteps - phase : L) : lo;
     }
 
     // x_s at any time: the row, the initial state before it, 0 elsewhere

@@ -19,9 +19,9 @@
 // Measured, sigmoid gate (copy rate 6529 GB/s): bf16 8 x 2048 x 4096 (batch, seqlen,
 // dim) forward 94 us, 4.28 TB/s, 66 %, backward from checkpoints 168 us, 4.02 TB/s,
 // 62 %; 16 x 2048 x 5120 forward 188 us, 82 %; fp32 4 x 2048 x 4096 82 and 154 us,
-// 75 and 67 %.  Neither memory nor the issue slots are full (8 x 1024 x 4096: DRAM 44 %
-// of its peak both ways, 58 % of the issue slots forward at 25 instructions per
-// element, 53 % backward at 45).  The warps stall on long-latency results first (2.5
+// 75 and 67 %.  Neither memory nor the issue slots are full (8 x 1024 x 4096: DRAM 42
+// and 43 % of its peak, 58 % of the issue slots forward at 25 instructions per
+// element, 53 % backward at 45).  The warps stall on long-latency results first (2.7
 // cycles per instruction forward; the polls of a hand-off count there) and on fixed
 // latencies; all eight meet at a barrier in every tile, between its maps and its
 // results.  Rounds of CTAs count too: 8 x 2048 x 4096 gives 1536 stretches to 444

@@ -44,7 +44,7 @@
 // tile of a pair through shared memory.  Chains are plentiful here (one per channel
 // instead of one per 64), so a chain stays with its warps and nothing waits; the
 // warps walk pair after pair, the next tile on its way by cp.async.  Bound by issue (75
-// and 67 % of the slots on 8 x 4096 x 1024: the scan across lanes and the addresses of
+// and 65 % of the slots on 8 x 4096 x 1024: the scan across lanes and the addresses of
 // every tile, beside the steps' arithmetic): 8 x 4096 x 2048 bf16 forward 98 us, 63 % of
 // the copy rate, backward 229 us, 45 %.  A backward row that needs a second tile pays a
 // sweep for it: 2047 steps, whose rows start up to 7 past a boundary, take 381 us.
